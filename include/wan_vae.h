@@ -63,8 +63,9 @@ typedef enum {
   WAN_ERR_NOT_IMPLEMENTED = 10
 } wan_status;
 
-/* Element types.  WAN_F32: IEEE fp32.  WAN_BF16: bfloat16 (top half of an fp32). */
-typedef enum { WAN_F32 = 0, WAN_BF16 = 1 } wan_dtype;
+/* Element types.  WAN_F32: IEEE fp32.  WAN_BF16: bfloat16 (top half of an
+ * fp32).  WAN_F16: IEEE half precision, taken by the token operators only. */
+typedef enum { WAN_F32 = 0, WAN_BF16 = 1, WAN_F16 = 2 } wan_dtype;
 
 /* One parameter of the weight table, under diffusers' names ("decoder.*",
  * "post_quant_conv.*"; other names are ignored, as the page's decode keeps
@@ -374,6 +375,125 @@ wan_status wan_causal_conv3d_noalloc(const void* x, int32_t B, int32_t n_hist, i
                                      int32_t Cin, const void* weight, const void* bias, int32_t w_dtype,
                                      int32_t Cout, int32_t kt, int32_t kh, int32_t kw, void* out,
                                      wan_cuda_stream stream);
+
+/* ---- token operators ----
+ * The latents of a clip come from a streaming video model: it turns queries
+ * and keys by each token's place in the clip, appends the keys and values of
+ * every new latent frame (or token) to a cache, and attends over the cache.
+ * These calls are those steps.  They are stream-ordered, allocate nothing and
+ * do not wait for the device.  Strides count elements; the channels of a head
+ * are contiguous. */
+
+/* Rotation of a head's channels: pair j of `pairs` is turned by position[axis[j]]
+ * * freq[j] radians.  interleaved: pair j is channels (2j, 2j + 1); otherwise
+ * channels (j, j + pairs).  Channels past 2 * pairs pass through.  freq and
+ * axis are HOST arrays of `pairs` values, read during the call.  Angles are
+ * formed modulo one turn in 64-bit integers, so positions may be negative or
+ * far: the angle is off by the rounding of freq to 2^-52 times the position. */
+typedef struct {
+  int32_t pairs;        /* 1 .. 128 */
+  int32_t axes;         /* coordinates per position, 1 .. 4 */
+  int32_t interleaved;  /* 0 or 1 */
+  const double* freq;   /* finite */
+  const int32_t* axis;  /* 0 .. axes - 1 */
+} wan_rotation;
+
+/* out[b, t, h, :] = x[b, t, h, :] turned at positions[b, t, :] (inverse != 0: by
+ * the opposite angles, which is the gradient with respect to x of that
+ * rotation applied to the gradient of its output).  x, out: device, `dtype`
+ * (WAN_F32, WAN_BF16, WAN_F16), B x T x heads x head_dim with batch, token and
+ * head strides; computed in fp32 and rounded once.  out may be x itself (same
+ * strides); any other overlap is undefined.  positions: device, int32 or
+ * int64 (positions_64), axes values per token, tokens contiguous, batches
+ * positions_batch values apart (0: shared).  head_dim: even, 2 * pairs .. 256.
+ * Errors: WAN_ERR_INVALID_ARG, WAN_ERR_DTYPE, WAN_ERR_UNSUPPORTED (head_dim
+ * above 256, more than 2^31 - 1 tokens), WAN_ERR_CUDA. */
+wan_status wan_rotary(const void* x, const int64_t x_strides[3], void* out, const int64_t out_strides[3],
+                      int32_t dtype, int32_t B, int32_t T, int32_t heads, int32_t head_dim, const void* positions,
+                      int32_t positions_64, int64_t positions_batch, const wan_rotation* rotation, int32_t inverse,
+                      wan_cuda_stream stream);
+
+/* A paged key-value cache in the caller's memory: channel c of row r (0 ..
+ * page_size - 1) of head h of page p of the keys is k[p * k_page + h * k_head
+ * + r * k_row + c], and likewise the values.  k and v 16-byte aligned, strides
+ * multiples of 8 elements, head_dim a multiple of 8 up to 256. */
+typedef struct {
+  void* k;
+  void* v;
+  int32_t dtype; /* WAN_BF16 or WAN_F16 */
+  int32_t heads, page_size, head_dim;
+  int64_t pages;
+  int64_t k_page, k_head, k_row, v_page, v_head, v_row;
+} wan_kv_cache;
+
+/* The sequences of one call (device arrays).  Sequence b holds lengths[b] keys,
+ * the new tokens of this call among them; its key i is row i % page_size of
+ * page pages[b * page_stride + i / page_size].  Its new tokens are rows
+ * cu_tokens[b] .. cu_tokens[b + 1] - 1 of the call's token tensors (cu_tokens
+ * NULL: one each, row b) and its last keys.  Rows behind the last sequence are
+ * not touched.  Several sequences may share pages that they only read.
+ * status: an int32 in device memory, or NULL.  A page number outside the
+ * cache, a length that the table cannot hold, or token ranges that are no
+ * ranges of the `tokens` rows, are left out by the kernels (no access, a key
+ * that nobody sees, no tokens) and leave a code there if it was 0. */
+typedef struct {
+  const int32_t* pages;
+  int64_t page_stride;
+  int32_t max_pages; /* page numbers per sequence in the table */
+  int32_t batch;
+  const int32_t* lengths;
+  const int32_t* cu_tokens;
+  int32_t tokens;
+  int32_t* status;
+} wan_kv_batch;
+
+/* Checks a batch held in HOST arrays (pages, lengths, cu_tokens; status is
+ * not used) against a cache's page_size and pages, with the kernels' own index
+ * arithmetic: WAN_OK, or WAN_ERR_INVALID_ARG and what is wrong with which
+ * sequence.  append != 0 also refuses sequences with more new tokens than
+ * keys, and two new tokens of the call in one row of the cache.  Host only. */
+wan_status wan_kv_check(const wan_kv_batch* batch, int32_t page_size, int64_t pages, int32_t append);
+
+/* Waits for `stream`, then reports what a batch's status word holds
+ * (WAN_ERR_INTERNAL with a message; the word is cleared), or WAN_OK. */
+wan_status wan_kv_status(int32_t* status, wan_cuda_stream stream);
+
+/* Appends the call's tokens to the cache: k turned (rotation NULL: as it is)
+ * and v as it is, into the row of each token's place; with q (optional), q
+ * turned into q_out (which may be q).  k, v: [tokens][heads][head_dim], q,
+ * q_out: [tokens][q_heads][head_dim], of the cache's dtype, with token and head
+ * strides.  positions: [tokens][axes], contiguous.  Each new token needs a row
+ * of its own: where the tables give two tokens one row, it holds a mixture.
+ * Errors: WAN_ERR_INVALID_ARG, WAN_ERR_DTYPE, WAN_ERR_UNSUPPORTED, WAN_ERR_CUDA. */
+wan_status wan_kv_append(const wan_kv_cache* cache, const wan_kv_batch* batch, const void* k, int64_t k_token,
+                         int64_t k_head, const void* v, int64_t v_token, int64_t v_head, const void* q,
+                         int32_t q_heads, int64_t q_token, int64_t q_head, void* q_out, int64_t q_out_token,
+                         int64_t q_out_head, const wan_rotation* rotation, const void* positions,
+                         int32_t positions_64, wan_cuda_stream stream);
+
+/* Attention of the call's tokens over the cache: for each token and query head,
+ * out = softmax(scale * q . k) v over the keys that the token sees, query heads
+ * h * g .. h * g + g - 1 reading key head h (g = q_heads / heads).  ranges: NULL
+ * (every key of the sequence) or [tokens][2] device int32, the first key a
+ * token sees and one past its last, cut to the sequence; this holds causal,
+ * frame-causal, prefix, sliding and document masks.  A token that sees
+ * nothing gets zeros.  What masked keys and values, or the rows past a
+ * sequence's length, hold does not matter (infinities and NaNs included).
+ * q, out: [tokens][q_heads][head_dim] of the cache's dtype with token and head
+ * strides; lse (optional): fp32 [tokens][q_heads] contiguous, the natural
+ * logarithm of the sum of exp(scale * q . k) (-inf for a token that sees
+ * nothing).  Scores, sums and outputs are held in fp32; weights enter the
+ * product with v as 16-bit values.  workspace: device memory of at least
+ * wan_kv_attention_workspace bytes, 16-byte aligned, not used by any other
+ * work until this call's is done (its contents need not be kept).
+ * Errors: WAN_ERR_INVALID_ARG, WAN_ERR_DTYPE, WAN_ERR_UNSUPPORTED, WAN_ERR_CUDA. */
+wan_status wan_kv_attention(const wan_kv_cache* cache, const wan_kv_batch* batch, const void* q, int32_t q_heads,
+                            int64_t q_token, int64_t q_head, const int32_t* ranges, float scale, void* out,
+                            int64_t out_token, int64_t out_head, float* lse, void* workspace,
+                            int64_t workspace_bytes, wan_cuda_stream stream);
+/* Bytes of workspace that wan_kv_attention needs for these sizes on the
+ * current device (-1 and an error message if it would refuse them). */
+int64_t wan_kv_attention_workspace(const wan_kv_cache* cache, const wan_kv_batch* batch, int32_t q_heads);
 
 #ifdef __cplusplus
 }

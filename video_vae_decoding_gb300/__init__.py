@@ -15,7 +15,9 @@ Typical use::
     tiled = model.decode_tiled(z, tile=(256, 256), stride=(192, 192))
     model.set_latent_stats(mean, std)               # de-normalise latents first
 
-``decode(z, weights, dtype)`` is the one-shot form.
+``decode(z, weights, dtype)`` is the one-shot form.  ``tokens.py`` holds the
+operators of the streaming model in front of the decode: rotary positions, the
+append to a paged key-value cache, and attention over it.
 """
 
 from __future__ import annotations
@@ -25,8 +27,10 @@ import ctypes
 import torch
 
 from ._lib import PROFILE_KINDS, WAN_BF16, WAN_F32, WanError, WanProfile, WanTensor, check, load  # noqa: F401
+from .tokens import Rotation, kv_append, kv_attention, kv_check, kv_status, rotary, rotary_grad
 
-__all__ = ["Model", "DecodeStream", "decode", "attention_block", "causal_conv3d", "out_frames", "WanError"]
+__all__ = ["Model", "DecodeStream", "decode", "attention_block", "causal_conv3d", "out_frames", "WanError",
+           "Rotation", "rotary", "rotary_grad", "kv_append", "kv_attention", "kv_check", "kv_status"]
 
 
 def _code(dtype: torch.dtype) -> int:

@@ -8,7 +8,7 @@ import os
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libwanvae.so")
 
-WAN_F32, WAN_BF16 = 0, 1
+WAN_F32, WAN_BF16, WAN_F16 = 0, 1, 2
 
 STATUS = {
     0: "WAN_OK", 1: "WAN_ERR_INVALID_ARG", 2: "WAN_ERR_DTYPE", 3: "WAN_ERR_MISSING_WEIGHT", 4: "WAN_ERR_SHAPE",
@@ -38,6 +38,47 @@ class WanProfile(ctypes.Structure):
         ("kind_launches", ctypes.c_int64 * 7),
         ("tc_exec_flops", ctypes.c_double),
         ("kind_exec", ctypes.c_double * 7),
+    ]
+
+
+class WanRotation(ctypes.Structure):
+    _fields_ = [
+        ("pairs", ctypes.c_int32),
+        ("axes", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("freq", ctypes.POINTER(ctypes.c_double)),
+        ("axis", ctypes.POINTER(ctypes.c_int32)),
+    ]
+
+
+class WanKvCache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("pages", ctypes.c_int64),
+        ("k_page", ctypes.c_int64),
+        ("k_head", ctypes.c_int64),
+        ("k_row", ctypes.c_int64),
+        ("v_page", ctypes.c_int64),
+        ("v_head", ctypes.c_int64),
+        ("v_row", ctypes.c_int64),
+    ]
+
+
+class WanKvBatch(ctypes.Structure):
+    _fields_ = [
+        ("pages", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64),
+        ("max_pages", ctypes.c_int32),
+        ("batch", ctypes.c_int32),
+        ("lengths", ctypes.c_void_p),
+        ("cu_tokens", ctypes.c_void_p),
+        ("tokens", ctypes.c_int32),
+        ("status", ctypes.c_void_p),
     ]
 
 
@@ -87,6 +128,15 @@ SIGNATURES = {
     "wan_selftest_attention_timeout": (_i32, [_i32, ctypes.POINTER(_i32), _vp]),
     "wan_causal_conv3d_noalloc": (_i32, [_vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _i32, _i32, _i32, _i32,
                                          _i32, _vp, _vp]),
+    "wan_rotary": (_i32, [_vp, ctypes.POINTER(_i64 * 3), _vp, ctypes.POINTER(_i64 * 3), _i32, _i32, _i32, _i32, _i32,
+                          _vp, _i32, _i64, ctypes.POINTER(WanRotation), _i32, _vp]),
+    "wan_kv_check": (_i32, [ctypes.POINTER(WanKvBatch), _i32, _i64, _i32]),
+    "wan_kv_status": (_i32, [_vp, _vp]),
+    "wan_kv_append": (_i32, [ctypes.POINTER(WanKvCache), ctypes.POINTER(WanKvBatch), _vp, _i64, _i64, _vp, _i64, _i64,
+                             _vp, _i32, _i64, _i64, _vp, _i64, _i64, ctypes.POINTER(WanRotation), _vp, _i32, _vp]),
+    "wan_kv_attention": (_i32, [ctypes.POINTER(WanKvCache), ctypes.POINTER(WanKvBatch), _vp, _i32, _i64, _i64, _vp,
+                                ctypes.c_float, _vp, _i64, _i64, _vp, _vp, _i64, _vp]),
+    "wan_kv_attention_workspace": (_i64, [ctypes.POINTER(WanKvCache), ctypes.POINTER(WanKvBatch), _i32]),
 }
 
 _lib = None

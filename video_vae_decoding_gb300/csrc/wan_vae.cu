@@ -23,6 +23,7 @@
 #include <string>
 #include <vector>
 
+#include "host.h"
 #include "kernels.h"
 #include "wan_vae.h"
 
@@ -32,7 +33,7 @@ namespace wan {
 
 thread_local std::string g_last_error;
 
-static wan_status fail(wan_status s, const char* fmt, ...) {
+wan_status fail(wan_status s, const char* fmt, ...) {
   char buf[1024];
   va_list ap;
   va_start(ap, fmt);
@@ -42,26 +43,13 @@ static wan_status fail(wan_status s, const char* fmt, ...) {
   return s;
 }
 
-#define CUDA_TRY(expr)                                                                                     \
-  do {                                                                                                     \
-    cudaError_t e_ = (expr);                                                                               \
-    if (e_ != cudaSuccess)                                                                                 \
-      return ::wan::fail(e_ == cudaErrorMemoryAllocation ? WAN_ERR_OOM : WAN_ERR_CUDA, "%s: %s (%s:%d)", #expr, \
-                         cudaGetErrorString(e_), __FILE__, __LINE__);                                      \
-  } while (0)
-#define WAN_TRY(expr)                 \
-  do {                                \
-    wan_status s_ = (expr);           \
-    if (s_ != WAN_OK) return s_;      \
-  } while (0)
-
 static inline long long rup(long long a, long long b) { return (a + b - 1) / b * b; }
 static inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 
 // ------------------------------------------------------------- tensor maps
 static PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-static wan_status init_encode() {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
   std::call_once(once, [] {
@@ -70,13 +58,13 @@ static wan_status init_encode() {
     err = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
     if (err == cudaSuccess && q == cudaDriverEntryPointSuccess) g_encode = (PFN_cuTensorMapEncodeTiled_v12000)fn;
   });
-  if (!g_encode) return fail(WAN_ERR_CUDA, "cuTensorMapEncodeTiled unavailable (%s)", cudaGetErrorString(err));
-  return WAN_OK;
+  if (!g_encode) fail(WAN_ERR_CUDA, "cuTensorMapEncodeTiled unavailable (%s)", cudaGetErrorString(err));
+  return g_encode;
 }
 
 static wan_status encode(CUtensorMap* m, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
                          const uint32_t* box) {
-  WAN_TRY(init_encode());
+  if (!tensor_map_encoder()) return WAN_ERR_CUDA;
   const uint32_t es[5] = {1, 1, 1, 1, 1};
   const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims,
                               strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -1562,15 +1550,6 @@ static wan_status tiled_impl(const wan_vae_model* m, const void* z, int z_dtype,
 }
 
 // ------------------------------------------------------------- C ABI
-#define API_GUARD(...)                                               \
-  try {                                                              \
-    __VA_ARGS__                                                      \
-  } catch (const std::bad_alloc&) {                                  \
-    return fail(WAN_ERR_OOM, "host allocation failed");              \
-  } catch (...) {                                                    \
-    return fail(WAN_ERR_INTERNAL, "unexpected C++ exception");       \
-  }
-
 extern "C" {
 
 int64_t wan_vae_out_frames(int64_t T) { return T >= 1 ? 4 * T - 3 : 0; }
