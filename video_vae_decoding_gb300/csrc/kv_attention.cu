@@ -21,11 +21,7 @@
 //    the order of the keys: the result does not depend on timing.
 // Sums, maxima and outputs are held in 32 bits; how the weights are rounded is
 // told at Weights.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "ptx.cuh"
-#include "token_ops.h"
+#include "kv_common.cuh"
 
 namespace wan {
 
@@ -119,60 +115,18 @@ struct Weights<__half> {
   }
   static __device__ __forceinline__ uint32_t lo(float, float) { return 0; }
 };
-template <typename T>
-__device__ __forceinline__ float val(T v);
-template <>
-__device__ __forceinline__ float val<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <>
-__device__ __forceinline__ float val<__half>(__half v) { return __half2float(v); }
-template <typename T>
-__device__ __forceinline__ T round_to(float v);
-template <>
-__device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half round_to<__half>(float v) { return __float2half_rn(v); }
-// bit masks of the exponent of a 16-bit value: all ones marks an infinity or a NaN
-template <typename T>
-struct Expo;
-template <>
-struct Expo<__nv_bfloat16> { static constexpr uint32_t m = 0x7F80u; };
-template <>
-struct Expo<__half> { static constexpr uint32_t m = 0x7C00u; };
-template <typename T>
-__device__ __forceinline__ bool odd16(uint32_t v) { return (v & Expo<T>::m) == Expo<T>::m; }
-template <typename T>
-__device__ __forceinline__ bool odd32(uint32_t v) { return odd16<T>(v) || odd16<T>(v >> 16); }
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// 2^(x - m); where m = -inf nothing but hidden keys (x = -inf) or a NaN was
-// seen: 0, or the NaN
-__device__ __forceinline__ float weight(float x, float m) { return m == -INFINITY ? (x == x ? 0.f : x) : ex2(x - m); }
-
 // ------------------------------------------------------------ the line of tiles
-struct Seq {
-  int r0, n, len, row_tiles, key_tiles;
-  long long tiles;
+// Tiles of a sequence on the line: row tiles x heads x key tiles.
+struct Tiles {
+  int key_tiles;
+  long long all;
 };
-__device__ __forceinline__ Seq sequence(const AttnArgs& a, int b, bool tell) {
-  Seq s;
-  const bool ok = kv_rows(a.b.cu, a.b.T, b, &s.r0, &s.n);
-  const bool okl = kv_length(a.b.lengths[b], a.b.max_pages, a.c.page_size, &s.len);
-  if (tell && !(ok && okl) && a.b.status) atomicCAS(a.b.status, 0, (int)kDevBadLength);
-  s.row_tiles = (int)(((long long)s.n * a.group + kRows - 1) / kRows);
-  s.key_tiles = (s.len + kKeys - 1) / kKeys;
-  s.tiles = (long long)s.row_tiles * a.c.heads * s.key_tiles;
-  return s;
+__device__ __forceinline__ Tiles tiles_of(const AttnArgs& a, const Seq& s) {
+  Tiles t;
+  t.key_tiles = (s.len + kKeys - 1) / kKeys;
+  t.all = ((long long)s.n * a.group + kRows - 1) / kRows * a.c.heads * t.key_tiles;
+  return t;
 }
-
-// What a block leaves for the join: a row tile whose first part it holds.
-struct Open {
-  int b, rt, h;
-  int parts;  // blocks after this one that hold the rest (0: nothing to join)
-};
 
 struct Space {  // the workspace: per block an Open and two parts (0: a row tile's later keys, 1: its first ones)
   Open* open;
@@ -191,18 +145,6 @@ long long space_bytes(int DP, int G) {
   return (long long)G * (sizeof(Open) + 2 * kRows * (sizeof(float2) + (size_t)DP * sizeof(float)));
 }
 
-template <typename T>
-__device__ __forceinline__ void put_row(const AttnArgs& a, const Seq& s, int h, int r, int c, float v) {
-  const int t = r / a.group, g = r - t * a.group;
-  ((T*)a.out)[(long long)(s.r0 + t) * a.o_t + (long long)(h * a.group + g) * a.o_h + c] = round_to<T>(v);
-}
-__device__ __forceinline__ void put_lse(const AttnArgs& a, const Seq& s, int h, int r, float m, float l) {
-  if (!a.lse) return;
-  const int t = r / a.group, g = r - t * a.group;
-  a.lse[(long long)(s.r0 + t) * a.q_heads + h * a.group + g] =
-      l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-}
-
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
     kv_split_kernel(const __grid_constant__ AttnArgs a) {
@@ -210,9 +152,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
   constexpr int CH = C::CH, ST = C::kStages, NK = DP / 16;
   constexpr bool kQRegs = DP <= 128;  // q fragments in registers; at 256 channels they are fetched again
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_scan[kWarps];
-  __shared__ int s_b;
-  __shared__ long long s_at;
   __shared__ uint32_t s_seen[kWarps][ST];
   __shared__ float2 s_ml[kWarps][kRows];
   __shared__ float s_p[kWarps][kRows][kWarpKeys];
@@ -227,68 +166,28 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
   // the join's blocks may start as soon as every block of this grid runs
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // sequences without a key: their rows see nothing
-  for (int b = me; b < a.b.B; b += G) {
-    const Seq s = sequence(a, b, true);
-    if (s.len > 0) continue;
-    for (int i = threadIdx.x; i < s.n * a.q_heads; i += kThreads) {
-      const int t = i / a.q_heads, h = i - t * a.q_heads;
-      for (int c = 0; c < a.c.D; ++c)
-        ((T*)a.out)[(long long)(s.r0 + t) * a.o_t + (long long)h * a.o_h + c] = round_to<T>(0.f);
-      if (a.lse) a.lse[(long long)(s.r0 + t) * a.q_heads + h] = -INFINITY;
-    }
-  }
+  put_empty<T>(a, me, G);
 
   // --------------------------------------------- this block's piece of the line
-  const int chunk = (a.b.B + kThreads - 1) / kThreads;
-  const int b_lo = min(a.b.B, (int)threadIdx.x * chunk), b_hi = min(a.b.B, b_lo + chunk);
-  long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += sequence(a, b, false).tiles;
-  long long incl = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += o;
-  }
-  if (lane == 31) s_scan[warp] = incl;
-  __syncthreads();
-  long long before = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s_scan[w];
-    total += s_scan[w];
-  }
-  const long long live = total < G ? total : G;  // blocks with a piece: one tile or more each
+  const Piece pc =
+      cut_line<kWarps>(a.b.B, me, G, [&](int b) { return tiles_of(a, sequence(a, b, false)).all; });
   if (threadIdx.x == 0) ws.open[me] = Open{0, 0, 0, 0};
-  if (me >= live) return;
-  const long long beg = total * me / live, end = total * (me + 1) / live;
-  if (beg >= before && beg < before + mine) {
-    long long at = beg - before;
-    int b = b_lo;
-    for (; b < b_hi; ++b) {
-      const long long n = sequence(a, b, false).tiles;
-      if (at < n) break;
-      at -= n;
-    }
-    s_b = b;
-    s_at = at;
-  }
-  __syncthreads();
-
-  int b = s_b;
-  long long at = s_at;
+  int b = pc.b;
+  long long at = pc.at;
   const T* kbase = (const T*)a.c.k;
   const T* vbase = (const T*)a.c.v;
 
-  for (long long line = beg; line < end;) {
+  for (long long line = pc.beg; line < pc.end;) {
     Seq s = sequence(a, b, false);
-    while (at >= s.tiles) {  // the next sequence with a tile
-      at -= s.tiles;
+    Tiles tl = tiles_of(a, s);
+    while (at >= tl.all) {  // the next sequence with a tile
+      at -= tl.all;
       s = sequence(a, ++b, false);
+      tl = tiles_of(a, s);
     }
     // the run: key tiles [kt0, kt1) of one row tile and head
-    const int seg = (int)(at / s.key_tiles), kt0 = (int)(at - (long long)seg * s.key_tiles);
-    const int kt1 = (int)min((long long)s.key_tiles, kt0 + (end - line));
+    const int seg = (int)(at / tl.key_tiles), kt0 = (int)(at - (long long)seg * tl.key_tiles);
+    const int kt1 = (int)min((long long)tl.key_tiles, kt0 + (pc.end - line));
     // heads of a row tile side by side, row tiles behind them
     const int rt = seg / a.c.heads, h = seg - rt * a.c.heads;
     const int row0 = rt * kRows, cnt = min(kRows, s.n * a.group - row0);
@@ -317,13 +216,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
     int lo_a = 0, hi_a = 0, lo_b = 0, hi_b = 0;
     int lo = 0x7fffffff, hi = 0;
     for (int r = 0; r < cnt; ++r) {
-      int f = 0, e = s.len;
-      if (a.ranges) {
-        const int t = s.r0 + (row0 + r) / a.group;
-        f = max(0, a.ranges[2 * t]);
-        e = min(s.len, a.ranges[2 * t + 1]);
-        if (f >= e) f = e = 0;
-      }
+      int f, e;
+      seen_range(a, s.r0 + (row0 + r) / a.group, s.len, &f, &e);
       if (r == r_a) lo_a = f, hi_a = e;
       if (r == r_b) lo_b = f, hi_b = e;
       if (f < e) {
@@ -556,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
       if (r_b < cnt) *reinterpret_cast<float2*>(so + r_b * DP + c) = make_float2(o[i][2], o[i][3]);
     }
     __syncthreads();
-    const bool whole = kt0 == 0 && kt1 == s.key_tiles;
+    const bool whole = kt0 == 0 && kt1 == tl.key_tiles;
     const int slot = 2 * me + (kt0 == 0 ? 1 : 0);
     for (int i = threadIdx.x; i < cnt * DP; i += kThreads) {
       const int r = i / DP, c = i - r * DP;
@@ -570,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
         v += f * reinterpret_cast<const float*>(smem + w * C::kRing)[r * DP + c];
       }
       if (whole) {
-        if (c < a.c.D) put_row<T>(a, s, h, row0 + r, c, l == 0.f ? 0.f : v / l);
+        if (c < a.c.D) out_row<T>(a, s, h, row0 + r)[c] = round_to<T>(l == 0.f ? 0.f : v / l);
         if (c == 0) put_lse(a, s, h, row0 + r, m, l);
       } else {
         ws.o[((long long)slot * kRows + r) * DP + c] = v;
@@ -578,8 +472,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
       }
     }
     if (!whole && kt0 == 0 && threadIdx.x == 0) {
-      const long long last = line + s.key_tiles - 1;  // the row tile's last tile: its block is the last part's
-      ws.open[me] = Open{b, rt, h, (int)(((last + 1) * live - 1) / total) - me};
+      const long long last = line + tl.key_tiles - 1;  // the row tile's last tile: its block is the last part's
+      ws.open[me] = Open{b, rt, h, pc.holder(last) - me};
     }
     __syncthreads();
     at += kt1 - kt0;
@@ -611,7 +505,7 @@ __global__ void __launch_bounds__(DP) kv_join_kernel(const __grid_constant__ Att
       v = v * f + x * g;
       m = n;
     }
-    if (c < a.c.D) put_row<T>(a, s, op.h, row0 + r, c, l == 0.f ? 0.f : v / l);
+    if (c < a.c.D) out_row<T>(a, s, op.h, row0 + r)[c] = round_to<T>(l == 0.f ? 0.f : v / l);
     if (c == 0) put_lse(a, s, op.h, row0 + r, m, l);
   }
 }

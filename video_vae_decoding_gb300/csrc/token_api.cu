@@ -1,10 +1,12 @@
 // C ABI of the token operators (include/wan_vae.h): argument checks and
 // launches.
+#include <algorithm>
 #include <cmath>
 #include <set>
 #include <utility>
 
 #include "host.h"
+#include "kv_chunk.h"
 #include "ptx.cuh"
 #include "token_ops.h"
 
@@ -89,6 +91,51 @@ wan_status sm_count(int* n) {
   CUDA_TRY(cudaGetDevice(&dev));
   CUDA_TRY(cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev));
   return WAN_OK;
+}
+
+// Rows of a sequence (tokens x query heads of a key head), on average, from
+// which the tensor-core kernel takes over from the split kernel.
+constexpr int kChunkRows = 64;
+
+bool chunk_rows(const AttnArgs& a, ChunkGeo* g) {
+  return (int64_t)a.b.T * a.group >= (int64_t)kChunkRows * a.b.B && kv_chunk_geometry(a, g);
+}
+
+// Tensor map over a cache: channels, then rows, heads and pages in the order of
+// their strides.  False if the strides cannot be described.
+bool cache_map(const KvCache& c, const void* base, long long page, long long head, long long row, ChunkGeo* g,
+               CUtensorMap* m) {
+  struct Dim {
+    uint64_t n;
+    long long stride;
+    int* place;
+    uint32_t box;
+  };
+  Dim d[3] = {{(uint64_t)c.page_size, row, &g->dim_row, (uint32_t)g->box_rows},
+              {(uint64_t)c.heads, head, &g->dim_head, 1},
+              {(uint64_t)c.pages, page, &g->dim_page, 1}};
+  // a dimension of one is never stepped along: it goes last, with any stride that fits
+  std::stable_sort(d, d + 3, [](const Dim& x, const Dim& y) {
+    return (x.n > 1) != (y.n > 1) ? x.n > 1 : x.n > 1 && x.stride < y.stride;
+  });
+  uint64_t dims[4] = {(uint64_t)c.D}, strides[3];
+  uint32_t box[4] = {64};
+  const uint32_t step[4] = {1, 1, 1, 1};
+  uint64_t last = (uint64_t)c.D * 2;
+  for (int i = 0; i < 3; ++i) {
+    if (d[i].n > 1 && d[i].stride <= 0) return false;
+    *d[i].place = i;
+    dims[i + 1] = d[i].n;
+    strides[i] = d[i].n > 1 ? (uint64_t)d[i].stride * 2 : last;
+    last = strides[i] * d[i].n;
+    box[i + 1] = d[i].box;
+    if (strides[i] >= 1ull << 40) return false;
+  }
+  const auto encode = tensor_map_encoder();
+  return encode && encode(m, c.elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                          const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 wan_status check_heads(const KvCache& c, int q_heads) {
@@ -271,7 +318,9 @@ wan_status wan_kv_attention(const wan_kv_cache* cache, const wan_kv_batch* batch
       return fail(WAN_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
     int sms = 0;
     WAN_TRY(sm_count(&sms));
-    const int64_t bytes = kv_attention_workspace(a, sms);
+    ChunkLaunch L;
+    bool chunk = chunk_rows(a, &L.geo);
+    const int64_t bytes = chunk ? kv_chunk_workspace(a, sms) : kv_attention_workspace(a, sms);
     if (!workspace || ((uintptr_t)workspace & 15) || workspace_bytes < bytes)
       return fail(WAN_ERR_INVALID_ARG, "workspace of %lld bytes, 16-byte aligned, needed (%lld given)", (long long)bytes,
                   (long long)workspace_bytes);
@@ -279,7 +328,16 @@ wan_status wan_kv_attention(const wan_kv_cache* cache, const wan_kv_batch* batch
     a.q_t = q_token, a.q_h = q_head, a.o_t = out_token, a.o_h = out_head;
     a.scale_log2 = (float)(scale * 1.4426950408889634);
     a.workspace = workspace;
-    CUDA_TRY(launch_kv_attention(a, sms, (cudaStream_t)stream));
+    if (chunk) {
+      // k and v may order their dimensions differently; then, and where a map cannot be made, the split kernel runs
+      // (its workspace is the smaller one)
+      ChunkGeo gk = L.geo;
+      chunk = cache_map(a.c, a.c.k, a.c.k_page, a.c.k_head, a.c.k_row, &gk, &L.k) &&
+              cache_map(a.c, a.c.v, a.c.v_page, a.c.v_head, a.c.v_row, &L.geo, &L.v) && gk.dim_row == L.geo.dim_row &&
+              gk.dim_head == L.geo.dim_head && gk.dim_page == L.geo.dim_page;
+      L.a = a;
+    }
+    CUDA_TRY(chunk ? launch_kv_chunk(L, sms, (cudaStream_t)stream) : launch_kv_attention(a, sms, (cudaStream_t)stream));
     return WAN_OK;
   })
 }
@@ -289,7 +347,8 @@ int64_t wan_kv_attention_workspace(const wan_kv_cache* cache, const wan_kv_batch
     AttnArgs a;
     int sms = 0;
     if (attention_args(cache, batch, q_heads, &a) != WAN_OK || sm_count(&sms) != WAN_OK) return -1;
-    return kv_attention_workspace(a, sms);
+    ChunkGeo g;
+    return chunk_rows(a, &g) ? kv_chunk_workspace(a, sms) : kv_attention_workspace(a, sms);
   } catch (...) {
     fail(WAN_ERR_INTERNAL, "unexpected C++ exception");
     return -1;
