@@ -128,15 +128,16 @@ SIGNATURES = {
     "wan_selftest_attention_timeout": (_i32, [_i32, ctypes.POINTER(_i32), _vp]),
     "wan_causal_conv3d_noalloc": (_i32, [_vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _i32, _i32, _i32, _i32,
                                          _i32, _vp, _vp]),
-    "wan_rotary": (_i32, [_vp, ctypes.POINTER(_i64 * 3), _vp, ctypes.POINTER(_i64 * 3), _i32, _i32, _i32, _i32, _i32,
-                          _vp, _i32, _i64, ctypes.POINTER(WanRotation), _i32, _vp]),
-    "wan_kv_check": (_i32, [ctypes.POINTER(WanKvBatch), _i32, _i64, _i32]),
+    # structs and stride triples go in as their bytes
+    "wan_rotary": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                          _vp, _i32, _i64, _vp, _i32, _vp]),
+    "wan_kv_check": (_i32, [_vp, _i32, _i64, _i32]),
     "wan_kv_status": (_i32, [_vp, _vp]),
-    "wan_kv_append": (_i32, [ctypes.POINTER(WanKvCache), ctypes.POINTER(WanKvBatch), _vp, _i64, _i64, _vp, _i64, _i64,
-                             _vp, _i32, _i64, _i64, _vp, _i64, _i64, ctypes.POINTER(WanRotation), _vp, _i32, _vp]),
-    "wan_kv_attention": (_i32, [ctypes.POINTER(WanKvCache), ctypes.POINTER(WanKvBatch), _vp, _i32, _i64, _i64, _vp,
+    "wan_kv_append": (_i32, [_vp, _vp, _vp, _i64, _i64, _vp, _i64, _i64,
+                             _vp, _i32, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i32, _vp]),
+    "wan_kv_attention": (_i32, [_vp, _vp, _vp, _i32, _i64, _i64, _vp,
                                 ctypes.c_float, _vp, _i64, _i64, _vp, _vp, _i64, _vp]),
-    "wan_kv_attention_workspace": (_i64, [ctypes.POINTER(WanKvCache), ctypes.POINTER(WanKvBatch), _i32]),
+    "wan_kv_attention_workspace": (_i64, [_vp, _vp, _i32]),
 }
 
 _lib = None

@@ -20,15 +20,22 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import struct
 
 import torch
 
-from ._lib import (WAN_BF16, WAN_F16, WAN_F32, WanKvBatch, WanKvCache, WanRotation, check, load)
+from ._lib import WAN_BF16, WAN_F16, WAN_F32, WanRotation, check, load
 
 __all__ = ["Rotation", "rotary", "rotary_grad", "kv_append", "kv_attention", "kv_check", "kv_status"]
 
 _CODES = {torch.float32: WAN_F32, torch.bfloat16: WAN_BF16, torch.float16: WAN_F16}
-_I64x3 = ctypes.c_int64 * 3
+_HALVES = (torch.bfloat16, torch.float16)
+_INT32 = (torch.int32,)
+# The C structs as bytes: packing costs a quarter of building a ctypes Structure
+# (the launch path's host time is what a small call costs).
+_pack3 = struct.Struct("@qqq").pack             # const int64_t[3]
+_pack_cache = struct.Struct("@PPiiiiqqqqqqq").pack  # wan_kv_cache
+_pack_batch = struct.Struct("@PqiiPPiP").pack       # wan_kv_batch
 
 
 class Rotation:
@@ -90,29 +97,21 @@ def _rows_of(t: torch.Tensor, name: str):
         raise ValueError(f"{name}: the channels of a head must be contiguous")
 
 
-class _Launch:
-    """The device and stream of a call: current while it is entered (allocations belong to the stream)."""
+class _Guard:
+    """Makes the tensors' device and the caller's stream current (allocations then belong to that stream)."""
 
-    __slots__ = ("ptr", "_guards")
+    __slots__ = ("_guards",)
 
     def __init__(self, device: torch.device, stream):
-        if device.type != "cuda":
-            raise ValueError(f"the tensors must be CUDA tensors, not on {device}")
-        self._guards = []
-        if device.index != torch.cuda.current_device():
-            self._guards.append(torch.cuda.device(device))
-        if stream is None:
-            self.ptr = torch.cuda.current_stream(device).cuda_stream
-        else:
+        self._guards = [torch.cuda.device(device)]
+        if stream is not None:
             if stream.device != device:
                 raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-            self.ptr = stream.cuda_stream
             self._guards.append(torch.cuda.stream(stream))
 
     def __enter__(self):
         for g in self._guards:
             g.__enter__()
-        return self.ptr
 
     def __exit__(self, *exc):
         for g in reversed(self._guards):
@@ -120,38 +119,60 @@ class _Launch:
         return False
 
 
+def _elsewhere(device: torch.device, stream) -> bool:
+    """Whether a call needs a _Guard; refuses tensors that are not on a GPU."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors must be CUDA tensors, not on {device}")
+    return stream is not None or device.index != torch.cuda.current_device()
+
+
+# The calling stream's handle without building a torch.cuda.Stream (2 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _turn(x, positions, sections, theta, interleaved, out, stream, inverse):
-    if x.dtype not in _CODES:
+    code = _CODES.get(x.dtype)
+    if code is None:
         raise ValueError(f"x must be float32, bfloat16 or float16, not {x.dtype}")
-    if x.dim() not in (3, 4):
-        raise ValueError(f"x must be [tokens, heads, head_dim] or [batch, tokens, heads, head_dim], not {tuple(x.shape)}")
+    shape, xs = x.shape, x.stride()
+    if len(shape) == 4:
+        B, T, H, D = shape
+    elif len(shape) == 3:
+        B, (T, H, D), xs = 1, shape, (0, *xs)
+    else:
+        raise ValueError(f"x must be [tokens, heads, head_dim] or [batch, tokens, heads, head_dim], not {tuple(shape)}")
     _refuse_grad(x, out)
     rot = _rotation(sections, theta, interleaved)
-    B = x.shape[0] if x.dim() == 4 else 1
-    T, H, D = x.shape[-3:]
     dev = x.device
     _on(positions, dev, "positions", (torch.int32, torch.int64))
-    shape = tuple(positions.shape)
-    shared = shape == (T, rot.axes)
-    if not shared and shape != (B, T, rot.axes):
-        raise ValueError(f"positions must be [{T}, {rot.axes}] or [{B}, {T}, {rot.axes}], not {shape}")
+    pshape = positions.shape
+    shared = pshape == (T, rot.axes)
+    if not shared and pshape != (B, T, rot.axes):
+        raise ValueError(f"positions must be [{T}, {rot.axes}] or [{B}, {T}, {rot.axes}], not {tuple(pshape)}")
     if not positions.is_contiguous():
         raise ValueError("positions must be contiguous")
-    _rows_of(x, "x")
-    with _Launch(dev, stream) as ptr:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        else:
-            _on(out, dev, "out", (x.dtype,), x.dim())
-            if out.shape != x.shape:
-                raise ValueError(f"out must be {tuple(x.shape)}, not {tuple(out.shape)}")
-            _rows_of(out, "out")
-        xs, os = x.stride(), out.stride()
-        if x.dim() == 3:
-            xs, os = (0, *xs), (0, *os)
-        check(load().wan_rotary(x.data_ptr(), _I64x3(*xs[:3]), out.data_ptr(), _I64x3(*os[:3]), _CODES[x.dtype], B, T, H,
-                                D, positions.data_ptr(), positions.dtype == torch.int64,
-                                0 if shared else T * rot.axes, rot._ref, inverse, ptr))
+    if xs[3] != 1:
+        _rows_of(x, "x")
+    if _elsewhere(dev, stream):
+        with _Guard(dev, stream):
+            return _turn(x, positions, rot, theta, interleaved, out, None, inverse)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=dev)
+        os = (T * H * D, H * D, D)
+    else:
+        _on(out, dev, "out", (x.dtype,), len(shape))
+        if out.shape != shape:
+            raise ValueError(f"out must be {tuple(shape)}, not {tuple(out.shape)}")
+        _rows_of(out, "out")
+        os = out.stride()[:-1]
+        if len(os) == 2:
+            os = (0, *os)
+    status = load().wan_rotary(x.data_ptr(), _pack3(*xs[:3]), out.data_ptr(), _pack3(*os), code, B, T, H, D,
+                               positions.data_ptr(), positions.dtype is torch.int64, 0 if shared else T * rot.axes,
+                               rot._ref, inverse, _raw_stream(dev.index))
+    if status:
+        check(status)
     return out
 
 
@@ -171,34 +192,43 @@ def rotary_grad(dy: torch.Tensor, positions: torch.Tensor, sections, theta: floa
     return _turn(dy, positions, sections, theta, interleaved, out, stream, 1)
 
 
-def _cache(k_cache, v_cache) -> WanKvCache:
-    dev = k_cache.device
-    _on(k_cache, dev, "k_cache", (torch.bfloat16, torch.float16), 4)
-    _on(v_cache, dev, "v_cache", (k_cache.dtype,), 4)
-    if k_cache.shape != v_cache.shape:
-        raise ValueError(f"k_cache is {tuple(k_cache.shape)}, v_cache {tuple(v_cache.shape)}")
-    _rows_of(k_cache, "k_cache")
-    _rows_of(v_cache, "v_cache")
-    pages, heads, size, D = k_cache.shape
-    ks, vs = k_cache.stride(), v_cache.stride()
-    return WanKvCache(k_cache.data_ptr(), v_cache.data_ptr(), _CODES[k_cache.dtype], heads, size, D, pages,
-                      ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
+def _cache(k_cache, v_cache, dev):
+    """wan_kv_cache of the two tensors (packed), and their common shape."""
+    dt = k_cache.dtype
+    if dt not in _HALVES:
+        _on(k_cache, dev, "k_cache", _HALVES, 4)
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.dtype is not dt or v_cache.device != dev:
+        _on(k_cache, dev, "k_cache", _HALVES, 4)
+        _on(v_cache, dev, "v_cache", (dt,), 4)
+    if v_cache.shape != shape:
+        raise ValueError(f"k_cache is {tuple(shape)}, v_cache {tuple(v_cache.shape)}")
+    k0, k1, k2, k3 = k_cache.stride()
+    v0, v1, v2, v3 = v_cache.stride()
+    if k3 != 1 or v3 != 1:
+        _rows_of(k_cache, "k_cache")
+        _rows_of(v_cache, "v_cache")
+    pages, heads, size, D = shape
+    return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), _CODES[dt], heads, size, D, pages, k0, k1, k2, v0, v1,
+                       v2), heads, size, D
 
 
-_INT32 = (torch.int32,)
-
-
-def _batch(dev, pages, lengths, cu_tokens, tokens, status) -> WanKvBatch:
-    _on(pages, dev, "pages", _INT32, 2)
-    _on(lengths, dev, "lengths", _INT32, 1)
-    B = lengths.shape[0]
-    if pages.shape[0] != B:
-        raise ValueError(f"pages has {pages.shape[0]} rows for {B} sequences")
-    if pages.shape[1] > 1 and pages.stride(1) != 1:
+def _batch(dev, pages, lengths, cu_tokens, tokens, status):
+    """wan_kv_batch of the tables (packed), and the number of sequences."""
+    i32 = torch.int32
+    if pages.dtype is not i32 or lengths.dtype is not i32 or pages.device != dev or lengths.device != dev or \
+            pages.dim() != 2 or lengths.dim() != 1:
+        _on(pages, dev, "pages", _INT32, 2)
+        _on(lengths, dev, "lengths", _INT32, 1)
+    B, n = pages.shape
+    if lengths.shape[0] != B:
+        raise ValueError(f"pages has {B} rows for {lengths.shape[0]} sequences")
+    p0, p1 = pages.stride()
+    if p1 != 1 and n > 1:
         raise ValueError("the rows of pages must be contiguous")
     if B > 1 and lengths.stride(0) != 1:
         raise ValueError("lengths must be contiguous")
-    cu = None
+    cu = st = 0
     if cu_tokens is not None:
         _on(cu_tokens, dev, "cu_tokens", _INT32, 1)
         if cu_tokens.shape[0] != B + 1 or cu_tokens.stride(0) != 1:
@@ -208,8 +238,8 @@ def _batch(dev, pages, lengths, cu_tokens, tokens, status) -> WanKvBatch:
         _on(status, dev, "status", _INT32)
         if status.numel() != 1:
             raise ValueError("status must hold one value")
-        status = status.data_ptr()
-    return WanKvBatch(pages.data_ptr(), pages.stride(0), pages.shape[1], B, lengths.data_ptr(), cu, tokens, status)
+        st = status.data_ptr()
+    return _pack_batch(pages.data_ptr(), p0, n, B, lengths.data_ptr(), cu, tokens, st), B
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor,
@@ -231,52 +261,76 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     sequence stay uninitialised).  status: an int32 tensor of one value that
     takes a code if the tables name something that is not there (kv_status)."""
     _refuse_grad(k, v, q, k_cache, v_cache, q_out)
-    c = _cache(k_cache, v_cache)
-    dev, dt = k_cache.device, (k_cache.dtype,)
-    _on(k, dev, "k", dt, 3)
-    _on(v, dev, "v", dt, 3)
-    T = k.shape[0]
-    if k.shape != v.shape or k.shape[1] != c.heads or k.shape[2] != c.head_dim:
-        raise ValueError(f"k is {tuple(k.shape)} and v {tuple(v.shape)}, the cache's tokens [n, {c.heads}, {c.head_dim}]")
-    _rows_of(k, "k")
-    _rows_of(v, "v")
-    b = _batch(dev, pages, lengths, cu_tokens, T, status)
-    rot, pos = None, None
+    dev = k_cache.device
+    c, heads, size, D = _cache(k_cache, v_cache, dev)
+    dt = k_cache.dtype
+    if k.dtype is not dt or v.dtype is not dt or k.device != dev or v.device != dev or k.dim() != 3:
+        _on(k, dev, "k", (dt,), 3)
+        _on(v, dev, "v", (dt,), 3)
+    shape = k.shape
+    T = shape[0]
+    if v.shape != shape or shape[1] != heads or shape[2] != D:
+        raise ValueError(f"k is {tuple(shape)} and v {tuple(v.shape)}, the cache's tokens [n, {heads}, {D}]")
+    ks, vs = k.stride(), v.stride()
+    if ks[2] != 1 or vs[2] != 1:
+        _rows_of(k, "k")
+        _rows_of(v, "v")
+    b, _ = _batch(dev, pages, lengths, cu_tokens, T, status)
+    rot = pos = None
+    pos64 = False
     if sections is not None:
         rot = _rotation(sections, theta, interleaved)
         if positions is None:
             raise ValueError("sections need positions")
         _on(positions, dev, "positions", (torch.int32, torch.int64), 2)
-        if tuple(positions.shape) != (T, rot.axes) or not positions.is_contiguous():
+        if positions.shape != (T, rot.axes) or not positions.is_contiguous():
             raise ValueError(f"positions must be contiguous [{T}, {rot.axes}], not {tuple(positions.shape)}")
-        pos = positions.data_ptr()
+        pos, pos64, rot = positions.data_ptr(), positions.dtype is torch.int64, rot._ref
     elif positions is not None:
         raise ValueError("positions need sections")
-    if q is None and q_out is not None:
-        raise ValueError("q_out needs q")
-    ks, vs = k.stride(), v.stride()
-    with _Launch(dev, stream) as ptr:
-        if q is None:
-            qa = (None, 0, 0, 0, None, 0, 0)
-        else:
-            _on(q, dev, "q", dt, 3)
-            if q.shape[0] != T or q.shape[2] != c.head_dim:
-                raise ValueError(f"q is {tuple(q.shape)}, not [{T}, heads, {c.head_dim}]")
+    if _elsewhere(dev, stream):
+        with _Guard(dev, stream):
+            return kv_append(k, v, k_cache, v_cache, pages, lengths, cu_tokens, positions, sections, theta, interleaved, q,
+                             q_out, status)
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out needs q")
+        qa = (None, 0, 0, 0, None, 0, 0)
+    else:
+        _on(q, dev, "q", (dt,), 3)
+        qshape, qs = q.shape, q.stride()
+        if qshape[0] != T or qshape[2] != D:
+            raise ValueError(f"q is {tuple(qshape)}, not [{T}, heads, {D}]")
+        if qs[2] != 1:
             _rows_of(q, "q")
-            if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            else:
-                _on(q_out, dev, "q_out", dt, 3)
-                if q_out.shape != q.shape:
-                    raise ValueError(f"q_out is {tuple(q_out.shape)}, not {tuple(q.shape)}")
-                _rows_of(q_out, "q_out")
-            qs, os = q.stride(), q_out.stride()
-            # an empty tensor has no address, but a call with q is one all the same
-            qa = (q.data_ptr() or None, q.shape[1], qs[0], qs[1], q_out.data_ptr() or None, os[0], os[1])
-        check(load().wan_kv_append(ctypes.byref(c), ctypes.byref(b), k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0],
-                                   vs[1], *qa, rot._ref if rot else None, pos,
-                                   pos is not None and positions.dtype == torch.int64, ptr))
+        if q_out is None:
+            q_out = torch.empty(qshape, dtype=dt, device=dev)
+            os = (qshape[1] * D, D)
+        else:
+            _on(q_out, dev, "q_out", (dt,), 3)
+            if q_out.shape != qshape:
+                raise ValueError(f"q_out is {tuple(q_out.shape)}, not {tuple(qshape)}")
+            _rows_of(q_out, "q_out")
+            os = q_out.stride()
+        # an empty tensor has no address, but a call with q is one all the same
+        qa = (q.data_ptr() or None, qshape[1], qs[0], qs[1], q_out.data_ptr() or None, os[0], os[1])
+    status = load().wan_kv_append(c, b, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], *qa, rot, pos, pos64,
+                                  _raw_stream(dev.index))
+    if status:
+        check(status)
     return q_out
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace(dtype, heads, size, D, B, T, q_heads, device_index) -> int:
+    """Bytes of workspace of a call of these sizes (wan_kv_attention_workspace), whatever the addresses."""
+    step = 8 * -(-D // 8)
+    c = _pack_cache(16, 16, dtype, heads, size, D, 1, step, step, step, step, step, step)
+    n = load().wan_kv_attention_workspace(c, _pack_batch(16, 1, 1, B, 16, 16, T, 0), q_heads)
+    if n < 0:
+        msg = load().wan_vae_last_error()
+        raise ValueError(msg.decode())
+    return n
 
 
 def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor,
@@ -293,39 +347,46 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     rows behind the last sequence stay uninitialised).  return_lse: also the
     fp32 logarithms of the sums, [tokens, q_heads]."""
     _refuse_grad(q, k_cache, v_cache, out)
-    c = _cache(k_cache, v_cache)
-    dev, dt = k_cache.device, (k_cache.dtype,)
-    _on(q, dev, "q", dt, 3)
-    T, H, D = q.shape
-    if D != c.head_dim:
-        raise ValueError(f"q is {tuple(q.shape)}, the cache's head dim {c.head_dim}")
-    _rows_of(q, "q")
-    b = _batch(dev, pages, lengths, cu_tokens, T, status)
+    dev = k_cache.device
+    c, heads, size, D = _cache(k_cache, v_cache, dev)
+    dt = k_cache.dtype
+    shape, qs = q.shape, q.stride()
+    if q.dtype is not dt or q.device != dev or len(shape) != 3:
+        _on(q, dev, "q", (dt,), 3)
+    T, H, qD = shape
+    if qD != D:
+        raise ValueError(f"q is {tuple(shape)}, the cache's head dim {D}")
+    if qs[2] != 1:
+        _rows_of(q, "q")
+    b, B = _batch(dev, pages, lengths, cu_tokens, T, status)
     rp = None
     if ranges is not None:
         _on(ranges, dev, "ranges", _INT32, 2)
-        if tuple(ranges.shape) != (T, 2) or not ranges.is_contiguous():
+        if ranges.shape != (T, 2) or not ranges.is_contiguous():
             raise ValueError(f"ranges must be contiguous [{T}, 2], not {tuple(ranges.shape)}")
         rp = ranges.data_ptr()
-    lib = load()
-    cp, bp = ctypes.byref(c), ctypes.byref(b)
-    with _Launch(dev, stream) as ptr:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        else:
-            _on(out, dev, "out", dt, 3)
-            if out.shape != q.shape:
-                raise ValueError(f"out is {tuple(out.shape)}, not {tuple(q.shape)}")
-            _rows_of(out, "out")
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev) if return_lse else None
-        n = lib.wan_kv_attention_workspace(cp, bp, H)
-        if n < 0:
-            check(lib.wan_kv_attention(cp, bp, None, H, 0, 0, None, 0.0, None, 0, 0, None, None, 0, ptr))
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        qs, os = q.stride(), out.stride()
-        check(lib.wan_kv_attention(cp, bp, q.data_ptr(), H, qs[0], qs[1], rp, D ** -0.5 if scale is None else scale,
-                                   out.data_ptr(), os[0], os[1], None if lse is None else lse.data_ptr(),
-                                   ws.data_ptr(), n, ptr))
+    if _elsewhere(dev, stream):
+        with _Guard(dev, stream):
+            return kv_attention(q, k_cache, v_cache, pages, lengths, cu_tokens, ranges, scale, out, return_lse, status)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=dev)
+        os = (H * D, D)
+    else:
+        _on(out, dev, "out", (dt,), 3)
+        if out.shape != shape:
+            raise ValueError(f"out is {tuple(out.shape)}, not {tuple(shape)}")
+        _rows_of(out, "out")
+        os = out.stride()
+    n = _workspace(_CODES[dt], heads, size, D, B, T, H, dev.index)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    lse, lp = None, None
+    if return_lse:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+        lp = lse.data_ptr()
+    status = load().wan_kv_attention(c, b, q.data_ptr(), H, qs[0], qs[1], rp, D ** -0.5 if scale is None else scale,
+                                     out.data_ptr(), os[0], os[1], lp, ws.data_ptr(), n, _raw_stream(dev.index))
+    if status:
+        check(status)
     return (out, lse) if return_lse else out
 
 
@@ -336,13 +397,16 @@ def kv_check(pages: torch.Tensor, lengths: torch.Tensor, page_size: int, n_pages
     cpu = torch.device("cpu")
     if tokens is None:
         tokens = int(cu_tokens[-1]) if cu_tokens is not None else lengths.shape[0]
-    b = _batch(cpu, pages, lengths, cu_tokens, tokens, None)
-    check(load().wan_kv_check(ctypes.byref(b), page_size, n_pages, append))
+    b, _ = _batch(cpu, pages, lengths, cu_tokens, tokens, None)
+    check(load().wan_kv_check(b, page_size, n_pages, append))
 
 
 def kv_status(status: torch.Tensor, stream=None):
     """Waits for the stream, then raises WanError if a call left a code in
     `status` (which is cleared)."""
-    _on(status, status.device, "status", _INT32)
-    with _Launch(status.device, stream) as ptr:
-        check(load().wan_kv_status(status.data_ptr(), ptr))
+    dev = status.device
+    _on(status, dev, "status", _INT32)
+    if _elsewhere(dev, stream):
+        with _Guard(dev, stream):
+            return kv_status(status)
+    check(load().wan_kv_status(status.data_ptr(), _raw_stream(dev.index)))
