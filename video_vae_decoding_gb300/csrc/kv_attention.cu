@@ -513,8 +513,8 @@ __global__ void __launch_bounds__(DP) kv_join_kernel(const __grid_constant__ Att
 template <typename T, int DP>
 cudaError_t go_split(const AttnArgs& a, int sms, cudaStream_t s) {
   using C = Cfg<DP>;
-  // every call: the attribute belongs to the current device
-  cudaError_t e = cudaFuncSetAttribute(kv_split_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem((const void*)kv_split_kernel<T, DP>, C::kSmem, &allowed);
   if (e != cudaSuccess) return e;
   const int G = sms * C::kCtas;
   kv_split_kernel<T, DP><<<G, kThreads, C::kSmem, s>>>(a);

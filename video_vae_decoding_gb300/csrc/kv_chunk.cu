@@ -671,7 +671,8 @@ __global__ void __launch_bounds__(kTileRows) kv_chunk_join_kernel(const __grid_c
 template <typename T, int DP>
 cudaError_t go(const ChunkLaunch& L, int sms, cudaStream_t s) {
   using C = Cfg<DP>;
-  cudaError_t e = cudaFuncSetAttribute(kv_chunk_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem((const void*)kv_chunk_kernel<T, DP>, C::kSmem, &allowed);
   if (e != cudaSuccess) return e;
   kv_chunk_kernel<T, DP><<<sms, kThreads, C::kSmem, s>>>(L.k, L.v, L.a, L.geo);
   e = cudaGetLastError();

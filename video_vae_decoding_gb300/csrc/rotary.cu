@@ -9,13 +9,17 @@
 // Bound: memory, each element read once and written once.  The angle is the
 // part that could exceed it: cos and sin cost about 30 instructions a pair,
 // against 8 bytes moved, so a thread forms them once for its channels of a
-// token and applies them to several heads.  The angle itself is an integer
+// token and applies them to up to eight heads, whose elements are on their way
+// meanwhile (Column).  The angle itself is an integer
 // product modulo one turn (RotaryPlan): exact to 2^-32 turns at any position,
 // where a product in 32-bit floating point loses the fraction of a turn from a
 // few thousand positions on, and 64-bit floating point runs at a small
 // fraction of the rate here.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <algorithm>
+#include <type_traits>
 
 #include "ptx.cuh"
 #include "token_ops.h"
@@ -24,19 +28,7 @@ namespace wan {
 
 namespace {
 
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
-template <typename T>
-__device__ __forceinline__ T from_f(float v);
-template <>
-__device__ __forceinline__ float from_f<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
-
-// E elements, as one access of W elements' bytes each.
+// N elements in accesses of W: 32-bit words of one fp32 or two 16-bit values.
 template <int BYTES>
 struct Raw;
 template <>
@@ -48,241 +40,313 @@ struct Raw<4> { using t = uint32_t; };
 template <>
 struct Raw<2> { using t = uint16_t; };
 
-template <typename T, int E, int W>
+template <typename T, int N, int W>
 struct Vec {
-  static_assert(E % W == 0, "whole accesses");
+  static_assert(N % W == 0, "whole accesses");
   using R = typename Raw<W * (int)sizeof(T)>::t;
+  static constexpr int kWords = (N * (int)sizeof(T) + 3) / 4;
   union {
-    R r[E / W];
-    T e[E];
+    R r[N / W];
+    uint32_t w[kWords];
   };
   __device__ __forceinline__ Vec() {}
   __device__ __forceinline__ void load(const T* p) {
+    if (W * sizeof(T) == 2) w[kWords - 1] = 0;
 #pragma unroll
-    for (int i = 0; i < E / W; ++i) r[i] = reinterpret_cast<const R*>(p)[i];
+    for (int i = 0; i < N / W; ++i) r[i] = reinterpret_cast<const R*>(p)[i];
   }
   __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
-    for (int i = 0; i < E / W; ++i) reinterpret_cast<R*>(p)[i] = r[i];
+    for (int i = 0; i < N / W; ++i) reinterpret_cast<R*>(p)[i] = r[i];
   }
 };
 
-__device__ __forceinline__ long long position(const void* pos, int pos64, long long i) {
-  return pos64 ? ((const long long*)pos)[i] : (long long)((const int*)pos)[i];
+// The two 16-bit values of a word, and back (one conversion for both).
+template <typename T>
+__device__ __forceinline__ float2 unpack(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack<__nv_bfloat16>(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+template <>
+__device__ __forceinline__ float2 unpack<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t repack(float x, float y);
+template <>
+__device__ __forceinline__ uint32_t repack<__nv_bfloat16>(float x, float y) { return pack_bf16x2(x, y); }
+template <>
+__device__ __forceinline__ uint32_t repack<__half>(float x, float y) {
+  const __half2 v = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float turn_x(float x, float y, float c, float s) { return fmaf(x, c, -(y * s)); }
+__device__ __forceinline__ float turn_y(float x, float y, float c, float s) { return fmaf(y, c, x * s); }
+
+// Pairs of neighbouring channels: pair i is (2i, 2i + 1).  Bit i of `on`: turned.
+template <typename T, int N, int W>
+__device__ __forceinline__ void turn_pairs(Vec<T, N, W>& v, const float* c, const float* s, uint32_t on) {
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    if (sizeof(T) == 4) {
+      const int e = sizeof(T) == 4 ? 2 * i : 0;
+      const float x = __uint_as_float(v.w[e]), y = __uint_as_float(v.w[sizeof(T) == 4 ? e + 1 : 0]);
+      if ((on >> i) & 1) {
+        v.w[e] = __float_as_uint(turn_x(x, y, c[i], s[i]));
+        v.w[sizeof(T) == 4 ? e + 1 : 0] = __float_as_uint(turn_y(x, y, c[i], s[i]));
+      }
+    } else {
+      const float2 f = unpack<typename std::conditional<sizeof(T) == 4, __half, T>::type>(v.w[sizeof(T) == 4 ? 0 : i]);
+      if ((on >> i) & 1)
+        v.w[sizeof(T) == 4 ? 0 : i] = repack<typename std::conditional<sizeof(T) == 4, __half, T>::type>(
+            turn_x(f.x, f.y, c[i], s[i]), turn_y(f.x, f.y, c[i], s[i]));
+    }
+  }
+}
+// Channels of the first half (a) with those of the second (b), all turned.
+template <typename T, int N, int W>
+__device__ __forceinline__ void turn_halves(Vec<T, N, W>& a, Vec<T, N, W>& b, const float* c, const float* s) {
+  using H = typename std::conditional<sizeof(T) == 4, __half, T>::type;
+#pragma unroll
+  for (int i = 0; i < Vec<T, N, W>::kWords; ++i) {
+    if (sizeof(T) == 4) {
+      const float x = __uint_as_float(a.w[i]), y = __uint_as_float(b.w[i]);
+      a.w[i] = __float_as_uint(turn_x(x, y, c[i], s[i]));
+      b.w[i] = __float_as_uint(turn_y(x, y, c[i], s[i]));
+    } else {
+      const float2 x = unpack<H>(a.w[i]), y = unpack<H>(b.w[i]);
+      const int p = 2 * i, q = 2 * i + 1 < N ? 2 * i + 1 : p;
+      a.w[i] = repack<H>(turn_x(x.x, y.x, c[p], s[p]), turn_x(x.y, y.y, c[q], s[q]));
+      b.w[i] = repack<H>(turn_y(x.x, y.x, c[p], s[p]), turn_y(x.y, y.y, c[q], s[q]));
+    }
+  }
 }
 
-// cos and sin of pair j's angle at the position whose coordinates start at
-// value i of pos.
-__device__ __forceinline__ void pair_angle(const RotaryPlan& plan, int j, const void* pos, int pos64, long long i,
-                                           float* c, float* s) {
-  const long long p = position(pos, pos64, i + plan.axis[j]);
-  const uint64_t turn = (uint64_t)p * plan.turn[j];
-  // the signed top word, -2^31 .. 2^31, is -1/2 .. 1/2 turns: -1 .. 1 half turns
-  const float half_turns = (float)(int)(turn >> 32) * 0x1p-31f;
-  sincospif(half_turns, s, c);
-  if (plan.inverse) *s = -*s;
-}
+constexpr int kRotaryThreads = 256;
 
-// The columns a thread handles in one head.  Interleaved: E consecutive
-// channels, E / 2 pairs.  Halves: columns below pairs / E hold E pairs, the
-// channels [E c, E c + E) and the ones `pairs` further on; the columns after
-// them hold E channels that pass through.
+// How a launch covers tokens x heads x columns.  A column is what a thread
+// handles of one head: interleaved, E consecutive channels (E / 2 pairs);
+// halves, below pairs / E the channels [E c, E c + E) and the ones `pairs`
+// further on (E pairs), after that E channels that pass through.  A block takes
+// tpb tokens at a time, `per` times, and one group of hpt heads (blockIdx.y).
+struct Cover {
+  int cols, tpb, per, hpt;
+};
+
 template <typename T, int E, int W, bool INTER>
 struct Column {
   static constexpr int NP = INTER ? E / 2 : E;
-  float c[NP], s[NP];
-  uint32_t on;  // interleaved: bit i set if pair i is turned (the others pass through)
+  // heads per thread: 128 bytes (16-byte columns), asked for together
+  static constexpr int U = INTER ? 8 : 4;
   int c0, c1;   // first channel, and the second half's first channel (or -1)
+  int p0;       // first pair
+  uint32_t on;  // bit i: pair p0 + i is turned
+  float c[NP], s[NP];
+  Vec<T, E, W> a[U], b[INTER ? 1 : U];
 
   static __host__ __device__ __forceinline__ int count(int D, int pairs) {
     return INTER ? D / E : pairs / E + (D - 2 * pairs) / E;
   }
-  __device__ __forceinline__ void place(int col, int pairs, bool turn) {
+  __device__ __forceinline__ void place(int col, int pairs) {
     on = 0;
+    c1 = -1;
     if (INTER) {
       c0 = col * E;
-      c1 = -1;
-      if (turn) {
+      p0 = col * NP;
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
-          if (col * NP + i < pairs) on |= 1u << i;
-      }
+      for (int i = 0; i < NP; ++i)
+        if (p0 + i < pairs) on |= 1u << i;
     } else {
       const int rot = pairs / E;
+      p0 = col * E;
+      c0 = col < rot ? col * E : 2 * pairs + (col - rot) * E;
       if (col < rot) {
-        c0 = col * E;
         c1 = c0 + pairs;
-        on = turn ? 1u : 0u;
-      } else {
-        c0 = 2 * pairs + (col - rot) * E;
-        c1 = -1;
+        on = (1u << NP) - 1u;
       }
     }
   }
-  __device__ __forceinline__ void angles(const RotaryPlan& plan, int col, const void* pos, int pos64, long long i0) {
+  // `n` heads (at most U) of a token
+  __device__ __forceinline__ void fetch(const T* x, long long xh, int n) {
+    x += c0;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      c[i] = 1.f;
-      s[i] = 0.f;
-      if (INTER ? (on >> i) & 1 : on) pair_angle(plan, col * NP + i, pos, pos64, i0, &c[i], &s[i]);
-    }
-  }
-  __device__ __forceinline__ void turn(Vec<T, E, W>& a, Vec<T, E, W>& b) const {
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      T& xr = INTER ? a.e[INTER ? 2 * i : i] : a.e[i];
-      T& yr = INTER ? a.e[INTER ? 2 * i + 1 : i] : b.e[i];
-      const float x = to_f(xr), y = to_f(yr);
-      const T nx = from_f<T>(fmaf(x, c[i], -(y * s[i]))), ny = from_f<T>(fmaf(y, c[i], x * s[i]));
-      if (INTER ? (on >> i) & 1 : on) {
-        xr = nx;
-        yr = ny;
+    for (int u = 0; u < U; ++u, x += xh)
+      if (u < n) {
+        a[u].load(x);
+        if (!INTER && c1 >= 0) b[INTER ? 0 : u].load(x + (c1 - c0));
       }
+  }
+  // the angles at the position whose coordinates start at value i0 of pos
+  __device__ __forceinline__ void angles(const uint64_t* turn, const uint8_t* axis, float sign, const void* pos,
+                                         int pos64, long long i0) {
+    if (!on) return;
+    uint64_t p = 0;
+    int ax = -1;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      if (!((on >> i) & 1)) continue;
+      const int x = axis[p0 + i];
+      if (x != ax) p = pos64 ? (uint64_t)((const long long*)pos)[i0 + x] : (uint64_t)(long long)((const int*)pos)[i0 + x];
+      ax = x;
+      // the product's signed top word, -2^31 .. 2^31, is -1/2 .. 1/2 turns: -1 .. 1 half turns
+      sincospif((float)(int)((p * turn[p0 + i]) >> 32) * 0x1p-31f, &s[i], &c[i]);
+      s[i] *= sign;
     }
   }
-  // heads h0 .. h1-1 of one token, U of them in flight
-  template <int U>
-  __device__ __forceinline__ void run(const T* x, long long xh, T* out, long long oh, int h0, int h1) const {
-    for (int h = h0; h < h1; h += U) {
-      Vec<T, E, W> a[U], b[U];
+  __device__ __forceinline__ void put(T* out, long long oh, int n) {
+    out += c0;
+    const bool all = on == (1u << NP) - 1u;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (h + u < h1) {
-          a[u].load(x + (h + u) * xh + c0);
-          if (!INTER && c1 >= 0) b[u].load(x + (h + u) * xh + c1);
+    for (int u = 0; u < U; ++u, out += oh)
+      if (u < n) {
+        if (INTER) {
+          if (all) turn_pairs(a[u], c, s, ~0u);
+          else if (on) turn_pairs(a[u], c, s, on);
+        } else if (on) {
+          turn_halves(a[u], b[INTER ? 0 : u], c, s);
         }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (h + u < h1) {
-          turn(a[u], b[u]);
-          a[u].store(out + (h + u) * oh + c0);
-          if (!INTER && c1 >= 0) b[u].store(out + (h + u) * oh + c1);
-        }
-    }
+        a[u].store(out);
+        if (!INTER && c1 >= 0) b[INTER ? 0 : u].store(out + (c1 - c0));
+      }
   }
 };
 
-constexpr int kRotaryThreads = 256;
+// The plan's frequencies and axes in shared memory: lanes that ask the kernel's
+// parameters for different ones are served one after the other.
+struct Table {
+  uint64_t turn[kMaxRotaryPairs];
+  uint8_t axis[kMaxRotaryPairs];
+  __device__ __forceinline__ void fill(const RotaryPlan& plan) {
+    for (int j = threadIdx.x; j < plan.pairs; j += blockDim.x) {
+      turn[j] = plan.turn[j];
+      axis[j] = plan.axis[j];
+    }
+    __syncthreads();
+  }
+};
 
 template <typename T, int E, int W, bool INTER>
-__global__ void __launch_bounds__(kRotaryThreads)
-    rotary_kernel(const __grid_constant__ RotaryArgs a, int cols, int tpb, int hpt) {
-  const int tl = threadIdx.x / cols, col = threadIdx.x - tl * cols;
-  const long long tok = (long long)blockIdx.x * tpb + tl;
-  if (tok >= (long long)a.B * a.S) return;
-  const int b = (int)(tok / a.S), t = (int)(tok - (long long)b * a.S);
+__global__ void __launch_bounds__(kRotaryThreads, 3)
+    rotary_kernel(const __grid_constant__ RotaryArgs a, const Cover cv) {
+  __shared__ Table table;
+  table.fill(a.plan);
+  const int tl = threadIdx.x / cv.cols, h0 = blockIdx.y * cv.hpt, n = min(a.H - h0, cv.hpt);
   Column<T, E, W, INTER> cl;
-  cl.place(col, a.plan.pairs, true);
-  cl.angles(a.plan, col, a.pos, a.pos64, b * a.pos_b + (long long)t * a.plan.axes);
-  const int h0 = blockIdx.y * hpt;
-  cl.template run<4>((const T*)a.x + b * a.xb + t * a.xs, a.xh, (T*)a.out + b * a.ob + t * a.os, a.oh, h0,
-                     min(a.H, h0 + hpt));
+  cl.place(threadIdx.x - tl * cv.cols, a.plan.pairs);
+  const float sign = a.plan.inverse ? -1.f : 1.f;
+  const T* x = (const T*)a.x + h0 * a.xh;
+  T* out = (T*)a.out + h0 * a.oh;
+  const uint32_t S = a.S, rows = (uint32_t)a.B * S;
+  uint32_t row = blockIdx.x * (uint32_t)(cv.tpb * cv.per) + tl;
+  for (int k = 0; k < cv.per && row < rows; ++k, row += cv.tpb) {
+    const uint32_t b = a.B == 1 ? 0 : row / S;
+    const long long t = row - b * S;
+    cl.fetch(x + b * a.xb + t * a.xs, a.xh, n);
+    cl.angles(table.turn, table.axis, sign, a.pos, a.pos64, b * a.pos_b + t * a.plan.axes);
+    cl.put(out + b * a.ob + t * a.os, a.oh, n);
+  }
 }
 
-// Rows of k (turned), v (as they are) and q (turned): grid.y runs over groups
-// of hpt heads of q, then of k, then of v.  A token whose slot does not exist
-// (no sequence, a bad page, a position outside the table) leaves the cache as
-// it is and says so in the status word; its q row is turned all the same when
-// a sequence owns it.
-template <typename T, int E, int W, bool INTER>
-__global__ void __launch_bounds__(kRotaryThreads)
-    kv_append_kernel(const __grid_constant__ AppendArgs a, int cols, int tpb, int hpt, int nq, int nk) {
-  const int tl = threadIdx.x / cols, col = threadIdx.x - tl * cols;
-  const long long row = (long long)blockIdx.x * tpb + tl;
-  if (row >= a.b.T) return;
-  const int t = (int)row;
-  // the sequence of the row: the last one that starts at or before it
-  int b = t, r0 = t, n = 1;
-  if (a.b.cu) {
-    int lo = 0, hi = a.b.B;  // cu[lo] <= t (if anything is)
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.b.cu[mid] <= t) lo = mid;
-      else hi = mid;
-    }
-    b = lo;
-    if (!kv_rows(a.b.cu, a.b.T, b, &r0, &n)) {
-      if (a.b.status) atomicCAS(a.b.status, 0, (int)kDevBadLength);
-      return;
-    }
-    if (t < r0 || t >= r0 + n) return;  // behind the last sequence
-  } else if (t >= a.b.B) {
-    return;
+// The sequence that owns row t, and its first row and number of rows; false if
+// none does (behind the last sequence, or a range that is none).
+__device__ __forceinline__ bool owner(const AppendArgs& a, int t, int* b, int* r0, int* n) {
+  *b = *r0 = t;
+  *n = 1;
+  if (!a.b.cu) return t < a.b.B;
+  int lo = 0, hi = a.b.B;  // the last sequence that starts at or before t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.b.cu[mid] <= t) lo = mid;
+    else hi = mid;
   }
-  const int y = blockIdx.y;
-  const int kind = y < nq ? 0 : y < nq + nk ? 1 : 2;  // q, k, v
+  *b = lo;
+  if (!kv_rows(a.b.cu, a.b.T, lo, r0, n)) {
+    if (a.b.status) atomicCAS(a.b.status, 0, (int)kDevBadLength);
+    return false;
+  }
+  return t >= *r0 && t < *r0 + *n;
+}
+
+// Rows of q (turned), k (turned) and v (as they are): blockIdx.y runs over groups
+// of hpt heads of q, then of k, then of v.  A token whose slot does not exist (a
+// bad page, a position outside the table) leaves the cache as it is and says
+// so in the status word; its q is turned all the same when a sequence owns it.
+template <typename T, int E, int W, bool INTER>
+__global__ void __launch_bounds__(kRotaryThreads, 3)
+    kv_append_kernel(const __grid_constant__ AppendArgs a, const Cover cv, const int nq, const int nk) {
+  __shared__ Table table;
+  table.fill(a.plan);
+  const int y = blockIdx.y, kind = y < nq ? 0 : y < nq + nk ? 1 : 2;  // q, k, v
+  const int tl = threadIdx.x / cv.cols;
+  const int h0 = (kind == 0 ? y : kind == 1 ? y - nq : y - nq - nk) * cv.hpt;
+  const int n = min((kind == 0 ? a.q_heads : a.c.heads) - h0, cv.hpt);
+  const long long xt = kind == 0 ? a.q_t : kind == 1 ? a.k_t : a.v_t, xh = kind == 0 ? a.q_h : kind == 1 ? a.k_h : a.v_h;
+  const long long oh = kind == 0 ? a.qo_h : kind == 1 ? a.c.k_head : a.c.v_head;
+  const T* x = (const T*)(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + h0 * xh;
+  T* out = (T*)(kind == 0 ? a.qo : kind == 1 ? a.c.k : a.c.v) + h0 * oh;
   Column<T, E, W, INTER> cl;
-  cl.place(col, a.plan.pairs, kind < 2);
-  const T* src;
-  T* dst;
-  long long sh, dh;
-  int h0, heads;
-  if (kind == 0) {
-    src = (const T*)a.q + t * a.q_t;
-    dst = (T*)a.qo + t * a.qo_t;
-    sh = a.q_h;
-    dh = a.qo_h;
-    h0 = y * hpt;
-    heads = a.q_heads;
-  } else {
-    const long long i = (long long)a.b.lengths[b] - n + (t - r0);
-    int len;
-    if (!kv_length(a.b.lengths[b], a.b.max_pages, a.c.page_size, &len) || i < 0) {
-      if (a.b.status) atomicCAS(a.b.status, 0, (int)kDevBadLength);
-      return;
-    }
-    const int p = kv_page(a.b.pages + b * a.b.page_stride, (int)i, a.c.page_size, a.c.pages);
-    if (p < 0) {
-      if (a.b.status) atomicCAS(a.b.status, 0, (int)kDevBadPage);
-      return;
-    }
-    const int off = (int)i % a.c.page_size;
-    heads = a.c.heads;
-    if (kind == 1) {
-      src = (const T*)a.k + t * a.k_t;
-      sh = a.k_h;
-      dst = (T*)a.c.k + p * a.c.k_page + off * a.c.k_row;
-      dh = a.c.k_head;
-      h0 = (y - nq) * hpt;
+  cl.place(threadIdx.x - tl * cv.cols, a.plan.pairs);
+  if (kind == 2) cl.on = 0;
+  uint32_t row = blockIdx.x * (uint32_t)(cv.tpb * cv.per) + tl;
+  for (int k = 0; k < cv.per && row < (uint32_t)a.b.T; ++k, row += cv.tpb) {
+    const int t = (int)row;
+    cl.fetch(x + t * xt, xh, n);
+    cl.angles(table.turn, table.axis, 1.f, a.pos, a.pos64, (long long)t * a.plan.axes);
+    int b, r0, m, len;
+    if (!owner(a, t, &b, &r0, &m)) continue;
+    long long to;
+    if (kind == 0) {
+      to = t * a.qo_t;
     } else {
-      src = (const T*)a.v + t * a.v_t;
-      sh = a.v_h;
-      dst = (T*)a.c.v + p * a.c.v_page + off * a.c.v_row;
-      dh = a.c.v_head;
-      h0 = (y - nq - nk) * hpt;
+      const long long i = (long long)a.b.lengths[b] - m + (t - r0);
+      if (!kv_length(a.b.lengths[b], a.b.max_pages, a.c.page_size, &len) || i < 0) {
+        if (a.b.status) atomicCAS(a.b.status, 0, (int)kDevBadLength);
+        continue;
+      }
+      const int p = kv_page(a.b.pages + b * a.b.page_stride, (int)i, a.c.page_size, a.c.pages);
+      if (p < 0) {
+        if (a.b.status) atomicCAS(a.b.status, 0, (int)kDevBadPage);
+        continue;
+      }
+      const int r = (int)i % a.c.page_size;
+      to = kind == 1 ? p * a.c.k_page + r * a.c.k_row : p * a.c.v_page + r * a.c.v_row;
     }
+    cl.put(out + to, oh, n);
   }
-  if (kind < 2) cl.angles(a.plan, col, a.pos, a.pos64, (long long)t * a.plan.axes);
-  cl.template run<4>(src, sh, dst, dh, h0, min(heads, h0 + hpt));
 }
 
-// Heads per thread: as many as leave two blocks of threads per SM (one angle
-// serves them all), up to 8.
-int heads_per_thread(long long rows, int cols, int heads) {
-  int hpt = 8;
-  while (hpt > 1 && rows * cols * ((heads + hpt - 1) / hpt) < 2LL * 152 * kRotaryThreads) hpt /= 2;
-  return hpt;
+// Heads per thread: up to `most`, fewer where that leaves less than two blocks
+// of threads per SM.  Tokens per thread: 4 where that leaves two waves of three
+// blocks per SM (the table is then filled for four times the work), else 1.
+Cover cover(long long rows, int cols, int heads, int most) {
+  Cover c;
+  c.cols = cols;
+  c.tpb = kRotaryThreads / cols;
+  c.hpt = most;
+  while (c.hpt > 1 && rows * cols * ((heads + c.hpt - 1) / c.hpt) < 2LL * 152 * kRotaryThreads) c.hpt /= 2;
+  const long long threads = rows * cols * ((heads + c.hpt - 1) / c.hpt);
+  c.per = threads >= 152LL * 3 * 2 * 4 * kRotaryThreads ? 4 : 1;
+  return c;
+}
+unsigned blocks(long long rows, const Cover& c) {
+  const long long n = (long long)c.tpb * c.per;
+  return (unsigned)((rows + n - 1) / n);
 }
 
 template <typename T, int E, int W, bool INTER>
 cudaError_t go_rotary(const RotaryArgs& a, cudaStream_t s) {
-  const int cols = Column<T, E, W, INTER>::count(a.D, a.plan.pairs);
-  const int tpb = kRotaryThreads / cols;
+  using Col = Column<T, E, W, INTER>;
   const long long rows = (long long)a.B * a.S;
-  const int hpt = heads_per_thread(rows, cols, a.H);
-  const dim3 grid((unsigned)((rows + tpb - 1) / tpb), (a.H + hpt - 1) / hpt);
-  rotary_kernel<T, E, W, INTER><<<grid, tpb * cols, 0, s>>>(a, cols, tpb, hpt);
+  const Cover c = cover(rows, Col::count(a.D, a.plan.pairs), a.H, Col::U);
+  rotary_kernel<T, E, W, INTER><<<dim3(blocks(rows, c), (a.H + c.hpt - 1) / c.hpt), c.tpb * c.cols, 0, s>>>(a, c);
   return cudaGetLastError();
 }
 
 template <typename T, int E, int W, bool INTER>
 cudaError_t go_append(const AppendArgs& a, cudaStream_t s) {
-  const int cols = Column<T, E, W, INTER>::count(a.c.D, a.plan.pairs);
-  const int tpb = kRotaryThreads / cols;
-  const int hpt = heads_per_thread(a.b.T, cols, 2 * a.c.heads + a.q_heads);
-  const int nq = (a.q_heads + hpt - 1) / hpt, nk = (a.c.heads + hpt - 1) / hpt;
-  const dim3 grid((unsigned)((a.b.T + tpb - 1) / tpb), nq + 2 * nk);
-  kv_append_kernel<T, E, W, INTER><<<grid, tpb * cols, 0, s>>>(a, cols, tpb, hpt, nq, nk);
+  using Col = Column<T, E, W, INTER>;
+  const Cover c = cover(a.b.T, Col::count(a.c.D, a.plan.pairs), 2 * a.c.heads + a.q_heads, Col::U);
+  const int nq = (a.q_heads + c.hpt - 1) / c.hpt, nk = (a.c.heads + c.hpt - 1) / c.hpt;
+  kv_append_kernel<T, E, W, INTER><<<dim3(blocks(a.b.T, c), nq + 2 * nk), c.tpb * c.cols, 0, s>>>(a, c, nq, nk);
   return cudaGetLastError();
 }
 

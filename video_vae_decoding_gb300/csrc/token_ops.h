@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace wan {
 
 constexpr int kMaxHeadDim = 256;
@@ -98,6 +100,19 @@ struct AttnArgs {
 // Bytes of workspace of a call (a bound from host-side sizes alone).
 long long kv_attention_workspace(const AttnArgs& a, int sms);
 cudaError_t launch_kv_attention(const AttnArgs& a, int sms, cudaStream_t s);
+
+// Raises a kernel's dynamic shared memory limit once per device: `done` holds a
+// bit per device that has it (a call costs 0.5 us on the launch path).
+inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* done) {
+  int dev;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (done->load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // ---------------------------------------------------- shared index arithmetic
 // Range of a batch's rows that sequence b owns; false if cu does not describe
