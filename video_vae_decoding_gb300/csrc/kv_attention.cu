@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
   constexpr bool kQRegs = DP <= 128;  // q fragments in registers; at 256 channels they are fetched again
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t s_seen[kWarps][ST];
+  __shared__ long long s_line[kWarps + 2];
   __shared__ float2 s_ml[kWarps][kRows];
   __shared__ float s_p[kWarps][kRows][kWarpKeys];
 
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
 
   // --------------------------------------------- this block's piece of the line
   const Piece pc =
-      cut_line<kWarps>(a.b.B, me, G, [&](int b) { return tiles_of(a, sequence(a, b, false)).all; });
+      cut_line<kWarps>(a.b.B, me, G, s_line, [&](int b) { return tiles_of(a, sequence(a, b, false)).all; });
   if (threadIdx.x == 0) ws.open[me] = Open{0, 0, 0, 0};
   int b = pc.b;
   long long at = pc.at;

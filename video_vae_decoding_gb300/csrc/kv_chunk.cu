@@ -4,7 +4,7 @@
 // For 256 rows (row r of a sequence and key head h: token r / group, query head
 // h * group + r % group) in two halves of 128, per block of up to 128 keys j:
 //   S_t = Q_t K_j^T          (t = 0, 1: the halves; M = 128, N = 128)
-//   P_t = 2^(scale S_t - m)  one thread per row: running maximum m, moved only
+//   P_t = 2^(scale S_t - m)  two threads per row: running maximum m, moved only
 //                            when a block exceeds it by 8 (O is then rescaled)
 //   O_t += P_t V_j           P_t read from tensor memory, in the half of S_t's
 //                            columns that its own thread has already read
@@ -31,7 +31,10 @@ namespace wan {
 
 namespace {
 
-constexpr int kThreads = 384;  // warps 0 loads, 1 MMA, 2 TMEM, 3 idle, 4-7 softmax of half 0, 8-11 of half 1
+// Warps 0 loads, 1 MMA, 2 TMEM, 3 idle; 4-11 softmax of half 0, 12-19 of half 1:
+// two threads per row, which share a block's keys (64 each) and the output's
+// channels.
+constexpr int kThreads = 640;
 constexpr int kHalfRows = 128;
 constexpr int kTileRows = 256;
 constexpr int kBlock = 128;      // key columns of a block
@@ -44,7 +47,7 @@ struct Cfg {
   static constexpr int kSlot = ND * kBoxBytes;          // K or V of a block
   static constexpr int kStages = DP == 128 ? 5 : 10;
   static constexpr int kQ = 2 * ND * kBoxBytes;
-  static constexpr int kSmem = 1024 + kQ + kStages * kSlot + 1024;
+  static constexpr int kSmem = kQ + kStages * kSlot + 512 + 2048;
 };
 
 // Weights 2^(x - m) reach 2^kSlack; in float16 they are taken 2^7 times larger
@@ -73,21 +76,41 @@ __device__ __forceinline__ constexpr uint32_t idesc(uint32_t format, bool b_mn, 
   return (1u << 4) | (format << 7) | (format << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(128 >> 4) << 24);
 }
-// Operand with N contiguous in the 128-byte swizzle: atoms of 64 channels x 8
-// keys (1024 B) stacked by 8 keys (stride byte offset), the next 64 channels a
-// box further on (leading byte offset).
-__device__ __forceinline__ uint64_t sdesc_n128(uint32_t saddr) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(kBoxBytes >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
-         ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+// Shared-memory operand descriptors (ptx.cuh: sdesc_k128): the low word holds
+// the address and the leading byte offset, the high word never changes.
+//  first operand and K: K contiguous, leading offset unused (1)
+//  V: N contiguous in the 128-byte swizzle: atoms of 64 channels x 8 keys (1024 B)
+//     stacked by 8 keys (stride byte offset), the next 64 channels a box further
+//     on (leading byte offset)
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_v(uint32_t saddr) { return (saddr >> 4) | ((uint32_t)(kBoxBytes >> 4) << 16); }
+// One thread of the calling warp.
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+// D[tmem] (+)= A[smem] B[smem]^T
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(alo), "r"(blo), "r"(id), "r"(accumulate), "n"(kDescHigh)
+      : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem]
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t id,
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t id,
                                         uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(id), "r"(accumulate)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(blo), "r"(id), "r"(accumulate), "n"(kDescHigh)
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
@@ -101,6 +124,34 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
         "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
       : "r"(taddr));
 }
+
+// Two 32-bit products and sums, or sums, in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// The two warps whose threads share their rows (named barriers 1-8).
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 
 // ------------------------------------------------------------- pages and blocks
 __device__ __forceinline__ int blocks_of(const ChunkGeo& g, int page_size, int len) {
@@ -165,22 +216,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ AttnArgs a, const __grid_constant__ ChunkGeo geo) {
   using C = Cfg<DP>;
   constexpr int S = C::kStages, ND = C::ND;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // the only shared memory of the kernel, so it starts on a 1024-byte boundary, as the swizzled boxes must
+  extern __shared__ __align__(1024) uint8_t smem[];
+  static_assert(sizeof(Run) + 8 * (2 * S + 9) + 80 <= 512, "barriers and the run's description");
   uint8_t* sQ = smem;  // [half][64-channel box][128 rows]
   uint8_t* sR = sQ + C::kQ;
   uint64_t* full = reinterpret_cast<uint64_t*>(sR + S * C::kSlot);
   uint64_t* empty = full + S;
   uint64_t* s_full = empty + S;   // [2] S_t in TMEM
-  uint64_t* p_full = s_full + 2;  // [2] 128 arrivals: P_t in TMEM (S_t read, O_t rescaled)
+  uint64_t* p_full = s_full + 2;  // [2] 256 arrivals: P_t in TMEM (S_t read, O_t rescaled)
   uint64_t* o_done = p_full + 2;  // [2] O_t += P_t V_j complete
   uint64_t* done = o_done + 2;
+  if (smem_u32(smem) & 1023) {
+    if (a.b.status) atomicCAS(a.b.status, 0, (int)kDevTimeoutFull);
+    return;
+  }
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* hole = tmem_slot + 2;  // [16]: bit i of hole[j % 16]: page i of block j is none of the cache's
   Run* run = reinterpret_cast<Run*>(hole + 16);
+  // [2 halves][2 key halves][128 rows]: what the two threads of a row tell each other.  One buffer: a block's values
+  // are read before the block's P is complete, and the next block's come after.
+  float* red = reinterpret_cast<float*>(run + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int G = gridDim.x, me = blockIdx.x;
   const Space ws = space<DP>(a.workspace, G);
   const int page_size = a.c.page_size;
@@ -193,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(&s_full[t]), 1);
-      mbar_init(smem_u32(&p_full[t]), 128);
+      mbar_init(smem_u32(&p_full[t]), 256);
       mbar_init(smem_u32(&o_done[t]), 1);
     }
     mbar_init(smem_u32(done), 1);
@@ -213,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   put_empty<T>(a, me, G);
   const Piece pc =
-      cut_line<kThreads / 32>(a.b.B, me, G, [&](int b) { return tiles_of(a, geo, sequence(a, b, false)).all; });
+      cut_line<kThreads / 32>(a.b.B, me, G, reinterpret_cast<long long*>(red), [&](int b) { return tiles_of(a, geo, sequence(a, b, false)).all; });
   if (threadIdx.x == 0) ws.open[me] = Open{0, 0, 0, 0};
   tc_fence_before();
   __syncthreads();
@@ -261,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Seq s = run->s;
     const bool two = cnt > kHalfRows;
     // softmax threads: their row's keys, and its q
-    const int half = (warp - 4) >> 2;                     // softmax warps
-    const int hrow = 32 * (warp & 3) + lane;              // the row in its half: its TMEM lane
+    const int half = (warp - 4) >> 3, hk = (warp - 4) >> 2 & 1;  // softmax warps: the half, and the half of its keys
+    const int hrow = 32 * (warp & 3) + lane;                     // the row in its half: its TMEM lane
     const int row = half * kHalfRows + hrow;
     const bool mine = warp >= 4 && row < cnt;
     int lo = 0, hi = 0x40000000;  // rows past the tile's see everything: they need no mask
@@ -286,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         src = (const T*)a.q + (long long)(s.r0 + t) * a.q_t + (long long)(h * a.group + g) * a.q_h;
       }
 #pragma unroll 4
-      for (int c = 0; c < DP / 8; ++c) {
+      for (int c = hk * (DP / 16); c < (hk + 1) * (DP / 16); ++c) {
         uint4 v = make_uint4(0, 0, 0, 0);
         if (mine && c * 8 < a.c.D) {
           if (((uintptr_t)src & 15) == 0) {
@@ -359,27 +418,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) *stop = 1;
-      } else if (warp == 1 && lane == 0) {
+      } else if (warp == 1) {
         // --------------------------------------------------------------- MMAs
+        // The whole warp walks the blocks (what it computes stays in uniform
+        // registers, which the instructions take their operands from); one
+        // thread issues.
         const uint32_t idS = idesc(Pack<T>::kFormat, false, kBlock);
         const int dn = (a.c.D + 15) / 16;  // k steps of S, N / 16 of O
         const uint32_t idO = idesc(Pack<T>::kFormat, true, 16 * dn);
         const int last = two ? 1 : 0;
+        const bool one = elect();
+        const uint32_t q0 = desc_k(smem_u32(sQ)), kd0 = desc_k(smem_u32(sR)), vd0 = desc_v(smem_u32(sR));
         int slot = it % S, phase = (it / S) & 1;
         auto next = [&] {
           if (++slot == S) slot = 0, phase ^= 1;
         };
-        auto scores = [&](int t, int sl) {
-          const uint32_t q = smem_u32(sQ + t * ND * kBoxBytes), k = smem_u32(sR + sl * C::kSlot);
-          for (int u = 0; u < dn; ++u)
-            umma_bf16(tS + kBlock * t, sdesc_k128(q + (u >> 2) * kBoxBytes) + 2 * (u & 3),
-                      sdesc_k128(k + (u >> 2) * kBoxBytes) + 2 * (u & 3), idS, u > 0);
-          umma_commit(smem_u32(&s_full[t]));
+        auto scores = [&](int t, int sl, bool done_with_slot) {
+          const uint32_t q = q0 + t * (ND * kBoxBytes >> 4), k = kd0 + sl * (C::kSlot >> 4);
+          if (one) {
+#pragma unroll
+            for (int u = 0; u < 4 * ND; ++u)
+              if (u < dn)
+                umma_ss(tS + kBlock * t, q + (u >> 2) * (kBoxBytes >> 4) + 2 * (u & 3),
+                        k + (u >> 2) * (kBoxBytes >> 4) + 2 * (u & 3), idS, u > 0);
+            umma_commit(smem_u32(&s_full[t]));
+            if (done_with_slot) umma_commit(smem_u32(&empty[sl]));
+          }
         };
         ok = mbar_wait_bounded(smem_u32(&full[slot]), phase, err, kDevTimeoutFull);
         tc_fence_after();
-        for (int t = 0; t <= last && ok; ++t) scores(t, slot);
-        if (ok) umma_commit(smem_u32(&empty[slot]));
+        for (int t = 0; t <= last && ok; ++t) scores(t, slot, t == last);
         next();
         for (int j = 0; j < nb && ok; ++j) {
           const int sv = slot, pv = phase;
@@ -389,26 +457,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (more) next();
           ok = mbar_wait_bounded(smem_u32(&full[sv]), pv, err, kDevTimeoutFull);
           for (int t = 0; t <= last && ok; ++t) {
+            const uint32_t v = vd0 + sv * (C::kSlot >> 4);
             ok = mbar_wait_bounded(smem_u32(&p_full[t]), (ns[t] + j) & 1, err, kDevTimeoutAccum);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t v = smem_u32(sR + sv * C::kSlot);
+            if (one) {
 #pragma unroll
-            for (int u = 0; u < kBlock / 16; ++u)
-              umma_ts(tO + DP * t, tS + kBlock * t + 64 + 8 * u, sdesc_n128(v + 2048 * u), idO, j > 0 || u > 0);
-            umma_commit(smem_u32(&o_done[t]));
-            if (t == last) umma_commit(smem_u32(&empty[sv]));
+              for (int u = 0; u < kBlock / 16; ++u)
+                umma_ts(tO + DP * t, tS + kBlock * t + 64 + 8 * u, v + 128 * u, idO, j > 0 || u > 0);
+              umma_commit(smem_u32(&o_done[t]));
+              if (t == last) umma_commit(smem_u32(&empty[sv]));
+            }
             if (more) {
               if (t == 0) {
                 ok = mbar_wait_bounded(smem_u32(&full[sk]), pk, err, kDevTimeoutFull);
                 if (!ok) break;
                 tc_fence_after();
               }
-              scores(t, sk);
-              if (t == last) umma_commit(smem_u32(&empty[sk]));
+              scores(t, sk, t == last);
             }
           }
         }
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) *stop = 1;
       } else if (warp >= 4 && (half == 0 || two)) {
         // ------------------------------------------------------ softmax, output
@@ -416,45 +486,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t myS = tS + kBlock * half + lane_off, myO = tO + DP * half + lane_off;
         const float sc = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
         const int n0 = ns[half];
+        const int all_lo = run->all_lo[half], all_hi = run->all_hi[half];
         float m = -INFINITY, l = 0.f;
+        int base, rows, off = 0;  // first key of the block, rows that its pages give it, its place in a long page
+        block_keys(geo, page_size, j0, &base, &rows);
+        if (geo.parts > 1) off = base % page_size;
         for (int j = 0; j < nb; ++j) {
-          int base, rows;
-          block_keys(geo, page_size, j0 + j, &base, &rows);
+          if (j > 0) {  // the next block: the next pages, or the next part of one
+            base += rows;
+            if (geo.parts > 1) {
+              off = off + kBlock < page_size ? off + kBlock : 0;
+              rows = min(kBlock, page_size - off);
+            }
+          }
           // columns [c0, c1) are keys of this row
-          int c0 = max(0, lo - base), c1 = min(rows, hi - base);
+          const int c0 = max(0, lo - base), c1 = min(rows, hi - base);
           ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&s_full[half]), (n0 + j) & 1, err, kDevTimeoutAccum));
           if (!ok) break;
           tc_fence_after();
-          float x[4][32];
+          float x[2][32];  // keys 64 hk ..
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(myS + 32 * c, x[c]);
+          for (int c = 0; c < 2; ++c) tmem_ld32(myS + 64 * hk + 32 * c, x[c]);
           tmem_ld_wait();
           const uint32_t nones = hole[(j0 + j) & 15];
-          if (__any_sync(0xffffffffu, c0 > 0 || c1 < kBlock || nones != 0)) {
+          const int d0 = c0 - 64 * hk, d1 = c1 - 64 * hk;
+          if (__any_sync(0xffffffffu, d0 > 0 || d1 < 64 || nones != 0)) {
+            // by groups of 16 columns: most lie inside every row's range, or past a page's end
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int q = 0; q < 4; ++q)
+              if (__any_sync(0xffffffffu, d0 > 16 * q || d1 < 16 * q + 16)) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int col = 32 * c + i;
-                if (col < c0 || col >= c1) x[c][i] = -INFINITY;
+                for (int i = 0; i < 16; ++i)
+                  if (16 * q + i < d0 || 16 * q + i >= d1) x[q >> 1][16 * (q & 1) + i] = -INFINITY;
               }
-            if (nones != 0) {
-              const int per = geo.parts == 1 ? page_size : kBlock;
-              for (uint32_t left = nones; left; left &= left - 1) {
-                const int p0 = (__ffs(left) - 1) * per;
+            const int per = geo.parts == 1 ? page_size : kBlock;
+            for (uint32_t left = nones; left; left &= left - 1) {
+              const int p0 = (__ffs(left) - 1) * per - 64 * hk;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+              for (int c = 0; c < 2; ++c)
 #pragma unroll
-                  for (int i = 0; i < 32; ++i)
-                    if (32 * c + i >= p0 && 32 * c + i < p0 + per) x[c][i] = -INFINITY;
-              }
+                for (int i = 0; i < 32; ++i)
+                  if (32 * c + i >= p0 && 32 * c + i < p0 + per) x[c][i] = -INFINITY;
             }
           }
-          float mb = x[0][0];
+          float mx[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            const float* xp = &x[c >> 1][16 * (c & 1)];
+            mx[c] = xp[0];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) mb = fmaxf(mb, x[c][i]);
+            for (int i = 1; i < 15; i += 2) mx[c] = max3(mx[c], xp[i], xp[i + 1]);
+            mx[c] = fmaxf(mx[c], xp[15]);
+          }
+          // the row's maximum: this thread's keys and its partner's
+          float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          float* rd = red + half * 256 + hrow;
+          rd[128 * hk] = mb;
+          pair_sync(1 + 4 * half + (warp & 3));
+          mb = fmaxf(mb, rd[128 * (1 - hk)]);
           mb *= sc;
           float alpha = 1.f;
           if (mb > m + kSlack) {
@@ -467,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < DP / 16; ++c) {
+            for (int c = hk * (DP / 32); c < (hk + 1) * (DP / 32); ++c) {
               uint32_t r[16];
               tmem_ld16(myO + 16 * c, r);
               tmem_ld_wait();
@@ -478,31 +567,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_wait();
           }
           const float ref = (m == -INFINITY ? 0.f : m) - Pack<T>::kBias;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t p[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float u = ex2(fmaf(x[c][2 * i], sc, -ref)), v = ex2(fmaf(x[c][2 * i + 1], sc, -ref));
-              sum[(2 * i) & 3] += u;
-              sum[(2 * i + 1) & 3] += v;
-              p[i] = Pack<T>::two(u, v);
-            }
-            tmem_st16(myS + 64 + 16 * c, p);
-          }
-          l = l * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
-          tmem_st_wait();
           // Keys that some row of this half does not see: an infinity or a NaN
           // among their values must not meet a weight of zero.  Such values
           // leave the block here, and the rows that see them get them at the
           // end.
-          if (base < run->all_lo[half] || base + rows > run->all_hi[half]) {
+          if (base < all_lo || base + rows > all_hi) {
             const int n = it + 2 * j + 1;
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&full[n % S]), (n / S) & 1, err, kDevTimeoutFull));
             if (!ok) break;
             uint4* v = reinterpret_cast<uint4*>(sR + (n % S) * C::kSlot);
-            for (int i = hrow; i < C::kSlot / 16; i += kHalfRows) {
+            for (int i = hrow + kHalfRows * hk; i < C::kSlot / 16; i += 2 * kHalfRows) {
               const uint4 w = v[i];
               if (odd32<T>(w.x) || odd32<T>(w.y) || odd32<T>(w.z) || odd32<T>(w.w)) {
                 atomicMin(&run->odd_lo, j0 + j);
@@ -515,8 +589,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_proxy_async_smem();
           }
+          const float2 sc2 = make_float2(sc, sc), nr2 = make_float2(-ref, -ref);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float2 e = fma2(make_float2(x[c][2 * i], x[c][2 * i + 1]), sc2, nr2);
+              e.x = ex2(e.x);
+              e.y = ex2(e.y);
+              sum[i & 1] = add2(sum[i & 1], e);
+              p[i] = Pack<T>::two(e.x, e.y);
+            }
+            tmem_st16(myS + 64 + 32 * hk + 16 * c, p);
+          }
+          tmem_st_wait();
           tc_fence_before();
           mbar_arrive(smem_u32(&p_full[half]));
+          sum[0] = add2(sum[0], sum[1]);
+          l = l * alpha + (sum[0].x + sum[0].y);
         }
         if (ok)
           ok = __all_sync(0xffffffffu,
@@ -528,11 +620,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool whole = k0 == 0 && k1 == run->blocks;
           const long long part = 2LL * me + (k0 == 0 ? 1 : 0);
           const float ref = (m == -INFINITY ? 0.f : m) - Pack<T>::kBias;  // what the weights are relative to
+          // the row's sum: both threads' keys
+          float* rd = red + half * 256 + hrow;
+          rd[128 * hk] = l;
+          pair_sync(1 + 4 * half + (warp & 3));
+          l += rd[128 * (1 - hk)];
           const float rl = l == 0.f ? 0.f : 1.f / l;
           const int odd_lo = max(run->odd_lo, j0), odd_hi = min(run->odd_hi, j1 - 1);
           T* dst = mine ? out_row<T>(a, s, h, row0 + row) : nullptr;
 #pragma unroll 1
-          for (int c = 0; c < DP / 16; ++c) {
+          for (int c = hk * (DP / 32); c < (hk + 1) * (DP / 32); ++c) {
             uint32_t r[16];
             __syncwarp();
             tmem_ld16(myO + 16 * c, r);
@@ -578,13 +675,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (mine) {
+          if (mine && hk == 0) {
             if (whole) put_lse(a, s, h, row0 + row, ref, l);
             else ws.ml[part * kTileRows + row] = make_float2(ref, l);
           }
         }
       }
-    } else if (mine) {
+    } else if (mine && hk == 0) {
       // no block of this run holds a key that any row sees
       if (k0 == 0 && k1 == run->blocks) {
         T* dst = out_row<T>(a, s, h, row0 + row);
@@ -629,9 +726,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of the row tile that block `blockIdx.x` left open, in the
-// order of the keys: a thread per row and four channels.
+// order of the keys.  A warp takes 8 rows x 16 channels: 128-byte reads of the
+// parts, 32-byte writes of the rows.
+constexpr int kJoinThreads = 256;
 template <typename T, int DP>
-__global__ void __launch_bounds__(kTileRows) kv_chunk_join_kernel(const __grid_constant__ AttnArgs a, const int G) {
+__global__ void __launch_bounds__(kJoinThreads) kv_chunk_join_kernel(const __grid_constant__ AttnArgs a, const int G) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int me = blockIdx.x;
   const Space ws = space<DP>(a.workspace, G);
@@ -639,9 +738,11 @@ __global__ void __launch_bounds__(kTileRows) kv_chunk_join_kernel(const __grid_c
   if (op.parts == 0) return;
   const Seq s = sequence(a, op.b, false);
   const int row0 = op.rt * kTileRows, cnt = min(kTileRows, s.n * a.group - row0);
-  const int r = threadIdx.x;
-  if (r >= cnt) return;
-  for (int c = blockIdx.y; 4 * c < a.c.D; c += gridDim.y) {
+  const int lane = threadIdx.x & 31;
+  for (int w = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); w < kTileRows / 8 * (DP / 16);
+       w += gridDim.y * (kJoinThreads / 32)) {
+    const int r = w / (DP / 16) * 8 + (lane & 7), c = w % (DP / 16) * 4 + (lane >> 3);
+    if (r >= cnt) continue;
     float m = -INFINITY, l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i = 0; i <= op.parts; ++i) {
@@ -659,11 +760,19 @@ __global__ void __launch_bounds__(kTileRows) kv_chunk_join_kernel(const __grid_c
       m = n;
     }
     const float rl = l == 0.f ? 0.f : 1.f / l;
-    T* dst = out_row<T>(a, s, op.h, row0 + r) + 4 * c;
-    dst[0] = round_to<T>(v.x * rl);
-    dst[1] = round_to<T>(v.y * rl);
-    dst[2] = round_to<T>(v.z * rl);
-    dst[3] = round_to<T>(v.w * rl);
+    if (4 * c < a.c.D) {
+      T* dst = out_row<T>(a, s, op.h, row0 + r) + 4 * c;
+      const uint32_t lo = Pack<T>::two(v.x * rl, v.y * rl), hi = Pack<T>::two(v.z * rl, v.w * rl);
+      if (((uintptr_t)dst & 7) == 0) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+      } else {
+        uint16_t* e = reinterpret_cast<uint16_t*>(dst);
+        e[0] = (uint16_t)lo;
+        e[1] = (uint16_t)(lo >> 16);
+        e[2] = (uint16_t)hi;
+        e[3] = (uint16_t)(hi >> 16);
+      }
+    }
     if (c == 0) put_lse(a, s, op.h, row0 + r, m, l);
   }
 }
@@ -678,8 +787,8 @@ cudaError_t go(const ChunkLaunch& L, int sms, cudaStream_t s) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sms, 8);
-  cfg.blockDim = dim3(kTileRows);
+  cfg.gridDim = dim3(sms, 16);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;

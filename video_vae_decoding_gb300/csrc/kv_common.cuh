@@ -108,10 +108,8 @@ struct Piece {
   __device__ __forceinline__ int holder(long long x) const { return (int)(((x + 1) * live - 1) / total); }
 };
 template <int WARPS, typename F>
-__device__ __forceinline__ Piece cut_line(int B, int me, int G, F of) {
-  __shared__ long long s_scan[WARPS];
-  __shared__ int s_b;
-  __shared__ long long s_at;
+__device__ __forceinline__ Piece cut_line(int B, int me, int G, long long* scratch, F of) {
+  long long *s_scan = scratch + 2, *s_b = scratch, *s_at = scratch + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunk = (B + 32 * WARPS - 1) / (32 * WARPS);
   const int b_lo = min(B, (int)threadIdx.x * chunk), b_hi = min(B, b_lo + chunk);
@@ -148,12 +146,12 @@ __device__ __forceinline__ Piece cut_line(int B, int me, int G, F of) {
       if (at < n) break;
       at -= n;
     }
-    s_b = b;
-    s_at = at;
+    *s_b = b;
+    *s_at = at;
   }
   __syncthreads();
-  p.b = s_b;
-  p.at = s_at;
+  p.b = (int)*s_b;
+  p.at = *s_at;
   return p;
 }
 
