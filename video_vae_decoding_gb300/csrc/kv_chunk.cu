@@ -152,6 +152,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // The two warps whose threads share their rows (named barriers 1-8).
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+// The same, and whether v holds for any of their 64 threads.
+__device__ __forceinline__ bool pair_any(int id, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id)
+      : "memory");
+  return r != 0;
+}
 
 // ------------------------------------------------------------- pages and blocks
 __device__ __forceinline__ int blocks_of(const ChunkGeo& g, int page_size, int len) {
@@ -456,6 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int sk = slot, pk = phase;
           if (more) next();
           ok = mbar_wait_bounded(smem_u32(&full[sv]), pv, err, kDevTimeoutFull);
+          if (more && ok) ok = mbar_wait_bounded(smem_u32(&full[sk]), pk, err, kDevTimeoutFull);
           for (int t = 0; t <= last && ok; ++t) {
             const uint32_t v = vd0 + sv * (C::kSlot >> 4);
             ok = mbar_wait_bounded(smem_u32(&p_full[t]), (ns[t] + j) & 1, err, kDevTimeoutAccum);
@@ -468,14 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               umma_commit(smem_u32(&o_done[t]));
               if (t == last) umma_commit(smem_u32(&empty[sv]));
             }
-            if (more) {
-              if (t == 0) {
-                ok = mbar_wait_bounded(smem_u32(&full[sk]), pk, err, kDevTimeoutFull);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              scores(t, sk, t == last);
-            }
+            if (more) scores(t, sk, t == last);
           }
         }
         ok = __all_sync(0xffffffffu, ok);
@@ -487,7 +494,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sc = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
         const int n0 = ns[half];
         const int all_lo = run->all_lo[half], all_hi = run->all_hi[half];
+        const int pair = 1 + 4 * half + (warp & 3);
+        float* rd = red + half * 256 + hrow;
         float m = -INFINITY, l = 0.f;
+        float ref = -Pack<T>::kBias;  // what the weights are relative to: m, or 0 while it is -inf
         int base, rows, off = 0;  // first key of the block, rows that its pages give it, its place in a long page
         block_keys(geo, page_size, j0, &base, &rows);
         if (geo.parts > 1) off = base % page_size;
@@ -499,18 +509,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               rows = min(kBlock, page_size - off);
             }
           }
-          // columns [c0, c1) are keys of this row
-          const int c0 = max(0, lo - base), c1 = min(rows, hi - base);
+          // this thread's columns [d0, d1) are keys of its row; `part`: not all of them, for some row
+          const int d0 = max(0, lo - base) - 64 * hk, d1 = min(rows, hi - base) - 64 * hk;
+          const bool part = __any_sync(0xffffffffu, d0 > 0 || d1 < 64);
           ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&s_full[half]), (n0 + j) & 1, err, kDevTimeoutAccum));
           if (!ok) break;
           tc_fence_after();
+          const uint32_t nones = hole[(j0 + j) & 15];
           float x[2][32];  // keys 64 hk ..
 #pragma unroll
           for (int c = 0; c < 2; ++c) tmem_ld32(myS + 64 * hk + 32 * c, x[c]);
           tmem_ld_wait();
-          const uint32_t nones = hole[(j0 + j) & 15];
-          const int d0 = c0 - 64 * hk, d1 = c1 - 64 * hk;
-          if (__any_sync(0xffffffffu, d0 > 0 || d1 < 64 || nones != 0)) {
+          if (__builtin_expect(part || nones != 0, 0)) {
             // by groups of 16 columns: most lie inside every row's range, or past a page's end
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -538,40 +548,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 1; i < 15; i += 2) mx[c] = max3(mx[c], xp[i], xp[i + 1]);
             mx[c] = fmaxf(mx[c], xp[15]);
           }
-          // the row's maximum: this thread's keys and its partner's
-          float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          float* rd = red + half * 256 + hrow;
-          rd[128 * hk] = mb;
-          pair_sync(1 + 4 * half + (warp & 3));
-          mb = fmaxf(mb, rd[128 * (1 - hk)]);
-          mb *= sc;
-          float alpha = 1.f;
-          if (mb > m + kSlack) {
-            alpha = weight(m, mb);
-            m = mb;
-          }
-          if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-            ok = __all_sync(0xffffffffu,
-                            mbar_wait_bounded(smem_u32(&o_done[half]), (n0 + j - 1) & 1, err, kDevTimeoutAccum));
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = hk * (DP / 32); c < (hk + 1) * (DP / 32); ++c) {
-              uint32_t r[16];
-              tmem_ld16(myO + 16 * c, r);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-              tmem_st16(myO + 16 * c, r);
+          float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+          // One barrier of the rows' two warps tells whether any row's maximum has
+          // outgrown its reference; if so, the threads of a row agree on the new
+          // one, and O and l are brought down to it.
+          if (__builtin_expect(pair_any(pair, mb > m + kSlack), 0)) {
+            rd[128 * hk] = mb;
+            pair_sync(pair);
+            mb = fmaxf(mb, rd[128 * (1 - hk)]);
+            float alpha = 1.f;
+            if (mb > m + kSlack) {
+              alpha = weight(m, mb);
+              m = mb;
+              ref = (m == -INFINITY ? 0.f : m) - Pack<T>::kBias;
             }
-            tmem_st_wait();
+            l *= alpha;
+            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+              ok = __all_sync(0xffffffffu,
+                              mbar_wait_bounded(smem_u32(&o_done[half]), (n0 + j - 1) & 1, err, kDevTimeoutAccum));
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = hk * (DP / 32); c < (hk + 1) * (DP / 32); ++c) {
+                uint32_t r[16];
+                tmem_ld16(myO + 16 * c, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+                tmem_st16(myO + 16 * c, r);
+              }
+              tmem_st_wait();
+            }
           }
-          const float ref = (m == -INFINITY ? 0.f : m) - Pack<T>::kBias;
           // Keys that some row of this half does not see: an infinity or a NaN
           // among their values must not meet a weight of zero.  Such values
           // leave the block here, and the rows that see them get them at the
           // end.
-          if (base < all_lo || base + rows > all_hi) {
+          if (__builtin_expect(base < all_lo || base + rows > all_hi, 0)) {
             const int n = it + 2 * j + 1;
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&full[n % S]), (n / S) & 1, err, kDevTimeoutFull));
             if (!ok) break;
@@ -608,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           mbar_arrive(smem_u32(&p_full[half]));
           sum[0] = add2(sum[0], sum[1]);
-          l = l * alpha + (sum[0].x + sum[0].y);
+          l += sum[0].x + sum[0].y;
         }
         if (ok)
           ok = __all_sync(0xffffffffu,
@@ -619,11 +632,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const bool whole = k0 == 0 && k1 == run->blocks;
           const long long part = 2LL * me + (k0 == 0 ? 1 : 0);
-          const float ref = (m == -INFINITY ? 0.f : m) - Pack<T>::kBias;  // what the weights are relative to
           // the row's sum: both threads' keys
-          float* rd = red + half * 256 + hrow;
           rd[128 * hk] = l;
-          pair_sync(1 + 4 * half + (warp & 3));
+          pair_sync(pair);
           l += rd[128 * (1 - hk)];
           const float rl = l == 0.f ? 0.f : 1.f / l;
           const int odd_lo = max(run->odd_lo, j0), odd_hi = min(run->odd_hi, j1 - 1);
