@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
 
   // --------------------------------------------- this block's piece of the line
   const Piece pc =
-      cut_line<kWarps>(a.b.B, me, G, s_line, [&](int b) { return tiles_of(a, sequence(a, b, false)).all; });
+      cut_line<kWarps>(a.b.B, me, G, 1, s_line, [&](int b) { return tiles_of(a, sequence(a, b, false)).all; });
   if (threadIdx.x == 0) ws.open[me] = Open{0, 0, 0, 0};
   int b = pc.b;
   long long at = pc.at;

@@ -3,13 +3,25 @@
 //
 // For 256 rows (row r of a sequence and key head h: token r / group, query head
 // h * group + r % group) in two halves of 128, per block of up to 128 keys j:
-//   S_t = Q_t K_j^T          (t = 0, 1: the halves; M = 128, N = 128)
-//   P_t = 2^(scale S_t - m)  two threads per row: running maximum m, moved only
+//   S = Q_t K_j^T            (t = 0, 1: the halves; M = 128, N = 128)
+//   P_t = 2^(scale S - m)    one thread per row: running maximum m, moved only
 //                            when a block exceeds it by 8 (O is then rescaled)
-//   O_t += P_t V_j           P_t read from tensor memory, in the half of S_t's
-//                            columns that its own thread has already read
-// and O_t / l at the end.  While one half's softmax runs, the tensor cores work
-// for the other.  TMEM: S_0, S_1 (128 columns each), O_0, O_1 (DP each).
+//   O_t += P_t V_j           P_t read from tensor memory
+// and O_t / l at the end.  A softmax reads S into registers at once, so that the
+// tensor cores form its next S while it works.  TMEM: S, P_0 and P_1 of 64 columns
+// each, O_0 and O_1 of DP; at DP = 64 each half has an S of its own (128 columns),
+// at 128 there is room for one, which the halves, half a period apart, take in
+// turn.  What else was tried at D = 128, cycles per block of 128 keys and 256 rows
+// (2048 of them products):
+//   S_t for each half with P_t in its place    3100, and P V has to be waited for
+//                                               before the next Q K
+//   64 keys, two S buffers a half              4300: with N = 64 the first operand's
+//                                               way from shared memory, 64 cycles
+//                                               an instruction, bounds Q K
+//   one S, 16 softmax warps                    4000: they starve the issuing warps
+//   this                                       2600
+// A tile of at most 128 rows puts its rows in both halves, which take the key
+// blocks in turn, and adds the halves up at the end.
 //
 // Bound: the tensor cores, 4 D operations per row and key; K and V come through
 // one ring in the order of their use and serve both halves, so a block of 128
@@ -23,7 +35,8 @@
 // zeros (the TMA's fill).
 //
 // The line of (sequence, row tile, head, key block) is cut into equal pieces,
-// one per SM, as in the split kernel; the join adds up what a cut divides.
+// one per SM, as in the split kernel (weighed by what a block costs in a larger
+// and in a smaller tile); the join adds up what a cut divides.
 #include "kv_common.cuh"
 #include "kv_chunk.h"
 
@@ -31,13 +44,12 @@ namespace wan {
 
 namespace {
 
-// Warps 0 loads, 1 MMA, 2 TMEM, 3 idle; 4-11 softmax of half 0, 12-19 of half 1:
-// two threads per row, which share a block's keys (64 each) and the output's
-// channels.
-constexpr int kThreads = 640;
+// Warps 0 loads, 1 issues Q K, 2 issues P V, 3 TMEM; 4-7 softmax of half 0, 8-11 of
+// half 1: a thread per row (TMEM lane).
+constexpr int kThreads = 384;
 constexpr int kHalfRows = 128;
 constexpr int kTileRows = 256;
-constexpr int kBlock = 128;      // key columns of a block
+constexpr int kBlock = 128;       // key columns of a block
 constexpr int kBoxBytes = 16384;  // 128 rows x 64 channels
 constexpr float kSlack = 8.f;    // log2 units that the reference maximum may lag behind
 
@@ -47,7 +59,7 @@ struct Cfg {
   static constexpr int kSlot = ND * kBoxBytes;          // K or V of a block
   static constexpr int kStages = DP == 128 ? 5 : 10;
   static constexpr int kQ = 2 * ND * kBoxBytes;
-  static constexpr int kSmem = kQ + kStages * kSlot + 512 + 2048;
+  static constexpr int kSmem = kQ + kStages * kSlot + 1024 + 1024;
 };
 
 // Weights 2^(x - m) reach 2^kSlack; in float16 they are taken 2^7 times larger
@@ -69,6 +81,46 @@ struct Pack<__half> {
     return *reinterpret_cast<const uint32_t*>(&v);
   }
 };
+
+// mbar_wait_bounded with few instructions per try (the waiting warps share the
+// issue slots with the working ones) and tries counted instead of timed: a try
+// takes about 50 cycles, so 2^26 of them are about two seconds.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* err, int code) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 67108864;\n"
+      "WAIT_%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE_%=;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra WAIT_%=;\n"
+      "DONE_%=:\n\t"
+      "selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  if (__builtin_expect(!done, 0)) {
+    if (err) atomicCAS(err, 0, code);
+    return false;
+  }
+  return true;
+}
+
+// One try.  It takes 100 cycles or more to answer, even if the phase is complete:
+// asked ahead of need, the answer costs nothing.
+__device__ __forceinline__ uint32_t ask_phase(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done;
+}
 
 // kind::f16, fp32 accumulator, operand format 1 (bf16) or 0 (fp16); b_mn: the
 // second operand's N dimension is the contiguous one.
@@ -124,7 +176,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
         "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
       : "r"(taddr));
 }
-
 // Two 32-bit products and sums, or sums, in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -150,21 +201,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// The two warps whose threads share their rows (named barriers 1-8).
-__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
-// The same, and whether v holds for any of their 64 threads.
-__device__ __forceinline__ bool pair_any(int id, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, %2, 64, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)v), "r"(id)
-      : "memory");
-  return r != 0;
-}
+// The 256 softmax threads (named barrier 1).
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // ------------------------------------------------------------- pages and blocks
 __device__ __forceinline__ int blocks_of(const ChunkGeo& g, int page_size, int len) {
@@ -187,14 +225,24 @@ __device__ __forceinline__ void block_keys(const ChunkGeo& g, int page_size, int
   }
 }
 
+// A sequence on the line: `pairs` row tiles of more than 128 rows and perhaps a
+// smaller one behind them, each with every head and block.  A block of the
+// former counts kPairUnits, of the latter kSingleUnits: what they cost.  (A
+// smaller tile does half the arithmetic, but asks for K and V as fast as a
+// larger one would at twice the speed.)
+constexpr int kPairUnits = 5, kSingleUnits = 4;
 struct Tiles {
-  int blocks;
-  long long all;
+  int blocks, pairs;
+  long long of_pairs, all;
 };
 __device__ __forceinline__ Tiles tiles_of(const AttnArgs& a, const ChunkGeo& g, const Seq& s) {
   Tiles t;
   t.blocks = blocks_of(g, a.c.page_size, s.len);
-  t.all = ((long long)s.n * a.group + kTileRows - 1) / kTileRows * a.c.heads * t.blocks;
+  const int rows = s.n * a.group, last = rows % kTileRows;
+  t.pairs = rows / kTileRows + (last > kHalfRows);
+  const long long each = (long long)a.c.heads * t.blocks;
+  t.of_pairs = kPairUnits * each * t.pairs;
+  t.all = t.of_pairs + (last > 0 && last <= kHalfRows ? kSingleUnits * each : 0);
   return t;
 }
 
@@ -212,15 +260,15 @@ __host__ __device__ inline Space space(void* w, int G) {
   return s;
 }
 
-// A run: blocks [j0, j1) of one row tile and head, [k0, k1) of the line's.
-struct Run {
+// A run: blocks [k0, k1) of one row tile and head.
+struct alignas(16) Run {
   Seq s;
   int b, rt, h, row0, cnt;
   int k0, k1, blocks;
-  int lo, hi;          // keys that some row sees
+  int units;                 // what it takes of the line
+  int lo, hi;                // keys that some row sees
   int all_lo[2], all_hi[2];  // per half: keys that every row sees
-  int odd_lo, odd_hi;  // blocks whose values were cleaned (below)
-  int stop;
+  int odd_lo, odd_hi;        // blocks whose values were cleaned (below)
 };
 
 template <typename T, int DP>
@@ -231,26 +279,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int S = C::kStages, ND = C::ND;
   // the only shared memory of the kernel, so it starts on a 1024-byte boundary, as the swizzled boxes must
   extern __shared__ __align__(1024) uint8_t smem[];
-  static_assert(sizeof(Run) + 8 * (2 * S + 9) + 80 <= 512, "barriers and the run's description");
+  static_assert(sizeof(Run) + 8 * (2 * S + 10) + 8 + 128 + 16 <= 1024, "barriers and the run's description");
   uint8_t* sQ = smem;  // [half][64-channel box][128 rows]
   uint8_t* sR = sQ + C::kQ;
   uint64_t* full = reinterpret_cast<uint64_t*>(sR + S * C::kSlot);
   uint64_t* empty = full + S;
-  uint64_t* s_full = empty + S;   // [2] S_t in TMEM
-  uint64_t* p_full = s_full + 2;  // [2] 256 arrivals: P_t in TMEM (S_t read, O_t rescaled)
+  uint64_t* s_full = empty + S;   // [2] a block's S of half t in TMEM
+  uint64_t* s_free = s_full + 2;  // [2] 128 arrivals: it has been read
+  uint64_t* p_full = s_free + 2;  // [2] 128 arrivals: P_t in TMEM (and O_t rescaled)
   uint64_t* o_done = p_full + 2;  // [2] O_t += P_t V_j complete
-  uint64_t* done = o_done + 2;
+  uint64_t* done = o_done + 2;    // [2] all products issued by warp 1, and by warp 2, complete
   if (smem_u32(smem) & 1023) {
     if (a.b.status) atomicCAS(a.b.status, 0, (int)kDevTimeoutFull);
     return;
   }
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 2);
   volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint32_t* hole = tmem_slot + 2;  // [16]: bit i of hole[j % 16]: page i of block j is none of the cache's
-  Run* run = reinterpret_cast<Run*>(hole + 16);
-  // [2 halves][2 key halves][128 rows]: what the two threads of a row tell each other.  One buffer: a block's values
-  // are read before the block's P is complete, and the next block's come after.
-  float* red = reinterpret_cast<float*>(run + 1);
+  uint32_t* hole = tmem_slot + 2;  // [32]: bit i of hole[j % 32]: page i of block j is none of the cache's
+  Run* run = reinterpret_cast<Run*>((reinterpret_cast<uintptr_t>(hole + 32) + 15) & ~uintptr_t(15));
+  float* half_ml = reinterpret_cast<float*>(run + 1);  // [2][128] reference and sum of half 1, handed to half 0
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int G = gridDim.x, me = blockIdx.x;
@@ -265,33 +312,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(&s_full[t]), 1);
-      mbar_init(smem_u32(&p_full[t]), 256);
+      mbar_init(smem_u32(&s_free[t]), 128);
+      mbar_init(smem_u32(&p_full[t]), 128);
+      mbar_init(smem_u32(&done[t]), 1);
       mbar_init(smem_u32(&o_done[t]), 1);
     }
-    mbar_init(smem_u32(done), 1);
     *stop = 0;
     fence_mbar_init();
     tma_prefetch_map(&mapK);
     tma_prefetch_map(&mapV);
   }
   // rows of a slot that no box fills stay zero: their weights are zero, and 0 times a stray NaN would not be
-  for (int i = threadIdx.x; i < S * C::kSlot / 16; i += kThreads)
-    reinterpret_cast<uint4*>(sR)[i] = make_uint4(0, 0, 0, 0);
-  fence_proxy_async_smem();
-  if (warp == 2) {
+  if (geo.pages * geo.box_rows < kBlock) {
+    for (int i = threadIdx.x; i < S * C::kSlot / 16; i += kThreads)
+      reinterpret_cast<uint4*>(sR)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
+  if (warp == 3) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   put_empty<T>(a, me, G);
   const Piece pc =
-      cut_line<kThreads / 32>(a.b.B, me, G, reinterpret_cast<long long*>(red), [&](int b) { return tiles_of(a, geo, sequence(a, b, false)).all; });
+      cut_line<kThreads / 32>(a.b.B, me, G, kPairUnits, reinterpret_cast<long long*>(half_ml),
+                                            [&](int b) { return tiles_of(a, geo, sequence(a, b, false)).all; });
   if (threadIdx.x == 0) ws.open[me] = Open{0, 0, 0, 0};
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tS = tmem, tO = tmem + 256;  // half t: S at tS + 128 t, P in its upper 64 columns, O at tO + DP t
+  constexpr bool kTwoS = DP == 64;  // an S of its own for each half
+  // half t: S at tS (+ 128 t if it has its own), P at tP + 64 t, O at tO + DP t
+  const uint32_t tS = tmem, tP = tmem + (kTwoS ? 256 : 128), tO = tP + 128;
 
   int b = pc.b;
   long long at = pc.at;
@@ -308,7 +361,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         s = sequence(a, ++b, false);
         tl = tiles_of(a, geo, s);
       }
-      const int seg = (int)(at / tl.blocks);
+      const bool pairs = at < tl.of_pairs;
+      const long long in = pairs ? at : at - tl.of_pairs;
+      const int w = pairs ? kPairUnits : kSingleUnits, n = w * tl.blocks;
+      const int seg = (int)(in / n) + (pairs ? 0 : tl.pairs * a.c.heads), u0 = (int)(in % n);
+      const int u1 = (int)min((long long)n, u0 + (pc.end - line));
       run->s = s;
       run->b = b;
       run->rt = seg / a.c.heads;
@@ -316,8 +373,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       run->row0 = run->rt * kTileRows;
       run->cnt = min(kTileRows, s.n * a.group - run->row0);
       run->blocks = tl.blocks;
-      run->k0 = (int)(at - (long long)seg * tl.blocks);
-      run->k1 = (int)min((long long)tl.blocks, run->k0 + (pc.end - line));
+      // a block belongs to the piece that holds its last unit
+      run->k0 = u0 / w;
+      run->k1 = u1 / w;
+      run->units = u1 - u0;
       run->lo = 0x7fffffff;
       run->hi = 0;
       for (int t = 0; t < 2; ++t) {
@@ -326,41 +385,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       run->odd_lo = 0x7fffffff;
       run->odd_hi = -1;
-      at += run->k1 - run->k0;
+      at += u1 - u0;
+      if (run->k0 == 0 && run->k1 > 0 && run->k1 < tl.blocks)
+        ws.open[me] = Open{b, run->rt, run->h, pc.holder(line + n - u0 - 1) - me};
     }
     __syncthreads();
     const int h = run->h, row0 = run->row0, cnt = run->cnt, k0 = run->k0, k1 = run->k1;
     const Seq s = run->s;
-    const bool two = cnt > kHalfRows;
-    // softmax threads: their row's keys, and its q
-    const int half = (warp - 4) >> 3, hk = (warp - 4) >> 2 & 1;  // softmax warps: the half, and the half of its keys
-    const int hrow = 32 * (warp & 3) + lane;                     // the row in its half: its TMEM lane
-    const int row = half * kHalfRows + hrow;
-    const bool mine = warp >= 4 && row < cnt;
+    const bool split = cnt <= kHalfRows;  // both halves hold the same rows and take the blocks in turn
+    const int half = (warp - 4) >> 2;     // softmax warps
+    line += run->units;
+    // softmax threads: the row (TMEM lane) in their half, and the keys that it sees
+    const int hrow = 32 * (warp & 3) + lane;
+    const int row = (split ? 0 : half * kHalfRows) + hrow;
+    const bool real = warp >= 4 && row < cnt;
     int lo = 0, hi = 0x40000000;  // rows past the tile's see everything: they need no mask
-    if (mine) {
-      seen_range(a, s.r0 + (row0 + row) / a.group, s.len, &lo, &hi);
-      if (lo < hi) {
-        atomicMin(&run->lo, lo);
-        atomicMax(&run->hi, hi);
+    if (warp >= 4) {
+      if (real) {
+        seen_range(a, s.r0 + (row0 + row) / a.group, s.len, &lo, &hi);
+        if (lo < hi) {
+          atomicMin(&run->lo, lo);
+          atomicMax(&run->hi, hi);
+        }
+        if (lo > 0) atomicMax(&run->all_lo[half], lo);
+        atomicMin(&run->all_hi[half], hi);
       }
-      if (lo > 0) atomicMax(&run->all_lo[half], lo);
-      atomicMin(&run->all_hi[half], hi);
-    }
-    if (warp >= 4 && (half == 0 || two)) {
       uint8_t* q = sQ + half * ND * kBoxBytes + hrow * 128;
       // q is negated for a negative scale (the maximum is then that of q . k) and cleared for a scale of zero
       // (whose product with a hidden key's -inf is none)
       const bool flip = a.scale_log2 < 0.f;
       const T* src = nullptr;
-      if (mine) {
+      if (real) {
         const int t = (row0 + row) / a.group, g = row0 + row - t * a.group;
         src = (const T*)a.q + (long long)(s.r0 + t) * a.q_t + (long long)(h * a.group + g) * a.q_h;
       }
 #pragma unroll 4
-      for (int c = hk * (DP / 16); c < (hk + 1) * (DP / 16); ++c) {
+      for (int c = 0; c < DP / 8; ++c) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (mine && c * 8 < a.c.D) {
+        if (real && c * 8 < a.c.D) {
           if (((uintptr_t)src & 15) == 0) {
             v = *reinterpret_cast<const uint4*>(src + c * 8);
           } else {
@@ -379,24 +441,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int j0 = run->hi > 0 ? max(k0, block_of_key(geo, page_size, run->lo)) : k1;
     const int j1 = run->hi > 0 ? min(k1, block_of_key(geo, page_size, run->hi - 1) + 1) : k1;
     const int nb = max(0, j1 - j0);
+    // blocks of each half; K leads V by `lead` blocks (one of each half) in the ring: K_0 .. K_{lead-1}, then
+    // K_{n+lead}, V_n in turn
+    const int nh[2] = {split ? (nb + 1) / 2 : nb, split ? nb / 2 : nb};
+    const int lead = min(split ? 2 : 1, nb);
     bool ok = true;
 
-    if (nb > 0) {
-      if (warp == 0) {
-        // ------------------------------------------------------------- loads
-        const int* table = a.b.pages + run->b * a.b.page_stride;
-        const int held = (s.len + page_size - 1) / page_size;  // pages of the sequence
-        const int bytes = geo.parts == 1 ? geo.pages * geo.box_rows * 128 * ND : C::kSlot;
-        int slot = it % S, lap = it / S;
-        for (int j = j0; j < j1 && ok; ++j) {
-          int idx, off = 0;
+    if (warp == 0) {
+      // --------------------------------------------------------------- loads
+      const int* table = a.b.pages + run->b * a.b.page_stride;
+      const int held = (s.len + page_size - 1) / page_size;  // pages of the sequence
+      const int bytes = geo.parts == 1 ? geo.pages * geo.box_rows * 128 * ND : C::kSlot;
+      int slot = it % S, lap = it / S;
+      // one box per lane, of the page that the lane holds
+      auto load = [&](const CUtensorMap* map, int page, int off) {
+        int good = 1;
+        if (lane == 0) {
+          if (lap > 0) good = wait_phase(&empty[slot], (lap - 1) & 1, err, kDevTimeoutEmpty);
+          if (*stop) good = 0;
+          if (good) mbar_arrive_expect_tx(smem_u32(&full[slot]), bytes);
+        }
+        if (!__shfl_sync(0xffffffffu, good, 0)) return false;
+        if (lane < geo.pages) {
+          int c[3];
+          c[geo.dim_row] = off;
+          c[geo.dim_head] = h;
+          c[geo.dim_page] = page;
+          const uint32_t d = smem_u32(sR + slot * C::kSlot) + lane * geo.box_rows * 128;
+#pragma unroll
+          for (int u = 0; u < ND; ++u)
+            tma_load_4d(d + u * kBoxBytes, map, smem_u32(&full[slot]), 64 * u, c[0], c[1], c[2]);
+        }
+        if (++slot == S) slot = 0, ++lap;
+        return true;
+      };
+      int page_q[2] = {0, 0}, off_q[2] = {0, 0};  // pages of the last two blocks: their V is still to come
+      for (int n = 0; n < nb + lead && ok; ++n) {
+        int page = (int)a.c.pages, off = 0;  // past the sequence: past the cache, which reads as zeros
+        if (n < nb) {
+          const int j = j0 + n;
+          int idx;
           if (geo.parts == 1) {
             idx = j * geo.pages + lane;
           } else {
             idx = j / geo.parts;
             off = (j - idx * geo.parts) * kBlock;
           }
-          int page = (int)a.c.pages;  // past the sequence: past the cache, which reads as zeros
           bool none = false;
           if (lane < geo.pages && idx < held) {
             page = table[idx];
@@ -407,309 +497,334 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const uint32_t nones = __ballot_sync(0xffffffffu, none);
-          if (lane == 0) hole[j & 15] = nones;
-          for (int kv = 0; kv < 2 && ok; ++kv) {
-            int good = 1;
-            if (lane == 0) {
-              if (lap > 0) good = mbar_wait_bounded(smem_u32(&empty[slot]), (lap - 1) & 1, err, kDevTimeoutEmpty);
-              if (*stop) good = 0;
-              if (good) mbar_arrive_expect_tx(smem_u32(&full[slot]), bytes);
-            }
-            ok = __shfl_sync(0xffffffffu, good, 0);
-            if (!ok) break;
-            if (lane < geo.pages) {
-              int c[3];
-              c[geo.dim_row] = off;
-              c[geo.dim_head] = h;
-              c[geo.dim_page] = page;
-              const uint32_t d = smem_u32(sR + slot * C::kSlot) + lane * geo.box_rows * 128;
-#pragma unroll
-              for (int u = 0; u < ND; ++u)
-                tma_load_4d(d + u * kBoxBytes, kv ? &mapV : &mapK, smem_u32(&full[slot]), 64 * u, c[0], c[1], c[2]);
-            }
-            if (++slot == S) slot = 0, ++lap;
-          }
+          if (lane == 0) hole[j & 31] = nones;
+          ok = load(&mapK, page, off);
         }
-        if (!ok) *stop = 1;
-      } else if (warp == 1) {
-        // --------------------------------------------------------------- MMAs
-        // The whole warp walks the blocks (what it computes stays in uniform
-        // registers, which the instructions take their operands from); one
-        // thread issues.
+        if (n >= lead && ok) ok = load(&mapV, page_q[lead - 1], off_q[lead - 1]);
+        page_q[1] = page_q[0];
+        off_q[1] = off_q[0];
+        page_q[0] = page;
+        off_q[0] = off;
+      }
+      if (!ok) *stop = 1;
+    } else if ((warp == 1 || warp == 2) && nb > 0) {
+      // ------------------------------------------------- products: Q K, and P V
+      // A whole warp walks the steps (what it computes stays in uniform
+      // registers, which the instructions take their operands from); one thread
+      // issues.  The steps alternate between the halves: step g is half g % 2's
+      // block number g / 2.  The two kinds of product touch nothing in common, so
+      // each warp goes by its own barriers.
+      const int dn = (a.c.D + 15) / 16;  // k steps of S, N / 16 of O
+      const bool one = elect();
+      const int steps = split ? nb : 2 * nb;
+      int slot = it % S, phase = (it / S) & 1;
+      auto move = [&](int d) {
+        slot += d;
+        if (slot >= S) slot -= S, phase ^= 1;
+      };
+      if (warp == 1) {
         const uint32_t idS = idesc(Pack<T>::kFormat, false, kBlock);
-        const int dn = (a.c.D + 15) / 16;  // k steps of S, N / 16 of O
-        const uint32_t idO = idesc(Pack<T>::kFormat, true, 16 * dn);
-        const int last = two ? 1 : 0;
-        const bool one = elect();
-        const uint32_t q0 = desc_k(smem_u32(sQ)), kd0 = desc_k(smem_u32(sR)), vd0 = desc_v(smem_u32(sR));
-        int slot = it % S, phase = (it / S) & 1;
-        auto next = [&] {
-          if (++slot == S) slot = 0, phase ^= 1;
-        };
-        auto scores = [&](int t, int sl, bool done_with_slot) {
-          const uint32_t q = q0 + t * (ND * kBoxBytes >> 4), k = kd0 + sl * (C::kSlot >> 4);
-          if (one) {
-#pragma unroll
-            for (int u = 0; u < 4 * ND; ++u)
-              if (u < dn)
-                umma_ss(tS + kBlock * t, q + (u >> 2) * (kBoxBytes >> 4) + 2 * (u & 3),
-                        k + (u >> 2) * (kBoxBytes >> 4) + 2 * (u & 3), idS, u > 0);
-            umma_commit(smem_u32(&s_full[t]));
-            if (done_with_slot) umma_commit(smem_u32(&empty[sl]));
+        const uint32_t q0 = desc_k(smem_u32(sQ)), kd0 = desc_k(smem_u32(sR));
+        for (int g = 0; g < steps; ++g) {
+          const int t = g & 1, n = split ? g : g >> 1;
+          if (split || t == 0) {  // K of its block: the first `lead` side by side, then every other slot
+            if (n > 0) move(n < lead ? 1 : n == lead ? 1 : 2);
+            ok = wait_phase(&full[slot], phase, err, kDevTimeoutFull);
           }
-        };
-        ok = mbar_wait_bounded(smem_u32(&full[slot]), phase, err, kDevTimeoutFull);
-        tc_fence_after();
-        for (int t = 0; t <= last && ok; ++t) scores(t, slot, t == last);
-        next();
-        for (int j = 0; j < nb && ok; ++j) {
-          const int sv = slot, pv = phase;
-          next();
-          const bool more = j + 1 < nb;
-          const int sk = slot, pk = phase;
-          if (more) next();
-          ok = mbar_wait_bounded(smem_u32(&full[sv]), pv, err, kDevTimeoutFull);
-          if (more && ok) ok = mbar_wait_bounded(smem_u32(&full[sk]), pk, err, kDevTimeoutFull);
-          for (int t = 0; t <= last && ok; ++t) {
-            const uint32_t v = vd0 + sv * (C::kSlot >> 4);
-            ok = mbar_wait_bounded(smem_u32(&p_full[t]), (ns[t] + j) & 1, err, kDevTimeoutAccum);
-            if (!ok) break;
-            tc_fence_after();
-            if (one) {
-#pragma unroll
-              for (int u = 0; u < kBlock / 16; ++u)
-                umma_ts(tO + DP * t, tS + kBlock * t + 64 + 8 * u, v + 128 * u, idO, j > 0 || u > 0);
-              umma_commit(smem_u32(&o_done[t]));
-              if (t == last) umma_commit(smem_u32(&empty[sv]));
-            }
-            if (more) scores(t, sk, t == last);
+          // the S buffer, once the step that used it last (the half's own, or the other's) has been read
+          if (kTwoS) {
+            if (g > 1 && ok) ok = wait_phase(&s_free[t], (ns[t] + (g >> 1) - 1) & 1, err, kDevTimeoutAccum);
+          } else {
+            if (g > 0 && ok) ok = wait_phase(&s_free[t ^ 1], (ns[t ^ 1] + ((g - 1) >> 1)) & 1, err, kDevTimeoutAccum);
           }
-        }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) *stop = 1;
-      } else if (warp >= 4 && (half == 0 || two)) {
-        // ------------------------------------------------------ softmax, output
-        const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t myS = tS + kBlock * half + lane_off, myO = tO + DP * half + lane_off;
-        const float sc = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
-        const int n0 = ns[half];
-        const int all_lo = run->all_lo[half], all_hi = run->all_hi[half];
-        const int pair = 1 + 4 * half + (warp & 3);
-        float* rd = red + half * 256 + hrow;
-        float m = -INFINITY, l = 0.f;
-        float ref = -Pack<T>::kBias;  // what the weights are relative to: m, or 0 while it is -inf
-        int base, rows, off = 0;  // first key of the block, rows that its pages give it, its place in a long page
-        block_keys(geo, page_size, j0, &base, &rows);
-        if (geo.parts > 1) off = base % page_size;
-        for (int j = 0; j < nb; ++j) {
-          if (j > 0) {  // the next block: the next pages, or the next part of one
-            base += rows;
-            if (geo.parts > 1) {
-              off = off + kBlock < page_size ? off + kBlock : 0;
-              rows = min(kBlock, page_size - off);
-            }
-          }
-          // this thread's columns [d0, d1) are keys of its row; `part`: not all of them, for some row
-          const int d0 = max(0, lo - base) - 64 * hk, d1 = min(rows, hi - base) - 64 * hk;
-          const bool part = __any_sync(0xffffffffu, d0 > 0 || d1 < 64);
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&s_full[half]), (n0 + j) & 1, err, kDevTimeoutAccum));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t nones = hole[(j0 + j) & 15];
-          float x[2][32];  // keys 64 hk ..
+          const uint32_t q = q0 + t * (ND * kBoxBytes >> 4), k = kd0 + slot * (C::kSlot >> 4);
+          if (one) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) tmem_ld32(myS + 64 * hk + 32 * c, x[c]);
-          tmem_ld_wait();
-          if (__builtin_expect(part || nones != 0, 0)) {
-            // by groups of 16 columns: most lie inside every row's range, or past a page's end
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (__any_sync(0xffffffffu, d0 > 16 * q || d1 < 16 * q + 16)) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  if (16 * q + i < d0 || 16 * q + i >= d1) x[q >> 1][16 * (q & 1) + i] = -INFINITY;
-              }
-            const int per = geo.parts == 1 ? page_size : kBlock;
-            for (uint32_t left = nones; left; left &= left - 1) {
-              const int p0 = (__ffs(left) - 1) * per - 64 * hk;
-#pragma unroll
-              for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (32 * c + i >= p0 && 32 * c + i < p0 + per) x[c][i] = -INFINITY;
-            }
+            for (int e = 0; e < 4 * ND; ++e)
+              if (e < dn)
+                umma_ss(tS + (kTwoS ? 128 * t : 0), q + (e >> 2) * (kBoxBytes >> 4) + 2 * (e & 3), k + (e >> 2) * (kBoxBytes >> 4) + 2 * (e & 3),
+                        idS, e > 0);
+            umma_commit(smem_u32(&s_full[t]));
+            if (split || t == 1) umma_commit(smem_u32(&empty[slot]));
           }
-          float mx[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float* xp = &x[c >> 1][16 * (c & 1)];
-            mx[c] = xp[0];
-#pragma unroll
-            for (int i = 1; i < 15; i += 2) mx[c] = max3(mx[c], xp[i], xp[i + 1]);
-            mx[c] = fmaxf(mx[c], xp[15]);
+        }
+      } else {
+        const uint32_t idO = idesc(Pack<T>::kFormat, true, 16 * dn);
+        const uint32_t vd0 = desc_v(smem_u32(sR));
+        move(lead);
+        for (int g = 0; g < steps; ++g) {
+          const int t = g & 1, n = split ? g : g >> 1;
+          if (split || t == 0) {  // V of its block, behind K of the block `lead` further on
+            move((n > 0 ? 1 : 0) + (n + lead < nb ? 1 : 0));
+            ok = wait_phase(&full[slot], phase, err, kDevTimeoutFull);
           }
-          float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-          // One barrier of the rows' two warps tells whether any row's maximum has
-          // outgrown its reference; if so, the threads of a row agree on the new
-          // one, and O and l are brought down to it.
-          if (__builtin_expect(pair_any(pair, mb > m + kSlack), 0)) {
-            rd[128 * hk] = mb;
-            pair_sync(pair);
-            mb = fmaxf(mb, rd[128 * (1 - hk)]);
-            float alpha = 1.f;
-            if (mb > m + kSlack) {
-              alpha = weight(m, mb);
-              m = mb;
-              ref = (m == -INFINITY ? 0.f : m) - Pack<T>::kBias;
-            }
-            l *= alpha;
-            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-              ok = __all_sync(0xffffffffu,
-                              mbar_wait_bounded(smem_u32(&o_done[half]), (n0 + j - 1) & 1, err, kDevTimeoutAccum));
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int c = hk * (DP / 32); c < (hk + 1) * (DP / 32); ++c) {
-                uint32_t r[16];
-                tmem_ld16(myO + 16 * c, r);
-                tmem_ld_wait();
+          if (ok) ok = wait_phase(&p_full[t], (ns[t] + (g >> 1)) & 1, err, kDevTimeoutAccum);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t v = vd0 + slot * (C::kSlot >> 4), p = tP + 64 * t;
+          if (one) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-                tmem_st16(myO + 16 * c, r);
-              }
-              tmem_st_wait();
+            for (int e = 0; e < kBlock / 16; ++e) umma_ts(tO + DP * t, p + 8 * e, v + 128 * e, idO, g > 1 || e > 0);
+            umma_commit(smem_u32(&o_done[t]));
+            if (split || t == 1) umma_commit(smem_u32(&empty[slot]));
+          }
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) *stop = 1;
+    } else if (warp >= 4 && k0 < k1) {
+      // -------------------------------------------------------- softmax, output
+      const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+      const uint32_t myS = tS + (kTwoS ? 128 * half : 0) + lane_off, myP = tP + 64 * half + lane_off, myO = tO + DP * half + lane_off;
+      const float sc = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
+      const int n0 = ns[half], mine = nh[half], step = split ? 2 : 1;
+      const int all_lo = run->all_lo[half], all_hi = run->all_hi[half];
+      float m = -INFINITY, l = 0.f;
+      float ref = -Pack<T>::kBias;  // what the weights are relative to: m, or 0 while it is -inf
+      // Blocks [plain_lo, plain_hi) hold keys that all rows of this half see in all
+      // their columns, but for the last part of a long page: `behind` parts come
+      // after the block in its page.
+      int plain_lo = 0x7fffffff, plain_hi = 0, behind = 1;
+      const bool tails = geo.parts > 1 ? page_size % kBlock != 0 : geo.pages * page_size != kBlock;
+      if (mine > 0 && !(geo.parts == 1 && tails)) {
+        plain_lo = all_lo > 0 ? block_of_key(geo, page_size, all_lo - 1) + 1 : 0;
+        plain_hi = block_of_key(geo, page_size, min(all_hi, s.len));
+      }
+      if (tails) behind = geo.parts - 1 - (j0 + (split ? half : 0)) % geo.parts;
+      uint32_t s_there = 0;  // S of block i is known to be there
+      for (int i = 0; i < mine; ++i) {
+        const int j = j0 + (split ? 2 * i + half : i);
+        const bool plain = j >= plain_lo && j < plain_hi && behind != 0;
+        if (tails && geo.parts > 1) behind = behind >= step ? behind - step : behind - step + geo.parts;
+        if (!__all_sync(0xffffffffu, s_there)) ok = wait_phase(&s_full[half], (n0 + i) & 1, err, kDevTimeoutAccum);
+        __syncwarp();
+        tc_fence_after();
+        const uint32_t nones = hole[j & 31];
+        float x[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(myS + 32 * c, x[c]);
+        // P's room, and O: free once O += P V of the block before is complete
+        const uint32_t o_there = i > 0 ? ask_phase(&o_done[half], (n0 + i - 1) & 1) : 1u;
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&s_free[half]));
+        if (__builtin_expect(!plain || nones != 0, 0)) {
+          int base, rows;
+          block_keys(geo, page_size, j, &base, &rows);
+          const int d0 = lo - base, d1 = min(rows, hi - base);  // columns [d0, d1) are keys of this row
+          // by groups of 16 columns, if some row of this half does not see them all
+          const int u0 = all_lo - base, u1 = min(rows, all_hi - base);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (u0 > 16 * q || u1 < 16 * q + 16) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (16 * q + e < d0 || 16 * q + e >= d1) x[q >> 1][16 * (q & 1) + e] = -INFINITY;
             }
+          const int per = geo.parts == 1 ? page_size : kBlock;
+          for (uint32_t left = nones; left; left &= left - 1) {
+            const int p0 = (__ffs(left) - 1) * per;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (32 * c + e >= p0 && 32 * c + e < p0 + per) x[c][e] = -INFINITY;
           }
           // Keys that some row of this half does not see: an infinity or a NaN
-          // among their values must not meet a weight of zero.  Such values
-          // leave the block here, and the rows that see them get them at the
-          // end.
-          if (__builtin_expect(base < all_lo || base + rows > all_hi, 0)) {
-            const int n = it + 2 * j + 1;
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&full[n % S]), (n / S) & 1, err, kDevTimeoutFull));
+          // among their values must not meet a weight of zero.  Such values leave
+          // the block here, and the rows that see them get them at the end.
+          if (base < all_lo || base + rows > all_hi) {
+            const int n = j - j0, at_v = it + lead + n + min(n + 1, nb - lead);  // V_n's place in the ring
+            ok = __all_sync(0xffffffffu, wait_phase(&full[at_v % S], (at_v / S) & 1, err, kDevTimeoutFull));
             if (!ok) break;
-            uint4* v = reinterpret_cast<uint4*>(sR + (n % S) * C::kSlot);
-            for (int i = hrow + kHalfRows * hk; i < C::kSlot / 16; i += 2 * kHalfRows) {
-              const uint4 w = v[i];
+            uint4* v = reinterpret_cast<uint4*>(sR + (at_v % S) * C::kSlot);
+            for (int e = hrow; e < C::kSlot / 16; e += kHalfRows) {
+              const uint4 w = v[e];
               if (odd32<T>(w.x) || odd32<T>(w.y) || odd32<T>(w.z) || odd32<T>(w.w)) {
-                atomicMin(&run->odd_lo, j0 + j);
-                atomicMax(&run->odd_hi, j0 + j);
+                atomicMin(&run->odd_lo, j);
+                atomicMax(&run->odd_hi, j);
                 __threadfence_block();
-                uint16_t* e = reinterpret_cast<uint16_t*>(v + i);
+                uint16_t* u = reinterpret_cast<uint16_t*>(v + e);
                 for (int k = 0; k < 8; ++k)
-                  if (odd16<T>(e[k])) e[k] = 0;
+                  if (odd16<T>(u[k])) u[k] = 0;
               }
             }
             fence_proxy_async_smem();
           }
-          const float2 sc2 = make_float2(sc, sc), nr2 = make_float2(-ref, -ref);
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t p[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float2 e = fma2(make_float2(x[c][2 * i], x[c][2 * i + 1]), sc2, nr2);
-              e.x = ex2(e.x);
-              e.y = ex2(e.y);
-              sum[i & 1] = add2(sum[i & 1], e);
-              p[i] = Pack<T>::two(e.x, e.y);
-            }
-            tmem_st16(myS + 64 + 32 * hk + 16 * c, p);
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(smem_u32(&p_full[half]));
-          sum[0] = add2(sum[0], sum[1]);
-          l += sum[0].x + sum[0].y;
         }
-        if (ok)
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait_bounded(smem_u32(&o_done[half]), (n0 + nb - 1) & 1, err, kDevTimeoutAccum));
-        if (!ok) {
-          *stop = 1;
-        } else {
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = x[c][0];
+#pragma unroll
+          for (int e = 1; e < 31; e += 2) mx[c] = max3(mx[c], x[c][e], x[c][e + 1]);
+          mx[c] = fmaxf(mx[c], x[c][31]);
+        }
+        const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        if (__builtin_expect(__any_sync(0xffffffffu, mb > m + kSlack || !o_there || !ok), 0)) {
+          if (ok && i > 0) ok = wait_phase(&o_done[half], (n0 + i - 1) & 1, err, kDevTimeoutAccum);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           tc_fence_after();
-          const bool whole = k0 == 0 && k1 == run->blocks;
-          const long long part = 2LL * me + (k0 == 0 ? 1 : 0);
-          // the row's sum: both threads' keys
-          rd[128 * hk] = l;
-          pair_sync(pair);
-          l += rd[128 * (1 - hk)];
-          const float rl = l == 0.f ? 0.f : 1.f / l;
-          const int odd_lo = max(run->odd_lo, j0), odd_hi = min(run->odd_hi, j1 - 1);
-          T* dst = mine ? out_row<T>(a, s, h, row0 + row) : nullptr;
+          float alpha = 1.f;
+          if (mb > m + kSlack) {
+            alpha = weight(m, mb);
+            m = mb;
+            ref = m - Pack<T>::kBias;
+          }
+          l *= alpha;
+          if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
-          for (int c = hk * (DP / 32); c < (hk + 1) * (DP / 32); ++c) {
+            for (int c = 0; c < DP / 16; ++c) {
+              uint32_t r[16];
+              tmem_ld16(myO + 16 * c, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+              tmem_st16(myO + 16 * c, r);
+            }
+            tmem_st_wait();
+          }
+        }
+        const float2 sc2 = make_float2(sc, sc), nr2 = make_float2(-ref, -ref);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t p[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float2 e = fma2(make_float2(x[c][2 * k], x[c][2 * k + 1]), sc2, nr2);
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            sum[k & 1] = add2(sum[k & 1], e);
+            p[k] = Pack<T>::two(e.x, e.y);
+          }
+          tmem_st16(myP + 16 * c, p);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&p_full[half]));
+        s_there = ask_phase(&s_full[half], (n0 + i + 1) & 1);
+        sum[0] = add2(sum[0], sum[1]);
+        l += sum[0].x + sum[0].y;
+      }
+      if (ok && mine > 0)
+        ok = __all_sync(0xffffffffu,
+                        wait_phase(&o_done[half], (n0 + mine - 1) & 1, err, kDevTimeoutAccum));
+      if (!ok) *stop = 1;
+      tc_fence_after();
+      const bool whole = k0 == 0 && k1 == run->blocks;
+      const long long part = 2LL * me + (k0 == 0 ? 1 : 0);
+      // Both halves' rows are the same: half 1 hands its sums to half 0, through
+      // the room of q (which no MMA needs any more).
+      float4* const other = reinterpret_cast<float4*>(sQ);  // [DP / 4][128 rows]
+      float f0 = 1.f, f1 = 0.f;                             // weights of the halves' sums
+      if (split) {
+        softmax_sync();
+        if (half == 1) {
+          half_ml[hrow] = ref;
+          half_ml[kHalfRows + hrow] = l;
+#pragma unroll 1
+          for (int c = 0; c < DP / 16 && mine > 0; ++c) {
             uint32_t r[16];
-            __syncwarp();
             tmem_ld16(myO + 16 * c, r);
             tmem_ld_wait();
-            float v[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = 16 * c < a.c.D ? __uint_as_float(r[i]) : 0.f;
-            if (odd_lo <= odd_hi && mine) {
-              const int* table = a.b.pages + run->b * a.b.page_stride;
-              int k_lo, k_hi, rows;
-              block_keys(geo, page_size, odd_lo, &k_lo, &rows);
-              block_keys(geo, page_size, odd_hi, &k_hi, &rows);
-              k_hi += rows;
-              for (int k = max(lo, k_lo); k < min(hi, k_hi); ++k) {
-                const int page = kv_page(table, k, page_size, a.c.pages);
-                if (page < 0) continue;
-                const T* src = (const T*)a.c.v + page * a.c.v_page + h * a.c.v_head + (k % page_size) * a.c.v_row;
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  if (16 * c + i < a.c.D && odd16<T>(reinterpret_cast<const uint16_t*>(src)[16 * c + i]))
-                    v[i] += val<T>(src[16 * c + i]);
-              }
-            }
-            if (mine && !whole) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                ws.o[(part * (DP / 4) + 4 * c + i) * kTileRows + row] =
-                    make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            } else if (mine) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] *= rl;
-              uint32_t w[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) w[i] = Pack<T>::two(v[2 * i], v[2 * i + 1]);
-              const int left = a.c.D - 16 * c;
-              if (((uintptr_t)dst & 15) == 0) {
-                if (left >= 8) *reinterpret_cast<uint4*>(dst + 16 * c) = make_uint4(w[0], w[1], w[2], w[3]);
-                if (left >= 16) *reinterpret_cast<uint4*>(dst + 16 * c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  if (i < left) reinterpret_cast<uint16_t*>(dst)[16 * c + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
-              }
-            }
+            for (int e = 0; e < 4; ++e)
+              other[(4 * c + e) * kHalfRows + hrow] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
+                                                                 __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
           }
-          if (mine && hk == 0) {
-            if (whole) put_lse(a, s, h, row0 + row, ref, l);
-            else ws.ml[part * kTileRows + row] = make_float2(ref, l);
+        }
+        softmax_sync();
+        if (half == 0 && nh[1] > 0 && half_ml[kHalfRows + hrow] != 0.f) {
+          const float r1 = half_ml[hrow], l1 = half_ml[kHalfRows + hrow];
+          if (l == 0.f) {
+            f0 = 0.f;
+            f1 = 1.f;
+            ref = r1;
+            l = l1;
+          } else {
+            const float to = fmaxf(ref, r1);
+            f0 = weight(ref, to);
+            f1 = weight(r1, to);
+            l = l * f0 + l1 * f1;
+            ref = to;
           }
         }
       }
-    } else if (mine && hk == 0) {
-      // no block of this run holds a key that any row sees
-      if (k0 == 0 && k1 == run->blocks) {
-        T* dst = out_row<T>(a, s, h, row0 + row);
-        for (int c = 0; c < a.c.D; ++c) dst[c] = round_to<T>(0.f);
-        put_lse(a, s, h, row0 + row, 0.f, 0.f);
-      } else {
-        const long long part = 2LL * me + (k0 == 0 ? 1 : 0);
-        for (int c = 0; c < DP / 4; ++c) ws.o[(part * (DP / 4) + c) * kTileRows + row] = make_float4(0.f, 0.f, 0.f, 0.f);
-        ws.ml[part * kTileRows + row] = make_float2(0.f, 0.f);
+      if (!split || half == 0) {
+        const float rl = l == 0.f ? 0.f : 1.f / l;
+        const int odd_lo = max(run->odd_lo, j0), odd_hi = min(run->odd_hi, j1 - 1);
+        T* dst = real ? out_row<T>(a, s, h, row0 + row) : nullptr;
+#pragma unroll 1
+        for (int c = 0; c < DP / 16; ++c) {
+          uint32_t r[16];
+          __syncwarp();
+          tmem_ld16(myO + 16 * c, r);
+          tmem_ld_wait();
+          float v[16];
+          // (what TMEM holds for a row that saw nothing, or a channel past D, is nobody's)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = mine > 0 && l != 0.f && 16 * c < a.c.D && f0 != 0.f ? __uint_as_float(r[e]) * f0 : 0.f;
+          if (f1 != 0.f) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 o = other[(4 * c + e) * kHalfRows + hrow];
+              if (16 * c < a.c.D) {
+                v[4 * e] += o.x * f1;
+                v[4 * e + 1] += o.y * f1;
+                v[4 * e + 2] += o.z * f1;
+                v[4 * e + 3] += o.w * f1;
+              }
+            }
+          }
+          if (__builtin_expect(odd_lo <= odd_hi && real, 0)) {
+            const int* table = a.b.pages + run->b * a.b.page_stride;
+            int k_lo, k_hi, kr;
+            block_keys(geo, page_size, odd_lo, &k_lo, &kr);
+            block_keys(geo, page_size, odd_hi, &k_hi, &kr);
+            k_hi += kr;
+            for (int k = max(lo, k_lo); k < min(hi, k_hi); ++k) {
+              const int page = kv_page(table, k, page_size, a.c.pages);
+              if (page < 0) continue;
+              const T* src = (const T*)a.c.v + page * a.c.v_page + h * a.c.v_head + (k % page_size) * a.c.v_row;
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (16 * c + e < a.c.D && odd16<T>(reinterpret_cast<const uint16_t*>(src)[16 * c + e]))
+                  v[e] += val<T>(src[16 * c + e]);
+            }
+          }
+          if (real && !whole) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              ws.o[(part * (DP / 4) + 4 * c + e) * kTileRows + row] =
+                  make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          } else if (real) {
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = Pack<T>::two(v[2 * e] * rl, v[2 * e + 1] * rl);
+            const int left = a.c.D - 16 * c;
+            if (((uintptr_t)dst & 15) == 0) {
+              if (left >= 8) *reinterpret_cast<uint4*>(dst + 16 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+              if (left >= 16) *reinterpret_cast<uint4*>(dst + 16 * c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (e < left) reinterpret_cast<uint16_t*>(dst)[16 * c + e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+            }
+          }
+        }
+        if (real) {
+          if (whole) put_lse(a, s, h, row0 + row, ref, l);
+          else ws.ml[part * kTileRows + row] = make_float2(ref, l);
+        }
       }
     }
-    if (threadIdx.x == 0 && k0 == 0 && k1 < run->blocks)
-      ws.open[me] = Open{run->b, run->rt, h, pc.holder(line + run->blocks - 1) - me};
     it += 2 * nb;
-    ns[0] += nb;
-    if (two) ns[1] += nb;
-    line += k1 - k0;
+    ns[0] += nh[0];
+    ns[1] += nh[1];
     // TMEM reads of this run come before the next run's MMAs
     tc_fence_before();
     __syncthreads();
@@ -724,13 +839,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_bounded(smem_u32(&full[s]), 1, err, kDevTimeoutFull, 20000000);
     }
   }
-  if (warp == 1 && lane == 0) {
-    umma_commit(smem_u32(done));
-    mbar_wait_bounded(smem_u32(done), 0, err, kDevTimeoutAccum);
+  if ((warp == 1 || warp == 2) && lane == 0) {
+    umma_commit(smem_u32(&done[warp - 1]));
+    mbar_wait_bounded(smem_u32(&done[warp - 1]), 0, err, kDevTimeoutAccum);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 2) {
+  if (warp == 3) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -752,7 +867,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_chunk_join_kernel(const __gri
   const int lane = threadIdx.x & 31;
   for (int w = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); w < kTileRows / 8 * (DP / 16);
        w += gridDim.y * (kJoinThreads / 32)) {
-    const int r = w / (DP / 16) * 8 + (lane & 7), c = w % (DP / 16) * 4 + (lane >> 3);
+    const int r = w / (DP / 16) * 8 + (lane & 7), c = w % (DP / 16) * 4 + (lane >> 3);  // row, four channels
     if (r >= cnt) continue;
     float m = -INFINITY, l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);

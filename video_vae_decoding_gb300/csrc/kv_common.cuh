@@ -97,7 +97,7 @@ __device__ __forceinline__ void put_empty(const AttnArgs& a, int me, int G) {
 }
 
 // A call's tiles form one line, sequence after sequence; block `me` of `G` takes
-// an equal piece of it.  All threads call this; `of(b)` counts the tiles of
+// an equal piece of it, of `least` tiles or more.  All threads call this; `of(b)` counts the tiles of
 // sequence b.
 struct Piece {
   long long beg, end;  // tiles of the line (empty: beg == end)
@@ -108,7 +108,7 @@ struct Piece {
   __device__ __forceinline__ int holder(long long x) const { return (int)(((x + 1) * live - 1) / total); }
 };
 template <int WARPS, typename F>
-__device__ __forceinline__ Piece cut_line(int B, int me, int G, long long* scratch, F of) {
+__device__ __forceinline__ Piece cut_line(int B, int me, int G, int least, long long* scratch, F of) {
   long long *s_scan = scratch + 2, *s_b = scratch, *s_at = scratch + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunk = (B + 32 * WARPS - 1) / (32 * WARPS);
@@ -131,7 +131,7 @@ __device__ __forceinline__ Piece cut_line(int B, int me, int G, long long* scrat
     if (w < warp) before += s_scan[w];
     p.total += s_scan[w];
   }
-  p.live = p.total < G ? p.total : G;  // one tile or more each
+  p.live = min((long long)G, max(p.total / least, p.total > 0 ? 1LL : 0LL));
   p.beg = p.end = 0;
   p.b = 0;
   p.at = 0;
