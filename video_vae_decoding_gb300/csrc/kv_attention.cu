@@ -8,19 +8,24 @@
 // Bound: memory.  Every key and value is read once for up to 16 rows, 4 D
 // bytes against 4 D operations a row, far below the tensor cores' rate; so
 // mma.sync on fragments fetched by ldmatrix is enough, and what matters is
-// that loads never wait for arithmetic:
-//  - a warp owns 16 keys of each tile and a ring of its own (cp.async, kStages
-//    deep), so warps never wait for one another inside a run;
-//  - the whole call's tiles (sequence x row tile x head x key tile) are one
-//    line that is cut into equal pieces, one per resident block, on the device
-//    from the lengths themselves: any raggedness gives every SM the same
-//    bytes, a captured graph follows its lengths, and one long sequence is
-//    spread over the whole card;
+// that loads never wait for arithmetic, nor a warp for another:
+//  - a warp has a ring of its own (cp.async, kStages deep, 16 keys a stage) and
+//    works alone: while one starts or ends a row tile, the others of its SM keep
+//    the memory busy;
+//  - the whole call's tiles (sequence x row tile x head x 16 keys) are one line
+//    that is cut into equal pieces, one per resident warp, on the device from the
+//    lengths themselves: any raggedness gives every warp the same bytes, a
+//    captured graph follows its lengths, and one long sequence is spread over
+//    the whole card;
 //  - a row tile that a cut divides leaves partial (m, l, o) in the workspace,
 //    and a second kernel, launched to start as the first drains, joins them in
 //    the order of the keys: the result does not depend on timing.
+// (With a block's four warps on one row tile, merged through shared memory at its
+// end, a batch of 64 ragged sequences took 182 us instead of HEADBATCH.)
 // Sums, maxima and outputs are held in 32 bits; how the weights are rounded is
 // told at Weights.
+#include <algorithm>
+
 #include "kv_common.cuh"
 
 namespace wan {
@@ -29,18 +34,21 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRows = 16;            // rows of a tile: the MMA's M
-constexpr int kWarpKeys = 16;        // keys per warp and tile
-constexpr int kKeys = kWarps * kWarpKeys;
+constexpr int kRows = 16;    // rows of a tile: the MMA's M
+constexpr int kKeys = 16;    // keys of a tile
+constexpr int kLeast = 2;    // tiles of a piece: fewer parts to join, and as many loads as a ring holds in flight
 
 template <int DP>
 struct Cfg {
   static constexpr int CH = DP / 8;                     // 16-byte chunks per row
-  static constexpr int kStages = DP == 64 ? 6 : 3;
+  static constexpr int kStages = DP == 64 ? 6 : DP == 128 ? 3 : 2;
   static constexpr int kCtas = DP == 256 ? 1 : 2;       // resident blocks per SM
-  static constexpr int kHalf = kWarpKeys * DP * 2;      // bytes of K (or V) per warp and stage
+  static constexpr int kHalf = kKeys * DP * 2;          // bytes of K (or V) per stage
   static constexpr int kRing = kStages * 2 * kHalf;     // bytes per warp
-  static constexpr int kSmem = kWarps * kRing + kRows * DP * 2;
+  static constexpr bool kQRegs = DP <= 128;             // q fragments in registers; at 256 channels they are fetched again
+  static constexpr int kQ = kRows * DP * 2;             // q, and then (or behind it) a tile's weights on a rare path
+  static constexpr int kWarp = kRing + kQ + (kQRegs ? 0 : kRows * kKeys * 4);
+  static constexpr int kSmem = kWarps * kWarp;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
@@ -128,7 +136,7 @@ __device__ __forceinline__ Tiles tiles_of(const AttnArgs& a, const Seq& s) {
   return t;
 }
 
-struct Space {  // the workspace: per block an Open and two parts (0: a row tile's later keys, 1: its first ones)
+struct Space {  // the workspace: per piece an Open and two parts (0: a row tile's later keys, 1: its first ones)
   Open* open;
   float2* ml;  // [2 G][kRows]: running max (log2 units) and sum
   float* o;    // [2 G][kRows][DP]
@@ -150,29 +158,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
     kv_split_kernel(const __grid_constant__ AttnArgs a) {
   using C = Cfg<DP>;
   constexpr int CH = C::CH, ST = C::kStages, NK = DP / 16;
-  constexpr bool kQRegs = DP <= 128;  // q fragments in registers; at 256 channels they are fetched again
+  constexpr bool kQRegs = C::kQRegs;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t s_seen[kWarps][ST];
-  __shared__ long long s_line[kWarps + 2];
-  __shared__ float2 s_ml[kWarps][kRows];
-  __shared__ float s_p[kWarps][kRows][kWarpKeys];
+  __shared__ long long s_line[3 * kWarps];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = gridDim.x, me = blockIdx.x;
-  uint8_t* ring = smem + warp * C::kRing;
-  uint8_t* sq = smem + kWarps * C::kRing;
+  const int me = blockIdx.x * kWarps + warp;  // the piece
+  uint8_t* ring = smem + warp * C::kWarp;
+  uint8_t* sq = ring + C::kRing;
+  float* s_p = reinterpret_cast<float*>(kQRegs ? sq : sq + C::kQ);  // [kRows][kKeys]
   const uint32_t ring_a = smem_u32(ring), sq_a = smem_u32(sq);
-  const Space ws = space<DP>(a.workspace, G);
+  const Space ws = space<DP>(a.workspace, gridDim.x * kWarps);
 
   // the join's blocks may start as soon as every block of this grid runs
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  put_empty<T>(a, me, G);
-
-  // --------------------------------------------- this block's piece of the line
-  const Piece pc =
-      cut_line<kWarps>(a.b.B, me, G, 1, s_line, [&](int b) { return tiles_of(a, sequence(a, b, false)).all; });
-  if (threadIdx.x == 0) ws.open[me] = Open{0, 0, 0, 0};
+  const Piece pc = cut_line<kWarps, kWarps>(a.b.B, kLeast, s_line,
+                                            [&](int b) { return tiles_of(a, sequence(a, b, false)).all; });
+  if (lane == 0) ws.open[me].parts = 0;
   int b = pc.b;
   long long at = pc.at;
   const T* kbase = (const T*)a.c.k;
@@ -187,95 +191,56 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
       tl = tiles_of(a, s);
     }
     // the run: key tiles [kt0, kt1) of one row tile and head
-    const int seg = (int)(at / tl.key_tiles), kt0 = (int)(at - (long long)seg * tl.key_tiles);
+    const int seg = (int)quotient(at, tl.key_tiles), kt0 = (int)(at - (long long)seg * tl.key_tiles);
     const int kt1 = (int)min((long long)tl.key_tiles, kt0 + (pc.end - line));
     // heads of a row tile side by side, row tiles behind them
     const int rt = seg / a.c.heads, h = seg - rt * a.c.heads;
     const int row0 = rt * kRows, cnt = min(kRows, s.n * a.group - row0);
 
-    // q into shared memory, 16-byte chunk c of row r at chunk c ^ (r & 7); zeros past the rows and channels
-    for (int i = threadIdx.x; i < kRows * CH; i += kThreads) {
-      const int r = i / CH, c = i - r * CH;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < cnt && c * 8 < a.c.D) {
-        const int t = (row0 + r) / a.group, g = row0 + r - t * a.group;
-        const T* src = (const T*)a.q + (long long)(s.r0 + t) * a.q_t + (long long)(h * a.group + g) * a.q_h + c * 8;
-        if (((uintptr_t)src & 15) == 0) {
-          v = *reinterpret_cast<const uint4*>(src);
-        } else {
-          uint32_t w[4];
-          const uint16_t* e = reinterpret_cast<const uint16_t*>(src);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = (uint32_t)e[2 * j] | ((uint32_t)e[2 * j + 1] << 16);
-          v = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-      *reinterpret_cast<uint4*>(sq + r * DP * 2 + ((c ^ (r & 7)) << 4)) = v;
-    }
     // the keys that this thread's two rows see, and those that any row does
     const int r_a = lane >> 2, r_b = r_a + 8;
-    int lo_a = 0, hi_a = 0, lo_b = 0, hi_b = 0;
-    int lo = 0x7fffffff, hi = 0;
-    for (int r = 0; r < cnt; ++r) {
-      int f, e;
-      seen_range(a, s.r0 + (row0 + r) / a.group, s.len, &f, &e);
-      if (r == r_a) lo_a = f, hi_a = e;
-      if (r == r_b) lo_b = f, hi_b = e;
-      if (f < e) {
-        lo = min(lo, f);
-        hi = max(hi, e);
-      }
-      if (!a.ranges) {  // all rows alike
-        if (r_a < cnt) lo_a = f, hi_a = e;
-        if (r_b < cnt) lo_b = f, hi_b = e;
-        break;
-      }
+    int lo_a = 0, hi_a = 0, lo_b = 0, hi_b = 0, lo = 0, hi = s.len;
+    if (!a.ranges) {
+      if (r_a < cnt) hi_a = hi;
+      if (r_b < cnt) hi_b = hi;
+    } else {
+      int f = 0, e = 0;  // lane r holds row r's
+      if (lane < cnt) seen_range(a, s.r0 + (row0 + lane) / a.group, s.len, &f, &e);
+      lo_a = __shfl_sync(0xffffffffu, f, r_a), hi_a = __shfl_sync(0xffffffffu, e, r_a);
+      lo_b = __shfl_sync(0xffffffffu, f, r_b), hi_b = __shfl_sync(0xffffffffu, e, r_b);
+      lo = __reduce_min_sync(0xffffffffu, f < e ? f : 0x7fffffff);
+      hi = __reduce_max_sync(0xffffffffu, e);
     }
     // rows of one token, or of tokens that see the same keys, need no mask of their own
     const bool differ = (r_a < cnt && (lo_a != lo || hi_a != hi)) || (r_b < cnt && (lo_b != lo || hi_b != hi));
     const bool mixed = __any_sync(0xffffffffu, differ);
-    __syncthreads();
-
-    uint32_t qf[kQRegs ? NK : 1][4];
-    const uint32_t q_row = sq_a + (lane & 15) * DP * 2;
-    if (kQRegs) {
-#pragma unroll
-      for (int k = 0; k < NK; ++k) ldsm4(q_row + (((2 * k + (lane >> 4)) ^ (lane & 7)) << 4), qf[kQRegs ? k : 0]);
-    }
-
-    float o[DP / 8][4];
-#pragma unroll
-    for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;
 
     const int* table = a.b.pages + b * a.b.page_stride;
-    const int w0 = max(kt0, lo == 0x7fffffff ? kt1 : lo / kKeys), w1 = min(kt1, (hi + kKeys - 1) / kKeys);
+    const int w0 = hi > 0 ? max(kt0, lo / kKeys) : kt1, w1 = min(kt1, (hi + kKeys - 1) / kKeys);
 
-    auto issue = [&](int kt) {
+    // The page of this lane's key in tile kt (lane & 15), asked for a tile ahead of
+    // the loads that need it; -1 if no row sees the key.
+    auto lookup = [&](int kt) {
+      const int key = kt * kKeys + (lane & 15);
+      return kt < w1 && key >= lo && key < hi ? table[key / a.c.page_size] : -1;
+    };
+    auto issue = [&](int kt, int page) {
       const int st = kt % ST;
-      const int key0 = kt * kKeys + warp * kWarpKeys;
+      const int key = kt * kKeys + (lane & 15);
       const uint32_t dk = ring_a + st * 2 * C::kHalf, dv = dk + C::kHalf;
-      uint32_t seen = 0;
-      // rows that hold a key some row sees
-      const int key = key0 + (lane & 15);
-      bool take = key >= lo && key < hi;
+      const bool take = page >= 0 && page < a.c.pages;
+      if (!take && key >= lo && key < hi && a.b.status) atomicCAS(a.b.status, 0, (int)kDevBadPage);
       long long ko = 0, vo = 0;
       if (take) {
-        const int pi = key / a.c.page_size, off = key - pi * a.c.page_size;
-        const int p = table[pi];
-        if (p >= 0 && p < a.c.pages) {
-          ko = p * a.c.k_page + h * a.c.k_head + off * a.c.k_row;
-          vo = p * a.c.v_page + h * a.c.v_head + off * a.c.v_row;
-        } else {
-          take = false;
-          if (a.b.status) atomicCAS(a.b.status, 0, (int)kDevBadPage);
-        }
+        const int off = key % a.c.page_size;
+        ko = page * a.c.k_page + h * a.c.k_head + off * a.c.k_row;
+        vo = page * a.c.v_page + h * a.c.v_head + off * a.c.v_row;
       }
-      seen = __ballot_sync(0xffffffffu, take) & 0xffffu;
+      const uint32_t seen = __ballot_sync(0xffffffffu, take) & 0xffffu;
       if (lane == 0) s_seen[warp][st] = seen;
       constexpr int RPI = 32 / CH > 0 ? 32 / CH : 1;  // rows per instruction
 #pragma unroll
-      for (int i = 0; i < kWarpKeys / RPI; ++i) {
+      for (int i = 0; i < kKeys / RPI; ++i) {
         const int r = i * RPI + lane / CH, c = lane % CH;
         const long long kr = __shfl_sync(0xffffffffu, ko, r), vr = __shfl_sync(0xffffffffu, vo, r);
         const bool ok = ((seen >> r) & 1) && c * 8 < a.c.D;
@@ -285,11 +250,57 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
       }
     };
 
+    // everything that only waits for memory first: the first pages' numbers and q, then the first tiles
+    int page[ST];
+#pragma unroll
+    for (int i = 0; i < ST; ++i) page[i] = lookup(w0 + i);
+    constexpr int NQ = kRows * CH / 32;
+    uint4 qv[NQ];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int r = (i * 32 + lane) / CH, c = lane % CH;
+      qv[i] = make_uint4(0, 0, 0, 0);  // past the rows and channels
+      if (r < cnt && c * 8 < a.c.D) {
+        const int t = (row0 + r) / a.group, g = row0 + r - t * a.group;
+        const T* src = (const T*)a.q + (long long)(s.r0 + t) * a.q_t + (long long)(h * a.group + g) * a.q_h + c * 8;
+        if (((uintptr_t)src & 15) == 0) {
+          qv[i] = *reinterpret_cast<const uint4*>(src);
+        } else {
+          uint32_t w[4];
+          const uint16_t* e = reinterpret_cast<const uint16_t*>(src);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = (uint32_t)e[2 * j] | ((uint32_t)e[2 * j + 1] << 16);
+          qv[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) {
-      if (w0 + i < w1) issue(w0 + i);
+      if (w0 + i < w1) issue(w0 + i, page[i]);
       cp_commit();
     }
+    int ahead = page[ST - 1];  // of tile kt + ST - 1
+    // q by way of shared memory: 16-byte chunk c of row r at chunk c ^ (r & 7)
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int r = (i * 32 + lane) / CH, c = lane % CH;
+      *reinterpret_cast<uint4*>(sq + r * DP * 2 + ((c ^ (r & 7)) << 4)) = qv[i];
+    }
+    __syncwarp();
+    uint32_t qf[kQRegs ? NK : 1][4];
+    const uint32_t q_row = sq_a + (lane & 15) * DP * 2;
+    if (kQRegs) {
+#pragma unroll
+      for (int k = 0; k < NK; ++k) ldsm4(q_row + (((2 * k + (lane >> 4)) ^ (lane & 7)) << 4), qf[kQRegs ? k : 0]);
+      __syncwarp();
+    }
+
+    float o[DP / 8][4];
+#pragma unroll
+    for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;
+
     for (int kt = w0; kt < w1; ++kt) {
       cp_wait<ST - 2>();
       __syncwarp();
@@ -297,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
       const uint32_t sk = ring_a + st * 2 * C::kHalf, sv = sk + C::kHalf;
       const uint32_t seen = s_seen[warp][st];
       if (seen) {
-        const int key0 = kt * kKeys + warp * kWarpKeys;
+        const int key0 = kt * kKeys;
         float sc[2][4] = {};
         const int kr = ((lane >> 4) << 3) + (lane & 7);
         const uint32_t krow = sk + kr * DP * 2;
@@ -317,8 +328,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
         }
         // mask: hidden keys to -inf
         bool part = seen != 0xffffu;  // some key hidden from every row
-        if (mixed) part = part || __any_sync(0xffffffffu, (r_a < cnt && (key0 < lo_a || key0 + kWarpKeys > hi_a)) ||
-                                                              (r_b < cnt && (key0 < lo_b || key0 + kWarpKeys > hi_b)));
+        if (mixed) part = part || __any_sync(0xffffffffu, (r_a < cnt && (key0 < lo_a || key0 + kKeys > hi_a)) ||
+                                                              (r_b < cnt && (key0 < lo_b || key0 + kKeys > hi_b)));
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -372,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
         // taken out of the tile and added to the rows that see them.
         bool odd = false;
         if (mixed && part) {
-          for (int i = lane; i < kWarpKeys * CH; i += 32) {
+          for (int i = lane; i < kKeys * CH; i += 32) {
             const uint4 v = *reinterpret_cast<const uint4*>(ring + (sv - ring_a) + i * 16);
             odd |= odd32<T>(v.x) || odd32<T>(v.y) || odd32<T>(v.z) || odd32<T>(v.w);
           }
@@ -382,22 +393,22 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
             for (int n = 0; n < 2; ++n)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                s_p[warp][(i < 2 ? r_a : r_b)][n * 8 + (lane & 3) * 2 + (i & 1)] = sc[n][i] == -INFINITY ? -1.f : p[n][i];
+                s_p[(i < 2 ? r_a : r_b) * kKeys + n * 8 + (lane & 3) * 2 + (i & 1)] = sc[n][i] == -INFINITY ? -1.f : p[n][i];
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < DP / 8; ++i)
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const int c = i * 8 + (lane & 3) * 2 + (j & 1);
-                for (int k = 0; k < kWarpKeys; ++k) {
-                  const float w = s_p[warp][j < 2 ? r_a : r_b][k];
+                for (int k = 0; k < kKeys; ++k) {
+                  const float w = s_p[(j < 2 ? r_a : r_b) * kKeys + k];
                   const uint8_t* e = ring + (sv - ring_a) + k * DP * 2 + ((((c >> 3) ^ (k & 7)) << 4) | ((c & 7) * 2));
                   const T v = *reinterpret_cast<const T*>(e);
                   if (w >= 0.f && odd16<T>(*reinterpret_cast<const uint16_t*>(e))) o[i][j] += w * val<T>(v);
                 }
               }
             __syncwarp();
-            for (int i = lane; i < kWarpKeys * DP; i += 32) {
+            for (int i = lane; i < kKeys * DP; i += 32) {
               uint16_t* e = reinterpret_cast<uint16_t*>(ring + (sv - ring_a)) + i;
               if (odd16<T>(*e)) *e = 0;
             }
@@ -418,97 +429,168 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
         }
       }
       __syncwarp();
-      if (kt + ST - 1 < w1) issue(kt + ST - 1);
+      if (kt + ST - 1 < w1) issue(kt + ST - 1, ahead);
       cp_commit();
+      ahead = lookup(kt + ST);
     }
     cp_wait<0>();
 
-    // --------------------------------------------- the warps' parts into one
-    if (Weights<T>::kBias != 0.f) {
-      const float f = exp2f(-Weights<T>::kBias);
-      l_a *= f;
-      l_b *= f;
-#pragma unroll
-      for (int i = 0; i < DP / 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][j] *= f;
-    }
+    // ------------------------------------------------------- out, or a part of it
+    const float unbias = Weights<T>::kBias != 0.f ? exp2f(-Weights<T>::kBias) : 1.f;
 #pragma unroll
     for (int d = 1; d < 4; d <<= 1) {
       l_a += __shfl_xor_sync(0xffffffffu, l_a, d);
       l_b += __shfl_xor_sync(0xffffffffu, l_b, d);
     }
-    if ((lane & 3) == 0) {
-      s_ml[warp][r_a] = make_float2(m_a, l_a);
-      s_ml[warp][r_b] = make_float2(m_b, l_b);
+    l_a *= unbias;
+    l_b *= unbias;
+    const bool whole = kt0 == 0 && kt1 == tl.key_tiles;
+    const long long slot = 2LL * me + (kt0 == 0 ? 1 : 0);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const int r = w ? r_b : r_a;
+      const float m = w ? m_b : m_a, l = w ? l_b : l_a;
+      if (r >= cnt) continue;
+      if (whole) {
+        const float rl = l == 0.f ? 0.f : unbias / l;
+        T* dst = out_row<T>(a, s, h, row0 + r);
+        const bool even = ((uintptr_t)dst & 3) == 0;
+#pragma unroll
+        for (int i = 0; i < DP / 8; ++i) {
+          const int c = i * 8 + (lane & 3) * 2;
+          if (c >= a.c.D) continue;
+          // a row that saw nothing: zeros, whatever else its products hold
+          const float x = l == 0.f ? 0.f : o[i][2 * w] * rl, y = l == 0.f ? 0.f : o[i][2 * w + 1] * rl;
+          const T e[2] = {round_to<T>(x), round_to<T>(y)};
+          if (even) {
+            *reinterpret_cast<uint32_t*>(dst + c) = *reinterpret_cast<const uint32_t*>(e);
+          } else {
+            dst[c] = e[0];
+            dst[c + 1] = e[1];
+          }
+        }
+        if ((lane & 3) == 0) put_lse(a, s, h, row0 + r, m, l);
+      } else {
+        float* dst = ws.o + (slot * kRows + r) * DP;
+#pragma unroll
+        for (int i = 0; i < DP / 8; ++i)
+          *reinterpret_cast<float2*>(dst + i * 8 + (lane & 3) * 2) = make_float2(o[i][2 * w] * unbias, o[i][2 * w + 1] * unbias);
+        if ((lane & 3) == 0) ws.ml[slot * kRows + r] = make_float2(m, l);
+      }
+    }
+    if (!whole && kt0 == 0 && lane == 0) {
+      const long long last = line + tl.key_tiles - 1;  // the row tile's last tile: its piece is the last part's
+      ws.open[me] = Open{pc.holder(last) - me, h, row0, cnt, s, 0};
     }
     __syncwarp();
-    float* so = reinterpret_cast<float*>(ring);  // [kRows][DP], in the warp's own ring
-#pragma unroll
-    for (int i = 0; i < DP / 8; ++i) {
-      const int c = i * 8 + (lane & 3) * 2;
-      if (r_a < cnt) *reinterpret_cast<float2*>(so + r_a * DP + c) = make_float2(o[i][0], o[i][1]);
-      if (r_b < cnt) *reinterpret_cast<float2*>(so + r_b * DP + c) = make_float2(o[i][2], o[i][3]);
-    }
-    __syncthreads();
-    const bool whole = kt0 == 0 && kt1 == tl.key_tiles;
-    const int slot = 2 * me + (kt0 == 0 ? 1 : 0);
-    for (int i = threadIdx.x; i < cnt * DP; i += kThreads) {
-      const int r = i / DP, c = i - r * DP;
-      float m = -INFINITY, l = 0.f, v = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w][r].x);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = weight(s_ml[w][r].x, m);
-        l += f * s_ml[w][r].y;
-        v += f * reinterpret_cast<const float*>(smem + w * C::kRing)[r * DP + c];
-      }
-      if (whole) {
-        if (c < a.c.D) out_row<T>(a, s, h, row0 + r)[c] = round_to<T>(l == 0.f ? 0.f : v / l);
-        if (c == 0) put_lse(a, s, h, row0 + r, m, l);
-      } else {
-        ws.o[((long long)slot * kRows + r) * DP + c] = v;
-        if (c == 0) ws.ml[slot * kRows + r] = make_float2(m, l);
-      }
-    }
-    if (!whole && kt0 == 0 && threadIdx.x == 0) {
-      const long long last = line + tl.key_tiles - 1;  // the row tile's last tile: its block is the last part's
-      ws.open[me] = Open{b, rt, h, pc.holder(last) - me};
-    }
-    __syncthreads();
     at += kt1 - kt0;
     line += kt1 - kt0;
   }
 }
 
-// Joins the parts of the row tile that block `blockIdx.x` of the split kernel
-// left open, in the order of the keys.
+// Joins the parts of the row tiles that the pieces of block `blockIdx.x` left open,
+// row `blockIdx.y` of each, in the order of the keys.  Eight warps share the open
+// pieces (a task each, or several to a task): lane i forms the weight of the i-th
+// part of its warp, all lanes add up the parts' channels, eight parts asked for
+// together, and the warps of a task meet in shared memory.  Rows of sequences
+// without a key get their zeros here.
+constexpr int kJoinWarps = 8;
 template <typename T, int DP>
-__global__ void __launch_bounds__(DP) kv_join_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_constant__ AttnArgs a) {
+  constexpr int N = DP / 32;  // channels per lane
+  __shared__ float s_v[kJoinWarps][DP];
+  __shared__ float2 s_ml[kJoinWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int me = blockIdx.x;
-  const Space ws = space<DP>(a.workspace, gridDim.x);
-  const Open op = ws.open[me];
-  if (op.parts == 0) return;
-  const Seq s = sequence(a, op.b, false);
-  const int row0 = op.rt * kRows, cnt = min(kRows, s.n * a.group - row0);
-  const int c = threadIdx.x;
-  for (int r = blockIdx.y; r < cnt; r += gridDim.y) {
-    float m = -INFINITY, l = 0.f, v = 0.f;
-    for (int i = 0; i <= op.parts; ++i) {
-      const long long slot = 2LL * (me + i) + (i == 0 ? 1 : 0);
-      const float2 ml = ws.ml[slot * kRows + r];
-      const float x = ws.o[(slot * kRows + r) * DP + c];
-      const float n = fmaxf(m, ml.x);
-      const float f = weight(m, n), g = weight(ml.x, n);
-      l = l * f + ml.y * g;
-      v = v * f + x * g;
-      m = n;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y;
+  const Space ws = space<DP>(a.workspace, gridDim.x * kWarps);
+  const Open* open = ws.open + blockIdx.x * kWarps;
+  // lane w: piece w
+  const Open mine = lane < kWarps ? open[lane] : Open{0, 0, 0, 0, {0, 0, 0}, 0};
+  uint32_t todo = __ballot_sync(0xffffffffu, mine.parts > 0 && r < mine.cnt);
+  const int tasks = __popc(todo);
+  if (tasks > 0) {
+    const int per = tasks > 2 ? 2 : tasks == 2 ? 4 : 8;  // warps per task (four tasks at most)
+    const int sub = warp % per, nth = warp / per;
+    for (int i = 0; i < nth; ++i) todo &= todo - 1;
+    const bool any = todo != 0;
+    const int w0 = any ? __ffs(todo) - 1 : 0, me = blockIdx.x * kWarps + w0;
+    Open o;
+    o.parts = __shfl_sync(0xffffffffu, mine.parts, w0);
+    o.h = __shfl_sync(0xffffffffu, mine.h, w0);
+    o.row0 = __shfl_sync(0xffffffffu, mine.row0, w0);
+    o.s.r0 = __shfl_sync(0xffffffffu, mine.s.r0, w0);
+    const int n = any ? o.parts + 1 : 0;
+    float m = -INFINITY, l = 0.f, v[N] = {};
+    for (int i0 = sub; i0 < n; i0 += 32 * per) {
+      const int k = min(32, (n - i0 + per - 1) / per);  // parts i0, i0 + per, ..
+      float2 ml = make_float2(-INFINITY, 0.f);
+      const int i = i0 + lane * per;
+      if (lane < k) ml = ws.ml[(2LL * (me + i) + (i == 0 ? 1 : 0)) * kRows + r];
+      float top = 0.f, w = 0.f, f = 0.f;
+      for (int q0 = 0; q0 < k; q0 += 8) {
+        float2 x[8][N / 2];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int p = i0 + min(q0 + q, k - 1) * per;
+          const float2* src =
+              reinterpret_cast<const float2*>(ws.o + ((2LL * (me + p) + (p == 0 ? 1 : 0)) * kRows + r) * DP + lane * N);
+#pragma unroll
+          for (int e = 0; e < N / 2; ++e) x[q][e] = src[e];
+        }
+        if (q0 == 0) {  // the weights, while the first channels are on their way
+          top = ml.x;
+#pragma unroll
+          for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          top = fmaxf(top, m);
+          w = lane < k ? weight(ml.x, top) : 0.f;
+          f = weight(m, top);
+          float part = lane < k ? ml.y * w : 0.f;
+#pragma unroll
+          for (int d = 16; d; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
+          l = l * f + part;
+          m = top;
+#pragma unroll
+          for (int e = 0; e < N; ++e) v[e] *= f;
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float wi = __shfl_sync(0xffffffffu, w, (q0 + q) & 31);
+          if (q0 + q < k) {
+#pragma unroll
+            for (int e = 0; e < N / 2; ++e) {
+              v[2 * e] = fmaf(x[q][e].x, wi, v[2 * e]);
+              v[2 * e + 1] = fmaf(x[q][e].y, wi, v[2 * e + 1]);
+            }
+          }
+        }
+      }
     }
-    if (c < a.c.D) out_row<T>(a, s, op.h, row0 + r)[c] = round_to<T>(l == 0.f ? 0.f : v / l);
-    if (c == 0) put_lse(a, s, op.h, row0 + r, m, l);
+    if (lane == 0) s_ml[warp] = make_float2(m, l);
+#pragma unroll
+    for (int e = 0; e < N; ++e) s_v[warp][lane * N + e] = v[e];
+    __syncthreads();
+    if (sub == 0 && any) {
+      float top = -INFINITY;
+      for (int w = 0; w < per; ++w) top = fmaxf(top, s_ml[warp + w].x);
+      l = 0.f;
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = 0.f;
+      for (int w = 0; w < per; ++w) {
+        const float2 ml = s_ml[warp + w];
+        const float f = weight(ml.x, top);
+        l += ml.y * f;
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = fmaf(s_v[warp + w][lane * N + e], f, v[e]);
+      }
+      const float rl = l == 0.f ? 0.f : 1.f / l;
+      T* dst = out_row<T>(a, o.s, o.h, o.row0 + r);
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (lane * N + e < a.c.D) dst[lane * N + e] = round_to<T>(l == 0.f ? 0.f : v[e] * rl);
+      if (lane == 0) put_lse(a, o.s, o.h, o.row0 + r, top, l);
+    }
   }
+  if (r == 0) put_empty<T>(a, blockIdx.x, gridDim.x);
 }
 
 template <typename T, int DP>
@@ -522,8 +604,8 @@ cudaError_t go_split(const AttnArgs& a, int sms, cudaStream_t s) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(G, min(kRows, 4));
-  cfg.blockDim = dim3(DP);
+  cfg.gridDim = dim3(G, a.b.cu ? kRows : std::min(kRows, a.group));  // rows that a tile can have
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -548,7 +630,7 @@ cudaError_t by_dim(const AttnArgs& a, int sms, cudaStream_t s) {
 
 long long kv_attention_workspace(const AttnArgs& a, int sms) {
   const int DP = padded(a.c.D);
-  return space_bytes(DP, sms * (DP == 256 ? Cfg<256>::kCtas : Cfg<128>::kCtas));
+  return space_bytes(DP, sms * kWarps * (DP == 256 ? Cfg<256>::kCtas : Cfg<128>::kCtas));
 }
 
 cudaError_t launch_kv_attention(const AttnArgs& a, int sms, cudaStream_t s) {

@@ -333,11 +333,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  put_empty<T>(a, me, G);
   const Piece pc =
-      cut_line<kThreads / 32>(a.b.B, me, G, kPairUnits, reinterpret_cast<long long*>(half_ml),
+      cut_line<kThreads / 32, 1>(a.b.B, kPairUnits, reinterpret_cast<long long*>(half_ml),
                                             [&](int b) { return tiles_of(a, geo, sequence(a, b, false)).all; });
-  if (threadIdx.x == 0) ws.open[me] = Open{0, 0, 0, 0};
+  if (threadIdx.x == 0) ws.open[me].parts = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -387,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       run->odd_hi = -1;
       at += u1 - u0;
       if (run->k0 == 0 && run->k1 > 0 && run->k1 < tl.blocks)
-        ws.open[me] = Open{b, run->rt, run->h, pc.holder(line + n - u0 - 1) - me};
+        ws.open[me] = Open{pc.holder(line + n - u0 - 1) - me, run->h, run->row0, run->cnt, s, 0};
     }
     __syncthreads();
     const int h = run->h, row0 = run->row0, cnt = run->cnt, k0 = run->k0, k1 = run->k1;
@@ -861,9 +860,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv_chunk_join_kernel(const __gri
   const int me = blockIdx.x;
   const Space ws = space<DP>(a.workspace, G);
   const Open op = ws.open[me];
+  if (blockIdx.y == 0) put_empty<T>(a, me, G);  // rows of sequences without a key get their zeros here
   if (op.parts == 0) return;
-  const Seq s = sequence(a, op.b, false);
-  const int row0 = op.rt * kTileRows, cnt = min(kTileRows, s.n * a.group - row0);
+  const int row0 = op.row0, cnt = op.cnt;
   const int lane = threadIdx.x & 31;
   for (int w = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); w < kTileRows / 8 * (DP / 16);
        w += gridDim.y * (kJoinThreads / 32)) {
@@ -887,7 +886,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_chunk_join_kernel(const __gri
     }
     const float rl = l == 0.f ? 0.f : 1.f / l;
     if (4 * c < a.c.D) {
-      T* dst = out_row<T>(a, s, op.h, row0 + r) + 4 * c;
+      T* dst = out_row<T>(a, op.s, op.h, row0 + r) + 4 * c;
       const uint32_t lo = Pack<T>::two(v.x * rl, v.y * rl), hi = Pack<T>::two(v.z * rl, v.w * rl);
       if (((uintptr_t)dst & 7) == 0) {
         *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
@@ -899,7 +898,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_chunk_join_kernel(const __gri
         e[3] = (uint16_t)(hi >> 16);
       }
     }
-    if (c == 0) put_lse(a, s, op.h, row0 + r, m, l);
+    if (c == 0) put_lse(a, op.s, op.h, row0 + r, m, l);
   }
 }
 

@@ -96,20 +96,33 @@ __device__ __forceinline__ void put_empty(const AttnArgs& a, int me, int G) {
   }
 }
 
-// A call's tiles form one line, sequence after sequence; block `me` of `G` takes
-// an equal piece of it, of `least` tiles or more.  All threads call this; `of(b)` counts the tiles of
-// sequence b.
+// A call's tiles form one line, sequence after sequence, that is cut into equal
+// pieces of `least` tiles or more; a block takes PIECES of them in a row (one
+// each for its warps, or one for all).
+//
+// 64-bit division takes a tenth of a microsecond; most operands fit 32 bits.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((unsigned long long)a | (unsigned long long)b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
 struct Piece {
   long long beg, end;  // tiles of the line (empty: beg == end)
-  long long total, live;  // all tiles, and the blocks that have a piece
-  int b;               // the sequence of tile beg
-  long long at;        // and the tile's number in it
-  // the block that holds tile x of the line
-  __device__ __forceinline__ int holder(long long x) const { return (int)(((x + 1) * live - 1) / total); }
+  long long live;      // pieces that are not empty: each of `size` tiles, the first `longer` of them one more
+  long long size, longer;
+  int b;         // the sequence of tile beg
+  long long at;  // and the tile's number in it
+  __device__ __forceinline__ long long start(long long q) const { return q * size + min(q, longer); }
+  // the piece that holds tile x of the line
+  __device__ __forceinline__ int holder(long long x) const {
+    const long long n = longer * (size + 1);
+    return (int)(x < n ? quotient(x, size + 1) : longer + quotient(x - n, size));
+  }
 };
-template <int WARPS, typename F>
-__device__ __forceinline__ Piece cut_line(int B, int me, int G, int least, long long* scratch, F of) {
-  long long *s_scan = scratch + 2, *s_b = scratch, *s_at = scratch + 1;
+// All threads of the block call this; `of(b)` counts the tiles of sequence b;
+// `scratch` is shared memory of WARPS + 2 PIECES values.
+template <int WARPS, int PIECES, typename F>
+__device__ __forceinline__ Piece cut_line(int B, int least, long long* scratch, F of) {
+  static_assert(PIECES == 1 || PIECES == WARPS, "a piece for the block, or one for each warp");
+  long long *s_scan = scratch, *s_b = scratch + WARPS, *s_at = s_b + PIECES;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunk = (B + 32 * WARPS - 1) / (32 * WARPS);
   const int b_lo = min(B, (int)threadIdx.x * chunk), b_hi = min(B, b_lo + chunk);
@@ -125,40 +138,53 @@ __device__ __forceinline__ Piece cut_line(int B, int me, int G, int least, long 
   __syncthreads();
   Piece p;
   long long before = incl - mine;
-  p.total = 0;
+  long long total = 0;
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) {
     if (w < warp) before += s_scan[w];
-    p.total += s_scan[w];
+    total += s_scan[w];
   }
-  p.live = min((long long)G, max(p.total / least, p.total > 0 ? 1LL : 0LL));
+  p.live = min((long long)gridDim.x * PIECES, max(quotient(total, least), total > 0 ? 1LL : 0LL));
+  p.size = total > 0 ? quotient(total, p.live) : 1;
+  p.longer = total - p.size * p.live;
   p.beg = p.end = 0;
   p.b = 0;
   p.at = 0;
-  if (me >= p.live) return p;
-  p.beg = p.total * me / p.live;
-  p.end = p.total * (me + 1) / p.live;
-  if (p.beg >= before && p.beg < before + mine) {
-    long long at = p.beg - before;
-    int b = b_lo;
-    for (; b < b_hi; ++b) {
-      const long long n = of(b);
-      if (at < n) break;
-      at -= n;
+#pragma unroll 1
+  for (int w = 0; w < PIECES; ++w) {
+    const long long q = (long long)blockIdx.x * PIECES + w;
+    if (q >= p.live) break;
+    const long long beg = p.start(q);
+    if (beg >= before && beg < before + mine) {
+      long long at = beg - before;
+      int b = b_lo;
+      for (; b < b_hi; ++b) {
+        const long long n = of(b);
+        if (at < n) break;
+        at -= n;
+      }
+      s_b[w] = b;
+      s_at[w] = at;
     }
-    *s_b = b;
-    *s_at = at;
   }
   __syncthreads();
-  p.b = (int)*s_b;
-  p.at = *s_at;
+  const int w = PIECES == 1 ? 0 : warp;
+  const long long q = (long long)blockIdx.x * PIECES + w;
+  if (q < p.live) {
+    p.beg = p.start(q);
+    p.end = p.start(q + 1);
+    p.b = (int)s_b[w];
+    p.at = s_at[w];
+  }
   return p;
 }
 
-// What a block leaves for the join: a row tile whose first part it holds.
+// What a piece leaves for the join: the row tile whose first part it holds.
 struct Open {
-  int b, rt, h;
-  int parts;  // blocks after this one that hold the rest (0: nothing to join)
+  int parts;  // parts of it in the pieces after this one (0: nothing to join)
+  int h, row0, cnt;
+  Seq s;
+  int pad;
 };
 
 }  // namespace wan
