@@ -577,3 +577,66 @@ def test_steps_in_graphs(wv):
             assert torch.equal(got, step(s))
             q = wv.rotary(s["x"][:, :hq], s["pos"], (D // 2,), interleaved=False)
             ref.check_attention(got, None, ref.attention(q, s["kc"], s["vc"], pages, s["lengths"]))
+
+
+class _Strange(torch.Tensor):
+    """A subclass: such tensors are marshalled in Python, plain ones in C++."""
+
+
+def test_both_ways_in_give_the_same(wv):
+    rot = wv.Rotation((22, 21, 21))
+    kc = torch.zeros(9, 2, 16, 128, dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    pages = torch.arange(8, dtype=torch.int32).reshape(2, 4).cuda()
+    lens = torch.tensor([40, 64], dtype=torch.int32).cuda()
+    cu = torch.tensor([0, 3, 5], dtype=torch.int32).cuda()
+    q, k, v = (_randn(5, h, 128, dtype=torch.bfloat16, seed=h) for h in (8, 2, 2))
+    pos = _positions(5, 3)
+    ranges = torch.tensor([[0, 39], [1, 40], [7, 7], [0, 60], [5, 64]], dtype=torch.int32).cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    results = []
+    for wrap in (lambda t: t), (lambda t: t.as_subclass(_Strange)):
+        kc.zero_(), vc.zero_()
+        q_, k_ = wrap(q), wrap(k)
+        turned = wv.rotary(q_, pos, rot)
+        back = wv.rotary_grad(q_, pos, (22, 21, 21))
+        wv.kv_append(k_, v, kc, vc, pages, lens, cu, pos, rot)
+        new = wv.kv_append(k_, v, kc, vc, pages, lens, cu, pos, rot, q=q_, status=status)
+        caches = kc.clone(), vc.clone()
+        out, lse = wv.kv_attention(wrap(new), kc, vc, pages, lens, cu, ranges, return_lse=True, status=status)
+        one = wv.kv_attention(wrap(new[:2]), kc, vc, pages, lens, scale=0.3)
+        results.append([t.as_subclass(torch.Tensor) for t in (turned, back, new, *caches, out, lse, one)])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    wv.kv_status(status)
+
+
+@pytest.mark.parametrize("way", ["plain", "subclass"])
+def test_refusals_are_the_same_on_both_ways(wv, way):
+    wrap = (lambda t: t) if way == "plain" else (lambda t: t.as_subclass(_Strange))
+    kc = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    pages = torch.arange(4, dtype=torch.int32).reshape(2, 2).cuda()
+    lens = torch.tensor([3, 5], dtype=torch.int32).cuda()
+    q = _randn(2, 4, 64, dtype=torch.bfloat16)
+    grad = wrap(q.clone()).requires_grad_()
+    with pytest.raises(ValueError, match="autograd"):
+        wv.kv_attention(grad, kc, kc, pages, lens)
+    with torch.no_grad():
+        wv.kv_attention(grad, kc, kc, pages, lens)
+    with pytest.raises(ValueError, match="not on cpu|is on cpu"):
+        wv.kv_attention(wrap(q), kc, kc, pages.cpu(), lens)
+    with pytest.raises(ValueError, match="lengths is torch.int64"):
+        wv.kv_attention(wrap(q), kc, kc, pages, lens.long())
+    with pytest.raises(ValueError, match="contiguous"):
+        wv.kv_attention(wrap(q), kc, kc, pages, torch.zeros(4, dtype=torch.int32, device="cuda")[::2])
+    with pytest.raises(ValueError, match="rows for"):
+        wv.kv_attention(wrap(q), kc, kc, pages, lens[:1])
+    with pytest.raises((ValueError, wv.WanError)):
+        wv.kv_attention(wrap(q[:, :3]), kc, kc, pages, lens)
+    with pytest.raises(ValueError, match="positions need sections"):
+        wv.kv_append(wrap(q[:, :2]), q[:, :2], kc, kc.clone(), pages, lens, positions=_positions(2, 1))
+    with pytest.raises(ValueError, match="positions must be"):
+        wv.rotary(wrap(q), _positions(2, 2), (32,))
+    with pytest.raises((ValueError, wv.WanError)):
+        wv.rotary(wrap(q), _positions(2, 1), (33,))
+    with pytest.raises(ValueError, match="out is"):
+        wv.rotary(wrap(q), _positions(2, 1), (32,), out=torch.empty(2, 4, 64, device="cuda"))

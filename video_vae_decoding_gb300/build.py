@@ -1,7 +1,8 @@
 """Builds libwanvae.so (the C-ABI library) in-tree with nvcc for sm_103a.
 
 Each CUDA source is compiled in parallel to an object under ``_build/``,
-then linked into ``libwanvae.so`` next to this file.  The CUDA runtime is
+then linked into ``libwanvae.so`` next to this file; the token operators'
+marshalling in C++ becomes the Python module ``_tokens`` beside it.  The CUDA runtime is
 linked statically; the driver's tensor-map encoder is looked up at run time,
 so the library loads on a machine without a GPU.
 """
@@ -9,10 +10,12 @@ so the library loads on a machine without a GPU.
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libwanvae.so")
+BINDING = os.path.join(HERE, "_tokens.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
@@ -37,14 +41,15 @@ def sources() -> "list[str]":
 
 def _deps() -> "list[str]":
     files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
+    files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cpp")]
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
     return files + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
@@ -67,9 +72,25 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
+    def compile_binding() -> None:
+        tmp = BINDING + ".tmp"
+        torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+        toolkit = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+        includes = [INCLUDE, os.path.join(torch, "include"), sysconfig.get_paths()["include"],
+                    os.path.join(toolkit, "include")]
+        cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", *(f"-I{d}" for d in includes),
+               os.path.join(CSRC, "token_binding.cpp"), "-o", tmp, "-L" + os.path.join(torch, "lib"), "-ltorch_python",
+               "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on token_binding.cpp:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, BINDING)
+
     srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding.result()
     tmp = LIB + ".tmp"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:

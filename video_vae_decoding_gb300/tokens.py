@@ -66,6 +66,7 @@ class Rotation:
         self._axis = (ctypes.c_int32 * self.pairs)(*axis)
         self._c = WanRotation(self.pairs, self.axes, int(self.interleaved), self._freq, self._axis)
         self._ref = ctypes.byref(self._c)
+        self._addr = ctypes.addressof(self._c)
 
 
 @functools.lru_cache(maxsize=64)
@@ -131,6 +132,21 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _short_way():
+    """The C++ marshalling of ordinary calls (_tokens), made at the first call: None where it does not take one."""
+    global _short
+    from . import _tokens
+
+    lib = load()
+    _tokens.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.wan_rotary, lib.wan_kv_append, lib.wan_kv_attention, lib.wan_kv_attention_workspace)))
+    _short = _tokens
+    return _short
+
+
+_short = None
+
+
 def _turn(x, positions, sections, theta, interleaved, out, stream, inverse):
     code = _CODES.get(x.dtype)
     if code is None:
@@ -182,6 +198,12 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, sections, theta: float = 10
     strides with contiguous channels) turned by positions [tokens, axes] (or
     [batch, tokens, axes]; int32 or int64): see Rotation for sections (or pass
     a Rotation).  Computed in fp32 and rounded once.  out may be x."""
+    short = _short or _short_way()
+    if stream is None:
+        rot = _rotation(sections, theta, interleaved)
+        got = short.rotary(x, positions, rot._addr, rot.axes, out, 0)
+        if got is not None:
+            return got
     return _turn(x, positions, sections, theta, interleaved, out, stream, 0)
 
 
@@ -189,6 +211,12 @@ def rotary_grad(dy: torch.Tensor, positions: torch.Tensor, sections, theta: floa
                 out: torch.Tensor = None, stream=None) -> torch.Tensor:
     """Gradient of rotary with respect to x, given that of its result: dy turned
     by the opposite angles."""
+    short = _short or _short_way()
+    if stream is None:
+        rot = _rotation(sections, theta, interleaved)
+        got = short.rotary(dy, positions, rot._addr, rot.axes, out, 1)
+        if got is not None:
+            return got
     return _turn(dy, positions, sections, theta, interleaved, out, stream, 1)
 
 
@@ -260,6 +288,13 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     (q itself is allowed; new memory by default, where rows behind the last
     sequence stay uninitialised).  status: an int32 tensor of one value that
     takes a code if the tables name something that is not there (kv_status)."""
+    short = _short or _short_way()
+    if stream is None:
+        rot = None if sections is None else _rotation(sections, theta, interleaved)
+        got = short.append(k, v, k_cache, v_cache, pages, lengths, cu_tokens, positions, rot._addr if rot else 0,
+                           rot.axes if rot else 0, q, q_out, status)
+        if got is not None:
+            return None if got is True else got
     _refuse_grad(k, v, q, k_cache, v_cache, q_out)
     dev = k_cache.device
     c, heads, size, D = _cache(k_cache, v_cache, dev)
@@ -346,6 +381,11 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     1 / sqrt(head_dim) by default.  out: like q (new memory by default, where
     rows behind the last sequence stay uninitialised).  return_lse: also the
     fp32 logarithms of the sums, [tokens, q_heads]."""
+    short = _short or _short_way()
+    if stream is None:
+        got = short.attention(q, k_cache, v_cache, pages, lengths, cu_tokens, ranges, scale, out, return_lse, status)
+        if got is not None:
+            return got
     _refuse_grad(q, k_cache, v_cache, out)
     dev = k_cache.device
     c, heads, size, D = _cache(k_cache, v_cache, dev)
