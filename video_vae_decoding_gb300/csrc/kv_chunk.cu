@@ -24,7 +24,7 @@
 // blocks in turn, and adds the halves up at the end.
 //
 // Bound: the tensor cores, 4 D operations per row and key; K and V come through
-// one ring in the order of their use and serve both halves, so a block of 128
+// a ring each and serve both halves, so a block of 128
 // keys asks 64 KB (D = 128) for 33.6 MFLOP.
 // V is taken as it lies in the cache, [key][channel]: the MMA's second operand
 // with its N dimension contiguous, so nothing is transposed on the way.
@@ -44,7 +44,7 @@ namespace wan {
 
 namespace {
 
-// Warps 0 loads, 1 issues Q K, 2 issues P V, 3 TMEM; 4-7 softmax of half 0, 8-11 of
+// Warps 0 loads K, 1 issues Q K, 2 issues P V, 3 loads V (and owns TMEM); 4-7 softmax of half 0, 8-11 of
 // half 1: a thread per row (TMEM lane).
 constexpr int kThreads = 384;
 constexpr int kHalfRows = 128;
@@ -57,7 +57,9 @@ template <int DP>
 struct Cfg {
   static constexpr int ND = DP / 64;
   static constexpr int kSlot = ND * kBoxBytes;          // K or V of a block
-  static constexpr int kStages = DP == 128 ? 5 : 10;
+  // K and V have a ring each: a barrier is then waited for by one warp, phase by phase, and a parity never stands for
+  // another lap of the ring than the next
+  static constexpr int kKeySlots = DP == 128 ? 2 : 5, kStages = DP == 128 ? 5 : 10;
   static constexpr int kQ = 2 * ND * kBoxBytes;
   static constexpr int kSmem = kQ + kStages * kSlot + 1024 + 1024;
 };
@@ -276,12 +278,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     kv_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                     const __grid_constant__ AttnArgs a, const __grid_constant__ ChunkGeo geo) {
   using C = Cfg<DP>;
-  constexpr int S = C::kStages, ND = C::ND;
+  constexpr int S = C::kStages, SK = C::kKeySlots, SV = S - SK, ND = C::ND;
   // the only shared memory of the kernel, so it starts on a 1024-byte boundary, as the swizzled boxes must
   extern __shared__ __align__(1024) uint8_t smem[];
   static_assert(sizeof(Run) + 8 * (2 * S + 10) + 8 + 128 + 16 <= 1024, "barriers and the run's description");
   uint8_t* sQ = smem;  // [half][64-channel box][128 rows]
-  uint8_t* sR = sQ + C::kQ;
+  uint8_t* sR = sQ + C::kQ;  // SK slots of K, SV of V
   uint64_t* full = reinterpret_cast<uint64_t*>(sR + S * C::kSlot);
   uint64_t* empty = full + S;
   uint64_t* s_full = empty + S;   // [2] a block's S of half t in TMEM
@@ -347,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   int b = pc.b;
   long long at = pc.at;
-  int it = 0;                 // ring slots used so far (all roles count alike)
+  int it = 0;                 // blocks so far (all roles count alike)
   int ns[2] = {0, 0};         // blocks of each half so far
 
   for (long long line = pc.beg; line < pc.end;) {
@@ -440,70 +442,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int j0 = run->hi > 0 ? max(k0, block_of_key(geo, page_size, run->lo)) : k1;
     const int j1 = run->hi > 0 ? min(k1, block_of_key(geo, page_size, run->hi - 1) + 1) : k1;
     const int nb = max(0, j1 - j0);
-    // blocks of each half; K leads V by `lead` blocks (one of each half) in the ring: K_0 .. K_{lead-1}, then
-    // K_{n+lead}, V_n in turn
+    // blocks of each half
     const int nh[2] = {split ? (nb + 1) / 2 : nb, split ? nb / 2 : nb};
-    const int lead = min(split ? 2 : 1, nb);
     bool ok = true;
 
-    if (warp == 0) {
-      // --------------------------------------------------------------- loads
+    if (warp == 0 || warp == 3) {
+      // ------------------------------------------------ loads: K, and V
+      const bool ofK = warp == 0;
+      const CUtensorMap* map = ofK ? &mapK : &mapV;
       const int* table = a.b.pages + run->b * a.b.page_stride;
       const int held = (s.len + page_size - 1) / page_size;  // pages of the sequence
       const int bytes = geo.parts == 1 ? geo.pages * geo.box_rows * 128 * ND : C::kSlot;
-      int slot = it % S, lap = it / S;
-      // one box per lane, of the page that the lane holds
-      auto load = [&](const CUtensorMap* map, int page, int off) {
+      // All counted along: a division here would queue behind the softmax's exponentials.  The lane's page of block
+      // j: its place `idx` in the table and the rows `off` of it that come first; asked for two blocks ahead.
+      int idx = geo.parts == 1 ? j0 * geo.pages + lane : j0 / geo.parts, part = geo.parts == 1 ? 0 : j0 - idx * geo.parts;
+      int idx2 = idx, part2 = part;
+      const int wide = lane < geo.pages ? held : 0;
+      auto advance = [&](int& i, int& p) {
+        if (geo.parts == 1) i += geo.pages;
+        else if (++p == geo.parts) p = 0, ++i;
+      };
+      auto entry = [&](int n) {
+        const int e = n < nb && idx2 < wide ? table[idx2] : (int)a.c.pages;  // past the cache, which reads as zeros
+        advance(idx2, part2);
+        return e;
+      };
+      int page = entry(0), next = entry(1);
+      const int slots = ofK ? SK : SV, first = ofK ? 0 : SK;
+      int slot = it % slots, lap = it / slots;
+      for (int n = 0; n < nb && ok; ++n) {
+        const int after = entry(n + 2);
+        const int off = part * kBlock;
+        const bool none = idx < wide && (page < 0 || page >= a.c.pages);
+        advance(idx, part);
+        if (none) {
+          page = (int)a.c.pages;
+          if (err) atomicCAS(err, 0, (int)kDevBadPage);
+        }
+        if (ofK) {
+          const uint32_t nones = __ballot_sync(0xffffffffu, none);
+          if (lane == 0) hole[(j0 + n) & 31] = nones;
+        }
         int good = 1;
         if (lane == 0) {
-          if (lap > 0) good = wait_phase(&empty[slot], (lap - 1) & 1, err, kDevTimeoutEmpty);
+          if (lap > 0) good = wait_phase(&empty[first + slot], (lap - 1) & 1, err, kDevTimeoutEmpty);
           if (*stop) good = 0;
-          if (good) mbar_arrive_expect_tx(smem_u32(&full[slot]), bytes);
+          if (good) mbar_arrive_expect_tx(smem_u32(&full[first + slot]), bytes);
         }
-        if (!__shfl_sync(0xffffffffu, good, 0)) return false;
-        if (lane < geo.pages) {
+        ok = __shfl_sync(0xffffffffu, good, 0);
+        if (!ok) break;
+        if (lane < geo.pages) {  // one box per lane, of the page that the lane holds
           int c[3];
           c[geo.dim_row] = off;
           c[geo.dim_head] = h;
           c[geo.dim_page] = page;
-          const uint32_t d = smem_u32(sR + slot * C::kSlot) + lane * geo.box_rows * 128;
+          const uint32_t d = smem_u32(sR + (first + slot) * C::kSlot) + lane * geo.box_rows * 128;
 #pragma unroll
           for (int u = 0; u < ND; ++u)
-            tma_load_4d(d + u * kBoxBytes, map, smem_u32(&full[slot]), 64 * u, c[0], c[1], c[2]);
+            tma_load_4d(d + u * kBoxBytes, map, smem_u32(&full[first + slot]), 64 * u, c[0], c[1], c[2]);
         }
-        if (++slot == S) slot = 0, ++lap;
-        return true;
-      };
-      int page_q[2] = {0, 0}, off_q[2] = {0, 0};  // pages of the last two blocks: their V is still to come
-      for (int n = 0; n < nb + lead && ok; ++n) {
-        int page = (int)a.c.pages, off = 0;  // past the sequence: past the cache, which reads as zeros
-        if (n < nb) {
-          const int j = j0 + n;
-          int idx;
-          if (geo.parts == 1) {
-            idx = j * geo.pages + lane;
-          } else {
-            idx = j / geo.parts;
-            off = (j - idx * geo.parts) * kBlock;
-          }
-          bool none = false;
-          if (lane < geo.pages && idx < held) {
-            page = table[idx];
-            none = page < 0 || page >= a.c.pages;
-            if (none) {
-              page = (int)a.c.pages;
-              if (err) atomicCAS(err, 0, (int)kDevBadPage);
-            }
-          }
-          const uint32_t nones = __ballot_sync(0xffffffffu, none);
-          if (lane == 0) hole[j & 31] = nones;
-          ok = load(&mapK, page, off);
-        }
-        if (n >= lead && ok) ok = load(&mapV, page_q[lead - 1], off_q[lead - 1]);
-        page_q[1] = page_q[0];
-        off_q[1] = off_q[0];
-        page_q[0] = page;
-        off_q[0] = off;
+        page = next;
+        next = after;
+        if (++slot == slots) slot = 0, ++lap;
       }
       if (!ok) *stop = 1;
     } else if ((warp == 1 || warp == 2) && nb > 0) {
@@ -516,20 +516,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int dn = (a.c.D + 15) / 16;  // k steps of S, N / 16 of O
       const bool one = elect();
       const int steps = split ? nb : 2 * nb;
-      int slot = it % S, phase = (it / S) & 1;
-      auto move = [&](int d) {
-        slot += d;
-        if (slot >= S) slot -= S, phase ^= 1;
-      };
       if (warp == 1) {
+        int slot = it % SK, phase = (it / SK) & 1;
         const uint32_t idS = idesc(Pack<T>::kFormat, false, kBlock);
         const uint32_t q0 = desc_k(smem_u32(sQ)), kd0 = desc_k(smem_u32(sR));
+        uint32_t there = 0;  // the block's K is known to be there (asked a step ahead)
         for (int g = 0; g < steps; ++g) {
           const int t = g & 1, n = split ? g : g >> 1;
-          if (split || t == 0) {  // K of its block: the first `lead` side by side, then every other slot
-            if (n > 0) move(n < lead ? 1 : n == lead ? 1 : 2);
+          if ((split || t == 0) && !__all_sync(0xffffffffu, there))  // K of its block
             ok = wait_phase(&full[slot], phase, err, kDevTimeoutFull);
-          }
           // the S buffer, once the step that used it last (the half's own, or the other's) has been read
           if (kTwoS) {
             if (g > 1 && ok) ok = wait_phase(&s_free[t], (ns[t] + (g >> 1) - 1) & 1, err, kDevTimeoutAccum);
@@ -548,17 +543,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_commit(smem_u32(&s_full[t]));
             if (split || t == 1) umma_commit(smem_u32(&empty[slot]));
           }
+          if (split || t == 1) {
+            if (++slot == SK) slot = 0, phase ^= 1;
+            there = n + 1 < nb && ask_phase(&full[slot], phase);
+          }
         }
       } else {
         const uint32_t idO = idesc(Pack<T>::kFormat, true, 16 * dn);
         const uint32_t vd0 = desc_v(smem_u32(sR));
-        move(lead);
+        int slot = SK + it % SV, phase = (it / SV) & 1;
+        uint32_t there = 0;
         for (int g = 0; g < steps; ++g) {
           const int t = g & 1, n = split ? g : g >> 1;
-          if (split || t == 0) {  // V of its block, behind K of the block `lead` further on
-            move((n > 0 ? 1 : 0) + (n + lead < nb ? 1 : 0));
+          if ((split || t == 0) && !__all_sync(0xffffffffu, there))  // V of its block
             ok = wait_phase(&full[slot], phase, err, kDevTimeoutFull);
-          }
           if (ok) ok = wait_phase(&p_full[t], (ns[t] + (g >> 1)) & 1, err, kDevTimeoutAccum);
           if (!ok) break;
           tc_fence_after();
@@ -568,6 +566,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < kBlock / 16; ++e) umma_ts(tO + DP * t, p + 8 * e, v + 128 * e, idO, g > 1 || e > 0);
             umma_commit(smem_u32(&o_done[t]));
             if (split || t == 1) umma_commit(smem_u32(&empty[slot]));
+          }
+          if (split || t == 1) {
+            if (++slot == S) slot = SK, phase ^= 1;
+            there = n + 1 < nb && ask_phase(&full[slot], phase);
           }
         }
       }
@@ -635,10 +637,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           // among their values must not meet a weight of zero.  Such values leave
           // the block here, and the rows that see them get them at the end.
           if (base < all_lo || base + rows > all_hi) {
-            const int n = j - j0, at_v = it + lead + n + min(n + 1, nb - lead);  // V_n's place in the ring
-            ok = __all_sync(0xffffffffu, wait_phase(&full[at_v % S], (at_v / S) & 1, err, kDevTimeoutFull));
+            const int at_v = it + j - j0;
+            // (this half's last P V has read its V, so every lap of the ring before this block's is known to be there)
+            if (i > 0) ok = wait_phase(&o_done[half], (n0 + i - 1) & 1, err, kDevTimeoutAccum);
+            if (ok) ok = wait_phase(&full[SK + at_v % SV], (at_v / SV) & 1, err, kDevTimeoutFull);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            uint4* v = reinterpret_cast<uint4*>(sR + (at_v % S) * C::kSlot);
+            uint4* v = reinterpret_cast<uint4*>(sR + (SK + at_v % SV) * C::kSlot);
             for (int e = hrow; e < C::kSlot / 16; e += kHalfRows) {
               const uint4 w = v[e];
               if (odd32<T>(w.x) || odd32<T>(w.y) || odd32<T>(w.z) || odd32<T>(w.w)) {
@@ -821,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    it += 2 * nb;
+    it += nb;
     ns[0] += nh[0];
     ns[1] += nh[1];
     // TMEM reads of this run come before the next run's MMAs
