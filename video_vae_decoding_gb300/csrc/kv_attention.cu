@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
 
   // the join's blocks may start as soon as every block of this grid runs
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for what came before on the stream
 
   const Piece pc = cut_line<kWarps, kWarps>(a.b.B, kLeast, s_line,
                                             [&](int b) { return tiles_of(a, sequence(a, b, false)).all; });
@@ -602,18 +603,22 @@ cudaError_t go_split(const AttnArgs& a, int sms, cudaStream_t s) {
   cudaError_t e = allow_smem((const void*)kv_split_kernel<T, DP>, C::kSmem, &allowed);
   if (e != cudaSuccess) return e;
   const int G = sms * C::kCtas;
-  kv_split_kernel<T, DP><<<G, kThreads, C::kSmem, s>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  // each may start as the kernel before it drains, and waits for its end
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(G, a.b.cu ? kRows : std::min(kRows, a.group));  // rows that a tile can have
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.stream = s;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
+  cfg.stream = s;
+  cfg.gridDim = dim3(G);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  e = cudaLaunchKernelEx(&cfg, kv_split_kernel<T, DP>, a);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(G, a.b.cu ? kRows : std::min(kRows, a.group));  // rows that a tile can have
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, kv_join_kernel<T, DP>, a);
 }
 

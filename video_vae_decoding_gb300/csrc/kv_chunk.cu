@@ -51,6 +51,7 @@ constexpr int kHalfRows = 128;
 constexpr int kTileRows = 256;
 constexpr int kBlock = 128;       // key columns of a block
 constexpr int kBoxBytes = 16384;  // 128 rows x 64 channels
+constexpr int kLeast = 5;         // units of a piece: a block's (with ten blocks' calls of 100 tokens take 42 us instead of 21)
 constexpr float kSlack = 8.f;    // log2 units that the reference maximum may lag behind
 
 template <int DP>
@@ -227,46 +228,93 @@ __device__ __forceinline__ void block_keys(const ChunkGeo& g, int page_size, int
   }
 }
 
-// A sequence on the line: `pairs` row tiles of more than 128 rows and perhaps a
-// smaller one behind them, each with every head and block.  A block of the
-// former counts kPairUnits, of the latter kSingleUnits: what they cost.  (A
-// smaller tile does half the arithmetic, but asks for K and V as fast as a
-// larger one would at twice the speed.)
-constexpr int kPairUnits = 5, kSingleUnits = 4;
-struct Tiles {
-  int blocks, pairs;
-  long long of_pairs, all;
+// A row tile: up to 256 rows of a sequence, and the blocks [k0, k1) that some of
+// them see (one block if they see none: it leaves their zeros).
+struct RowTile {
+  int b, rt;  // b < 0: none
+  int k0, k1;
 };
-__device__ __forceinline__ Tiles tiles_of(const AttnArgs& a, const ChunkGeo& g, const Seq& s) {
-  Tiles t;
-  t.blocks = blocks_of(g, a.c.page_size, s.len);
-  const int rows = s.n * a.group, last = rows % kTileRows;
-  t.pairs = rows / kTileRows + (last > kHalfRows);
-  const long long each = (long long)a.c.heads * t.blocks;
-  t.of_pairs = kPairUnits * each * t.pairs;
-  t.all = t.of_pairs + (last > 0 && last <= kHalfRows ? kSingleUnits * each : 0);
-  return t;
+// Room for the row tiles of T tokens in B sequences; those of a sequence that starts at row r0 stand from r0 * group /
+// 256 + b on, so that sequences never meet.
+__host__ __device__ inline long long row_tiles(const AttnArgs& a) {
+  return (long long)a.b.T * a.group / kTileRows + a.b.B;
+}
+
+// What a row tile with a head takes of the line: kRunUnits (start, end and the blocks at a mask's edge), and for each
+// block kPairUnits, or kSingleUnits in a tile of at most 128 rows.  They stand for what these cost: with 20 for a run two
+// chunks of 1300 causal tokens of 48 heads take 217 us, with 45 187, with 60 175, with 80 174.  (A smaller tile does half the arithmetic, but asks for K and V as
+// fast as a larger one would at twice the speed.)
+constexpr int kPairUnits = 5, kSingleUnits = 4, kRunUnits = 50;
+__device__ __forceinline__ int tile_weight(const AttnArgs& a, const Seq& s, int rt) {
+  return s.n * a.group - rt * kTileRows <= kHalfRows ? kSingleUnits : kPairUnits;
 }
 
 struct Space {
+  RowTile* tiles;
   Open* open;
   float2* ml;  // [2 G][kTileRows]
   float4* o;   // [2 G][DP / 4][kTileRows]: the rows side by side
 };
 template <int DP>
-__host__ __device__ inline Space space(void* w, int G) {
+__host__ __device__ inline Space space(const AttnArgs& a, int G) {
   Space s;
-  s.open = (Open*)w;
-  s.ml = (float2*)((char*)w + (size_t)G * sizeof(Open));
-  s.o = (float4*)((char*)s.ml + (size_t)2 * G * kTileRows * sizeof(float2));
+  s.tiles = (RowTile*)a.workspace;
+  s.open = (Open*)(s.tiles + row_tiles(a));
+  s.ml = (float2*)(s.open + G);
+  s.o = (float4*)(s.ml + (size_t)2 * G * kTileRows);
   return s;
+}
+
+// The row tiles of a call, a warp for each place.
+constexpr int kPlanWarps = 4;
+__global__ void __launch_bounds__(32 * kPlanWarps)
+    kv_chunk_plan_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ ChunkGeo geo) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const long long place = (long long)blockIdx.x * kPlanWarps + (threadIdx.x >> 5);
+  if (place >= row_tiles(a)) return;
+  RowTile t{-1, 0, 0, 0};
+  for (int b0 = 0; b0 < a.b.B; b0 += 32) {
+    Seq s{0, 0, 0};
+    long long rt = 0;
+    if (b0 + lane < a.b.B) {
+      s = sequence(a, b0 + lane, false);
+      rt = place - ((long long)s.r0 * a.group / kTileRows + b0 + lane);
+    }
+    const uint32_t mine = __ballot_sync(0xffffffffu, s.len > 0 && rt >= 0 && rt * kTileRows < (long long)s.n * a.group);
+    if (mine == 0) continue;
+    const int from = __ffs(mine) - 1;
+    t.b = b0 + from;
+    t.rt = __shfl_sync(0xffffffffu, (int)rt, from);
+    s.r0 = __shfl_sync(0xffffffffu, s.r0, from);
+    s.n = __shfl_sync(0xffffffffu, s.n, from);
+    s.len = __shfl_sync(0xffffffffu, s.len, from);
+    t.k1 = blocks_of(geo, a.c.page_size, s.len);
+    if (a.ranges) {
+      int lo = 0x7fffffff, hi = 0;
+      const int row0 = t.rt * kTileRows, last = (min(row0 + kTileRows, s.n * a.group) - 1) / a.group;
+      for (int i = row0 / a.group + lane; i <= last; i += 32) {
+        int x, y;
+        seen_range(a, s.r0 + i, s.len, &x, &y);
+        if (x < y) lo = min(lo, x), hi = max(hi, y);
+      }
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      t.k0 = hi > 0 ? block_of_key(geo, a.c.page_size, lo) : 0;
+      t.k1 = hi > 0 ? block_of_key(geo, a.c.page_size, hi - 1) + 1 : 1;
+    }
+    break;
+  }
+  if (lane == 0) space<64>(a, 0).tiles[place] = t;
 }
 
 // A run: blocks [k0, k1) of one row tile and head.
 struct alignas(16) Run {
   Seq s;
-  int b, rt, h, row0, cnt;
-  int k0, k1, blocks;
+  int b, h, row0, cnt;
+  int k0, k1;
+  int first, last;           // of the tile's blocks [first, last)
   int units;                 // what it takes of the line
   int lo, hi;                // keys that some row sees
   int all_lo[2], all_hi[2];  // per half: keys that every row sees
@@ -303,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int G = gridDim.x, me = blockIdx.x;
-  const Space ws = space<DP>(a.workspace, G);
+  const Space ws = space<DP>(a, G);
   const int page_size = a.c.page_size;
   int* const err = a.b.status;
 
@@ -335,9 +383,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const Piece pc =
-      cut_line<kThreads / 32, 1>(a.b.B, kPairUnits, reinterpret_cast<long long*>(half_ml),
-                                            [&](int b) { return tiles_of(a, geo, sequence(a, b, false)).all; });
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the plan
+  auto units = [&](const RowTile& t, int w) { return (long long)(kRunUnits + w * (t.k1 - t.k0)); };
+  const Piece pc = cut_line<kThreads / 32, 1>((int)row_tiles(a), kLeast, reinterpret_cast<long long*>(half_ml), [&](int i) {
+    const RowTile t = ws.tiles[i];
+    return t.b < 0 ? 0 : a.c.heads * units(t, tile_weight(a, sequence(a, t.b, false), t.rt));
+  });
   if (threadIdx.x == 0) ws.open[me].parts = 0;
   tc_fence_before();
   __syncthreads();
@@ -347,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // half t: S at tS (+ 128 t if it has its own), P at tP + 64 t, O at tO + DP t
   const uint32_t tS = tmem, tP = tmem + (kTwoS ? 256 : 128), tO = tP + 128;
 
-  int b = pc.b;
+  int i = pc.b;
   long long at = pc.at;
   int it = 0;                 // blocks so far (all roles count alike)
   int ns[2] = {0, 0};         // blocks of each half so far
@@ -355,28 +406,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (long long line = pc.beg; line < pc.end;) {
     // ------------------------------------------------------------- the next run
     if (threadIdx.x == 0) {
-      Seq s = sequence(a, b, false);
-      Tiles tl = tiles_of(a, geo, s);
-      while (at >= tl.all) {
-        at -= tl.all;
-        s = sequence(a, ++b, false);
-        tl = tiles_of(a, geo, s);
+      RowTile t = ws.tiles[i];
+      Seq s{0, 0, 0};
+      long long n = 0;  // units of a head
+      int w = 0;
+      for (;;) {
+        if (t.b >= 0) {
+          s = sequence(a, t.b, false);
+          w = tile_weight(a, s, t.rt);
+          n = units(t, w);
+          if (at < a.c.heads * n) break;
+          at -= a.c.heads * n;
+        }
+        if (++i >= row_tiles(a)) break;  // (the tables changed under the call)
+        t = ws.tiles[i];
       }
-      const bool pairs = at < tl.of_pairs;
-      const long long in = pairs ? at : at - tl.of_pairs;
-      const int w = pairs ? kPairUnits : kSingleUnits, n = w * tl.blocks;
-      const int seg = (int)(in / n) + (pairs ? 0 : tl.pairs * a.c.heads), u0 = (int)(in % n);
-      const int u1 = (int)min((long long)n, u0 + (pc.end - line));
+      if (i >= row_tiles(a)) {
+        t = RowTile{0, 0, 0, 0};
+        at = 0;
+        n = pc.end - line;
+        w = 1;
+      }
+      const int h = (int)quotient(at, n), u0 = (int)(at - h * n), u1 = (int)min(n, u0 + (pc.end - line));
       run->s = s;
-      run->b = b;
-      run->rt = seg / a.c.heads;
-      run->h = seg - run->rt * a.c.heads;
-      run->row0 = run->rt * kTileRows;
+      run->b = t.b;
+      run->h = h;
+      run->row0 = t.rt * kTileRows;
       run->cnt = min(kTileRows, s.n * a.group - run->row0);
-      run->blocks = tl.blocks;
+      run->first = t.k0;
+      run->last = t.k1;
       // a block belongs to the piece that holds its last unit
-      run->k0 = u0 / w;
-      run->k1 = u1 / w;
+      run->k0 = t.k0 + max(0, u0 - kRunUnits) / w;
+      run->k1 = t.k0 + max(0, u1 - kRunUnits) / w;
       run->units = u1 - u0;
       run->lo = 0x7fffffff;
       run->hi = 0;
@@ -387,8 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       run->odd_lo = 0x7fffffff;
       run->odd_hi = -1;
       at += u1 - u0;
-      if (run->k0 == 0 && run->k1 > 0 && run->k1 < tl.blocks)
-        ws.open[me] = Open{pc.holder(line + n - u0 - 1) - me, run->h, run->row0, run->cnt, s, 0};
+      if (run->k0 == t.k0 && run->k1 > t.k0 && run->k1 < t.k1)
+        ws.open[me] = Open{pc.holder(line + n - u0 - 1) - me, h, run->row0, run->cnt, s, 0};
     }
     __syncthreads();
     const int h = run->h, row0 = run->row0, cnt = run->cnt, k0 = run->k0, k1 = run->k1;
@@ -396,6 +457,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool split = cnt <= kHalfRows;  // both halves hold the same rows and take the blocks in turn
     const int half = (warp - 4) >> 2;     // softmax warps
     line += run->units;
+    if (k0 == k1) {  // only units of a block that the next piece holds
+      __syncthreads();
+      continue;
+    }
     // softmax threads: the row (TMEM lane) in their half, and the keys that it sees
     const int hrow = 32 * (warp & 3) + lane;
     const int row = (split ? 0 : half * kHalfRows) + hrow;
@@ -575,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) *stop = 1;
-    } else if (warp >= 4 && k0 < k1) {
+    } else if (warp >= 4) {
       // -------------------------------------------------------- softmax, output
       const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
       const uint32_t myS = tS + (kTwoS ? 128 * half : 0) + lane_off, myP = tP + 64 * half + lane_off, myO = tO + DP * half + lane_off;
@@ -719,8 +784,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         wait_phase(&o_done[half], (n0 + mine - 1) & 1, err, kDevTimeoutAccum));
       if (!ok) *stop = 1;
       tc_fence_after();
-      const bool whole = k0 == 0 && k1 == run->blocks;
-      const long long part = 2LL * me + (k0 == 0 ? 1 : 0);
+      const bool whole = k0 == run->first && k1 == run->last;
+      const long long part = 2LL * me + (k0 == run->first ? 1 : 0);
       // Both halves' rows are the same: half 1 hands its sums to half 0, through
       // the room of q (which no MMA needs any more).
       float4* const other = reinterpret_cast<float4*>(sQ);  // [DP / 4][128 rows]
@@ -863,7 +928,7 @@ template <typename T, int DP>
 __global__ void __launch_bounds__(kJoinThreads) kv_chunk_join_kernel(const __grid_constant__ AttnArgs a, const int G) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int me = blockIdx.x;
-  const Space ws = space<DP>(a.workspace, G);
+  const Space ws = space<DP>(a, G);
   const Open op = ws.open[me];
   if (blockIdx.y == 0) put_empty<T>(a, me, G);  // rows of sequences without a key get their zeros here
   if (op.parts == 0) return;
@@ -875,19 +940,29 @@ __global__ void __launch_bounds__(kJoinThreads) kv_chunk_join_kernel(const __gri
     if (r >= cnt) continue;
     float m = -INFINITY, l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i <= op.parts; ++i) {
-      const long long part = 2LL * (me + i) + (i == 0 ? 1 : 0);
-      const float2 ml = ws.ml[part * kTileRows + r];
-      const float4 x = ws.o[(part * (DP / 4) + c) * kTileRows + r];
-      if (ml.y == 0.f) continue;  // nothing seen there
-      const float n = fmaxf(m, ml.x);
-      const float f = weight(m, n), g = weight(ml.x, n);
-      l = l * f + ml.y * g;
-      v.x = v.x * f + x.x * g;
-      v.y = v.y * f + x.y * g;
-      v.z = v.z * f + x.z * g;
-      v.w = v.w * f + x.w * g;
-      m = n;
+    constexpr int kAhead = 4;  // loads of as many parts are in flight together
+    for (int i0 = 0; i0 <= op.parts; i0 += kAhead) {
+      float2 ml[kAhead];
+      float4 x[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = min(i0 + u, op.parts);
+        const long long part = 2LL * (me + i) + (i == 0 ? 1 : 0);
+        ml[u] = ws.ml[part * kTileRows + r];
+        x[u] = ws.o[(part * (DP / 4) + c) * kTileRows + r];
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (i0 + u > op.parts || ml[u].y == 0.f) continue;  // none, or nothing seen there
+        const float n = fmaxf(m, ml[u].x);
+        const float f = weight(m, n), g = weight(ml[u].x, n);
+        l = l * f + ml[u].y * g;
+        v.x = v.x * f + x[u].x * g;
+        v.y = v.y * f + x[u].y * g;
+        v.z = v.z * f + x[u].z * g;
+        v.w = v.w * f + x[u].w * g;
+        m = n;
+      }
     }
     const float rl = l == 0.f ? 0.f : 1.f / l;
     if (4 * c < a.c.D) {
@@ -913,18 +988,26 @@ cudaError_t go(const ChunkLaunch& L, int sms, cudaStream_t s) {
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem((const void*)kv_chunk_kernel<T, DP>, C::kSmem, &allowed);
   if (e != cudaSuccess) return e;
-  kv_chunk_kernel<T, DP><<<sms, kThreads, C::kSmem, s>>>(L.k, L.v, L.a, L.geo);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  // each may start as the kernel before it drains, and waits for its end
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sms, 16);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = s;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
+  cfg.stream = s;
+  cfg.gridDim = dim3((unsigned)((row_tiles(L.a) + kPlanWarps - 1) / kPlanWarps));
+  cfg.blockDim = dim3(32 * kPlanWarps);
+  e = cudaLaunchKernelEx(&cfg, kv_chunk_plan_kernel, L.a, L.geo);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(sms);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  e = cudaLaunchKernelEx(&cfg, kv_chunk_kernel<T, DP>, L.k, L.v, L.a, L.geo);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(sms, 16);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, kv_chunk_join_kernel<T, DP>, L.a, sms);
 }
 
@@ -942,7 +1025,7 @@ bool kv_chunk_geometry(const AttnArgs& a, ChunkGeo* g) {
 
 long long kv_chunk_workspace(const AttnArgs& a, int sms) {
   const int DP = a.c.D <= 64 ? 64 : 128;
-  return (long long)sms * (sizeof(Open) + 2 * kTileRows * (sizeof(float2) + (size_t)DP * sizeof(float)));
+  return row_tiles(a) * (long long)sizeof(RowTile) + (long long)sms * (sizeof(Open) + 2 * kTileRows * (sizeof(float2) + (size_t)DP * sizeof(float)));
 }
 
 cudaError_t launch_kv_chunk(const ChunkLaunch& L, int sms, cudaStream_t s) {
