@@ -347,6 +347,21 @@ def test_attention_of_many_tokens(wv, case, dtype):
     assert torch.equal(again, got[:T])
 
 
+# heads of more than 128 channels (one half of a tile's rows), pages in part and in parts, pieces that meet in a tile
+WIDE = [
+    ([64], [64], 1, 1, 256, 16, "causal"), ([700, 33], [300, 33], 2, 2, 256, 64, "causal"), ([900], [440], 3, 1, 136, 220, "frames"),
+    ([513, 1000], [257, 512], 2, 5, 192, 24, "causal"), ([350], [350], 2, 2, 200, 390, "documents"),
+    ([300], [128], 1, 8, 256, 128, "window"), ([260, 130], [260, 130], 1, 1, 144, 8, "holes"), ([4000], [200], 1, 1, 256, 256, None),
+    ([0, 150], [70, 150], 1, 16, 256, 16, "holes"),
+]
+
+
+@pytest.mark.parametrize("dtype", HALVES, ids=str)
+@pytest.mark.parametrize("case", WIDE, ids=lambda c: "t{}n{}h{}g{}d{}p{}{}".format(sum(c[1]), max(c[0]), *c[2:6], c[6] or ""))
+def test_attention_of_wide_heads(wv, case, dtype):
+    test_attention_of_many_tokens(wv, case, dtype)
+
+
 @pytest.mark.parametrize("new", [[1, 1], [3, 2], [150, 200]], ids=str)
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
 def test_attention_scales(wv, new, scale):

@@ -48,20 +48,26 @@ namespace {
 // half 1: a thread per row (TMEM lane).
 constexpr int kThreads = 384;
 constexpr int kHalfRows = 128;
-constexpr int kTileRows = 256;
 constexpr int kBlock = 128;       // key columns of a block
 constexpr int kBoxBytes = 16384;  // 128 rows x 64 channels
 constexpr int kLeast = 5;         // units of a piece: a block's (with ten blocks' calls of 100 tokens take 42 us instead of 21)
 constexpr float kSlack = 8.f;    // log2 units that the reference maximum may lag behind
 
+// Rows of a row tile: at a head dim above 128 O takes half of TMEM, which leaves room for one half.
+__host__ __device__ inline constexpr int tile_rows(int D) { return D > 128 ? kHalfRows : 2 * kHalfRows; }
+
 template <int DP>
 struct Cfg {
+  static constexpr bool kOne = DP > 128;  // one half (warps 8-11 have nothing to do)
+  static constexpr int kRows = tile_rows(DP);
   static constexpr int ND = DP / 64;
-  static constexpr int kSlot = ND * kBoxBytes;          // K or V of a block
+  // K or V of a block fill a slot; at 256 channels a slot holds 64 of them and a block takes as many as it has channels
+  static constexpr int kBoxes = kOne ? 1 : ND;  // 64-channel boxes of a slot
+  static constexpr int kSlot = kBoxes * kBoxBytes;
   // K and V have a ring each: a barrier is then waited for by one warp, phase by phase, and a parity never stands for
   // another lap of the ring than the next
   static constexpr int kKeySlots = DP == 128 ? 2 : 5, kStages = DP == 128 ? 5 : 10;
-  static constexpr int kQ = 2 * ND * kBoxBytes;
+  static constexpr int kQ = (kOne ? 1 : 2) * ND * kBoxBytes;
   static constexpr int kSmem = kQ + kStages * kSlot + 1024 + 1024;
 };
 
@@ -228,16 +234,16 @@ __device__ __forceinline__ void block_keys(const ChunkGeo& g, int page_size, int
   }
 }
 
-// A row tile: up to 256 rows of a sequence, and the blocks [k0, k1) that some of
+// A row tile: up to tile_rows rows of a sequence, and the blocks [k0, k1) that some of
 // them see (one block if they see none: it leaves their zeros).
 struct RowTile {
   int b, rt;  // b < 0: none
   int k0, k1;
 };
 // Room for the row tiles of T tokens in B sequences; those of a sequence that starts at row r0 stand from r0 * group /
-// 256 + b on, so that sequences never meet.
+// tile_rows + b on, so that sequences never meet.
 __host__ __device__ inline long long row_tiles(const AttnArgs& a) {
-  return (long long)a.b.T * a.group / kTileRows + a.b.B;
+  return (long long)a.b.T * a.group / tile_rows(a.c.D) + a.b.B;
 }
 
 // What a row tile with a head takes of the line: kRunUnits (start, end and the blocks at a mask's edge), and for each
@@ -246,14 +252,14 @@ __host__ __device__ inline long long row_tiles(const AttnArgs& a) {
 // fast as a larger one would at twice the speed.)
 constexpr int kPairUnits = 5, kSingleUnits = 4, kRunUnits = 50;
 __device__ __forceinline__ int tile_weight(const AttnArgs& a, const Seq& s, int rt) {
-  return s.n * a.group - rt * kTileRows <= kHalfRows ? kSingleUnits : kPairUnits;
+  return a.c.D <= 128 && s.n * a.group - rt * tile_rows(a.c.D) <= kHalfRows ? kSingleUnits : kPairUnits;
 }
 
 struct Space {
   RowTile* tiles;
   Open* open;
-  float2* ml;  // [2 G][kTileRows]
-  float4* o;   // [2 G][DP / 4][kTileRows]: the rows side by side
+  float2* ml;  // [2 G][rows of a tile]
+  float4* o;   // [2 G][DP / 4][rows of a tile]: the rows side by side
 };
 template <int DP>
 __host__ __device__ inline Space space(const AttnArgs& a, int G) {
@@ -261,7 +267,7 @@ __host__ __device__ inline Space space(const AttnArgs& a, int G) {
   s.tiles = (RowTile*)a.workspace;
   s.open = (Open*)(s.tiles + row_tiles(a));
   s.ml = (float2*)(s.open + G);
-  s.o = (float4*)(s.ml + (size_t)2 * G * kTileRows);
+  s.o = (float4*)(s.ml + (size_t)2 * G * Cfg<DP>::kRows);
   return s;
 }
 
@@ -271,7 +277,7 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
     kv_chunk_plan_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ ChunkGeo geo) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, tile = tile_rows(a.c.D);
   const long long place = (long long)blockIdx.x * kPlanWarps + (threadIdx.x >> 5);
   if (place >= row_tiles(a)) return;
   RowTile t{-1, 0, 0, 0};
@@ -280,9 +286,9 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
     long long rt = 0;
     if (b0 + lane < a.b.B) {
       s = sequence(a, b0 + lane, false);
-      rt = place - ((long long)s.r0 * a.group / kTileRows + b0 + lane);
+      rt = place - ((long long)s.r0 * a.group / tile + b0 + lane);
     }
-    const uint32_t mine = __ballot_sync(0xffffffffu, s.len > 0 && rt >= 0 && rt * kTileRows < (long long)s.n * a.group);
+    const uint32_t mine = __ballot_sync(0xffffffffu, s.len > 0 && rt >= 0 && rt * tile < (long long)s.n * a.group);
     if (mine == 0) continue;
     const int from = __ffs(mine) - 1;
     t.b = b0 + from;
@@ -293,7 +299,7 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
     t.k1 = blocks_of(geo, a.c.page_size, s.len);
     if (a.ranges) {
       int lo = 0x7fffffff, hi = 0;
-      const int row0 = t.rt * kTileRows, last = (min(row0 + kTileRows, s.n * a.group) - 1) / a.group;
+      const int row0 = t.rt * tile, last = (min(row0 + tile, s.n * a.group) - 1) / a.group;
       for (int i = row0 / a.group + lane; i <= last; i += 32) {
         int x, y;
         seen_range(a, s.r0 + i, s.len, &x, &y);
@@ -326,7 +332,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     kv_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                     const __grid_constant__ AttnArgs a, const __grid_constant__ ChunkGeo geo) {
   using C = Cfg<DP>;
-  constexpr int S = C::kStages, SK = C::kKeySlots, SV = S - SK, ND = C::ND;
+  constexpr int S = C::kStages, SK = C::kKeySlots, SV = S - SK, ND = C::ND, NB = C::kBoxes, kRows = C::kRows;
+  constexpr bool kOne = C::kOne;
+  constexpr int kSoftEnd = kOne ? 8 : 12;  // softmax warps are 4 up to this one
   // the only shared memory of the kernel, so it starts on a 1024-byte boundary, as the swizzled boxes must
   extern __shared__ __align__(1024) uint8_t smem[];
   static_assert(sizeof(Run) + 8 * (2 * S + 10) + 8 + 128 + 16 <= 1024, "barriers and the run's description");
@@ -431,8 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       run->s = s;
       run->b = t.b;
       run->h = h;
-      run->row0 = t.rt * kTileRows;
-      run->cnt = min(kTileRows, s.n * a.group - run->row0);
+      run->row0 = t.rt * kRows;
+      run->cnt = min(kRows, s.n * a.group - run->row0);
       run->first = t.k0;
       run->last = t.k1;
       // a block belongs to the piece that holds its last unit
@@ -454,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     const int h = run->h, row0 = run->row0, cnt = run->cnt, k0 = run->k0, k1 = run->k1;
     const Seq s = run->s;
-    const bool split = cnt <= kHalfRows;  // both halves hold the same rows and take the blocks in turn
+    const bool split = !kOne && cnt <= kHalfRows;  // both halves hold the same rows and take the blocks in turn
     const int half = (warp - 4) >> 2;     // softmax warps
     line += run->units;
     if (k0 == k1) {  // only units of a block that the next piece holds
@@ -464,9 +472,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // softmax threads: the row (TMEM lane) in their half, and the keys that it sees
     const int hrow = 32 * (warp & 3) + lane;
     const int row = (split ? 0 : half * kHalfRows) + hrow;
-    const bool real = warp >= 4 && row < cnt;
+    const bool softmax = warp >= 4 && warp < kSoftEnd, real = softmax && row < cnt;
     int lo = 0, hi = 0x40000000;  // rows past the tile's see everything: they need no mask
-    if (warp >= 4) {
+    if (softmax) {
       if (real) {
         seen_range(a, s.r0 + (row0 + row) / a.group, s.len, &lo, &hi);
         if (lo < hi) {
@@ -508,7 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int j1 = run->hi > 0 ? min(k1, block_of_key(geo, page_size, run->hi - 1) + 1) : k1;
     const int nb = max(0, j1 - j0);
     // blocks of each half
-    const int nh[2] = {split ? (nb + 1) / 2 : nb, split ? nb / 2 : nb};
+    const int nh[2] = {split ? (nb + 1) / 2 : nb, kOne ? 0 : split ? nb / 2 : nb};
+    const int pb = kOne ? (a.c.D + 63) / 64 : 1;  // slots of a block
     bool ok = true;
 
     if (warp == 0 || warp == 3) {
@@ -517,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const CUtensorMap* map = ofK ? &mapK : &mapV;
       const int* table = a.b.pages + run->b * a.b.page_stride;
       const int held = (s.len + page_size - 1) / page_size;  // pages of the sequence
-      const int bytes = geo.parts == 1 ? geo.pages * geo.box_rows * 128 * ND : C::kSlot;
+      const int bytes = geo.parts == 1 ? geo.pages * geo.box_rows * 128 * NB : C::kSlot;
       // All counted along: a division here would queue behind the softmax's exponentials.  The lane's page of block
       // j: its place `idx` in the table and the rows `off` of it that come first; asked for two blocks ahead.
       int idx = geo.parts == 1 ? j0 * geo.pages + lane : j0 / geo.parts, part = geo.parts == 1 ? 0 : j0 - idx * geo.parts;
@@ -534,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       int page = entry(0), next = entry(1);
       const int slots = ofK ? SK : SV, first = ofK ? 0 : SK;
-      int slot = it % slots, lap = it / slots;
+      int slot = it * pb % slots, lap = it * pb / slots;
       for (int n = 0; n < nb && ok; ++n) {
         const int after = entry(n + 2);
         const int off = part * kBlock;
@@ -548,27 +557,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t nones = __ballot_sync(0xffffffffu, none);
           if (lane == 0) hole[(j0 + n) & 31] = nones;
         }
-        int good = 1;
-        if (lane == 0) {
-          if (lap > 0) good = wait_phase(&empty[first + slot], (lap - 1) & 1, err, kDevTimeoutEmpty);
-          if (*stop) good = 0;
-          if (good) mbar_arrive_expect_tx(smem_u32(&full[first + slot]), bytes);
-        }
-        ok = __shfl_sync(0xffffffffu, good, 0);
-        if (!ok) break;
-        if (lane < geo.pages) {  // one box per lane, of the page that the lane holds
-          int c[3];
-          c[geo.dim_row] = off;
-          c[geo.dim_head] = h;
-          c[geo.dim_page] = page;
-          const uint32_t d = smem_u32(sR + (first + slot) * C::kSlot) + lane * geo.box_rows * 128;
+        for (int u = 0; u < pb && ok; ++u) {
+          int good = 1;
+          if (lane == 0) {
+            if (lap > 0) good = wait_phase(&empty[first + slot], (lap - 1) & 1, err, kDevTimeoutEmpty);
+            if (*stop) good = 0;
+            if (good) mbar_arrive_expect_tx(smem_u32(&full[first + slot]), bytes);
+          }
+          ok = __shfl_sync(0xffffffffu, good, 0);
+          if (!ok) break;
+          if (lane < geo.pages) {  // one box per lane, of the page that the lane holds
+            int c[3];
+            c[geo.dim_row] = off;
+            c[geo.dim_head] = h;
+            c[geo.dim_page] = page;
+            const uint32_t d = smem_u32(sR + (first + slot) * C::kSlot) + lane * geo.box_rows * 128;
 #pragma unroll
-          for (int u = 0; u < ND; ++u)
-            tma_load_4d(d + u * kBoxBytes, map, smem_u32(&full[first + slot]), 64 * u, c[0], c[1], c[2]);
+            for (int v = 0; v < NB; ++v)
+              tma_load_4d(d + v * kBoxBytes, map, smem_u32(&full[first + slot]), 64 * (u * NB + v), c[0], c[1], c[2]);
+          }
+          if (++slot == slots) slot = 0, ++lap;
         }
         page = next;
         next = after;
-        if (++slot == slots) slot = 0, ++lap;
       }
       if (!ok) *stop = 1;
     } else if ((warp == 1 || warp == 2) && nb > 0) {
@@ -580,67 +591,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       // each warp goes by its own barriers.
       const int dn = (a.c.D + 15) / 16;  // k steps of S, N / 16 of O
       const bool one = elect();
-      const int steps = split ? nb : 2 * nb;
+      const bool turns = !split && !kOne;  // both halves take every block
+      const int steps = turns ? 2 * nb : nb;
       if (warp == 1) {
-        int slot = it % SK, phase = (it / SK) & 1;
         const uint32_t idS = idesc(Pack<T>::kFormat, false, kBlock);
         const uint32_t q0 = desc_k(smem_u32(sQ)), kd0 = desc_k(smem_u32(sR));
-        uint32_t there = 0;  // the block's K is known to be there (asked a step ahead)
+        int slot = it * pb % SK, phase = (it * pb / SK) & 1;
+        uint32_t there = 0;  // the block's K (its first slot) is known to be there (asked a step ahead)
         for (int g = 0; g < steps; ++g) {
-          const int t = g & 1, n = split ? g : g >> 1;
-          if ((split || t == 0) && !__all_sync(0xffffffffu, there))  // K of its block
-            ok = wait_phase(&full[slot], phase, err, kDevTimeoutFull);
+          const int t = kOne ? 0 : g & 1;
+          const bool starts = !turns || t == 0, ends = !turns || t == 1;  // the block's first and last step
+          if (starts && !__all_sync(0xffffffffu, there)) ok = wait_phase(&full[slot], phase, err, kDevTimeoutFull);
           // the S buffer, once the step that used it last (the half's own, or the other's) has been read
           if (kTwoS) {
             if (g > 1 && ok) ok = wait_phase(&s_free[t], (ns[t] + (g >> 1) - 1) & 1, err, kDevTimeoutAccum);
+          } else if (kOne) {
+            if (g > 0 && ok) ok = wait_phase(&s_free[0], (ns[0] + g - 1) & 1, err, kDevTimeoutAccum);
           } else {
             if (g > 0 && ok) ok = wait_phase(&s_free[t ^ 1], (ns[t ^ 1] + ((g - 1) >> 1)) & 1, err, kDevTimeoutAccum);
           }
           if (!ok) break;
           tc_fence_after();
-          const uint32_t q = q0 + t * (ND * kBoxBytes >> 4), k = kd0 + slot * (C::kSlot >> 4);
-          if (one) {
+          const uint32_t q = q0 + t * (ND * kBoxBytes >> 4), s_at = tS + (kTwoS ? 128 * t : 0);
+          for (int u = 0; u < pb; ++u) {
+            if (kOne && u > 0) {
+              ok = wait_phase(&full[slot], phase, err, kDevTimeoutFull);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            const uint32_t k = kd0 + slot * (C::kSlot >> 4), qu = q + u * (kBoxBytes >> 4);
+            if (one) {
 #pragma unroll
-            for (int e = 0; e < 4 * ND; ++e)
-              if (e < dn)
-                umma_ss(tS + (kTwoS ? 128 * t : 0), q + (e >> 2) * (kBoxBytes >> 4) + 2 * (e & 3), k + (e >> 2) * (kBoxBytes >> 4) + 2 * (e & 3),
-                        idS, e > 0);
-            umma_commit(smem_u32(&s_full[t]));
-            if (split || t == 1) umma_commit(smem_u32(&empty[slot]));
+              for (int e = 0; e < 4 * NB; ++e)
+                if (4 * u + e < dn)
+                  umma_ss(s_at, qu + (e >> 2) * (kBoxBytes >> 4) + 2 * (e & 3), k + (e >> 2) * (kBoxBytes >> 4) + 2 * (e & 3),
+                          idS, u > 0 || e > 0);
+              if (u == pb - 1) umma_commit(smem_u32(&s_full[t]));
+              if (ends) umma_commit(smem_u32(&empty[slot]));
+            }
+            if (ends && ++slot == SK) slot = 0, phase ^= 1;
           }
-          if (split || t == 1) {
-            if (++slot == SK) slot = 0, phase ^= 1;
-            there = n + 1 < nb && ask_phase(&full[slot], phase);
-          }
+          if (!ok) break;
+          if (ends) there = g + 1 < steps && ask_phase(&full[slot], phase);
         }
       } else {
-        const uint32_t idO = idesc(Pack<T>::kFormat, true, 16 * dn);
         const uint32_t vd0 = desc_v(smem_u32(sR));
-        int slot = SK + it % SV, phase = (it / SV) & 1;
+        int slot = SK + it * pb % SV, phase = (it * pb / SV) & 1;
         uint32_t there = 0;
         for (int g = 0; g < steps; ++g) {
-          const int t = g & 1, n = split ? g : g >> 1;
-          if ((split || t == 0) && !__all_sync(0xffffffffu, there))  // V of its block
-            ok = wait_phase(&full[slot], phase, err, kDevTimeoutFull);
-          if (ok) ok = wait_phase(&p_full[t], (ns[t] + (g >> 1)) & 1, err, kDevTimeoutAccum);
+          const int t = kOne ? 0 : g & 1, i = kOne ? g : g >> 1;
+          const bool starts = !turns || t == 0, ends = !turns || t == 1;
+          if (starts && !__all_sync(0xffffffffu, there)) ok = wait_phase(&full[slot], phase, err, kDevTimeoutFull);
+          if (ok) ok = wait_phase(&p_full[t], (ns[t] + i) & 1, err, kDevTimeoutAccum);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t v = vd0 + slot * (C::kSlot >> 4), p = tP + 64 * t;
-          if (one) {
+          for (int u = 0; u < pb; ++u) {
+            if (kOne && u > 0) {
+              ok = wait_phase(&full[slot], phase, err, kDevTimeoutFull);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            const uint32_t v = vd0 + slot * (C::kSlot >> 4), p = tP + 64 * t;
+            const uint32_t idO = idesc(Pack<T>::kFormat, true, 16 * min(4 * NB, dn - 4 * u));
+            if (one) {
 #pragma unroll
-            for (int e = 0; e < kBlock / 16; ++e) umma_ts(tO + DP * t, p + 8 * e, v + 128 * e, idO, g > 1 || e > 0);
-            umma_commit(smem_u32(&o_done[t]));
-            if (split || t == 1) umma_commit(smem_u32(&empty[slot]));
+              for (int e = 0; e < kBlock / 16; ++e) umma_ts(tO + DP * t + 64 * u, p + 8 * e, v + 128 * e, idO, i > 0 || e > 0);
+              if (u == pb - 1) umma_commit(smem_u32(&o_done[t]));
+              if (ends) umma_commit(smem_u32(&empty[slot]));
+            }
+            if (ends && ++slot == S) slot = SK, phase ^= 1;
           }
-          if (split || t == 1) {
-            if (++slot == S) slot = SK, phase ^= 1;
-            there = n + 1 < nb && ask_phase(&full[slot], phase);
-          }
+          if (!ok) break;
+          if (ends) there = g + 1 < steps && ask_phase(&full[slot], phase);
         }
       }
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) *stop = 1;
-    } else if (warp >= 4) {
+    } else if (softmax) {
       // -------------------------------------------------------- softmax, output
       const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
       const uint32_t myS = tS + (kTwoS ? 128 * half : 0) + lane_off, myP = tP + 64 * half + lane_off, myO = tO + DP * half + lane_off;
@@ -702,22 +729,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           // among their values must not meet a weight of zero.  Such values leave
           // the block here, and the rows that see them get them at the end.
           if (base < all_lo || base + rows > all_hi) {
-            const int at_v = it + j - j0;
+            const int at_v = (it + j - j0) * pb;
             // (this half's last P V has read its V, so every lap of the ring before this block's is known to be there)
             if (i > 0) ok = wait_phase(&o_done[half], (n0 + i - 1) & 1, err, kDevTimeoutAccum);
-            if (ok) ok = wait_phase(&full[SK + at_v % SV], (at_v / SV) & 1, err, kDevTimeoutFull);
+            for (int u = 0; u < pb && ok; ++u) ok = wait_phase(&full[SK + (at_v + u) % SV], ((at_v + u) / SV) & 1, err, kDevTimeoutFull);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            uint4* v = reinterpret_cast<uint4*>(sR + (SK + at_v % SV) * C::kSlot);
-            for (int e = hrow; e < C::kSlot / 16; e += kHalfRows) {
-              const uint4 w = v[e];
-              if (odd32<T>(w.x) || odd32<T>(w.y) || odd32<T>(w.z) || odd32<T>(w.w)) {
-                atomicMin(&run->odd_lo, j);
-                atomicMax(&run->odd_hi, j);
-                __threadfence_block();
-                uint16_t* u = reinterpret_cast<uint16_t*>(v + e);
-                for (int k = 0; k < 8; ++k)
-                  if (odd16<T>(u[k])) u[k] = 0;
+            for (int u = 0; u < pb; ++u) {
+              uint4* v = reinterpret_cast<uint4*>(sR + (SK + (at_v + u) % SV) * C::kSlot);
+              for (int e = hrow; e < C::kSlot / 16; e += kHalfRows) {
+                const uint4 w = v[e];
+                if (odd32<T>(w.x) || odd32<T>(w.y) || odd32<T>(w.z) || odd32<T>(w.w)) {
+                  atomicMin(&run->odd_lo, j);
+                  atomicMax(&run->odd_hi, j);
+                  __threadfence_block();
+                  uint16_t* h16 = reinterpret_cast<uint16_t*>(v + e);
+                  for (int k = 0; k < 8; ++k)
+                    if (odd16<T>(h16[k])) h16[k] = 0;
+                }
               }
             }
             fence_proxy_async_smem();
@@ -868,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (real && !whole) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              ws.o[(part * (DP / 4) + 4 * c + e) * kTileRows + row] =
+              ws.o[(part * (DP / 4) + 4 * c + e) * kRows + row] =
                   make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
           } else if (real) {
             uint32_t w[8];
@@ -887,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (real) {
           if (whole) put_lse(a, s, h, row0 + row, ref, l);
-          else ws.ml[part * kTileRows + row] = make_float2(ref, l);
+          else ws.ml[part * kRows + row] = make_float2(ref, l);
         }
       }
     }
@@ -927,6 +956,7 @@ constexpr int kJoinThreads = 256;
 template <typename T, int DP>
 __global__ void __launch_bounds__(kJoinThreads) kv_chunk_join_kernel(const __grid_constant__ AttnArgs a, const int G) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kRows = Cfg<DP>::kRows;
   const int me = blockIdx.x;
   const Space ws = space<DP>(a, G);
   const Open op = ws.open[me];
@@ -934,7 +964,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_chunk_join_kernel(const __gri
   if (op.parts == 0) return;
   const int row0 = op.row0, cnt = op.cnt;
   const int lane = threadIdx.x & 31;
-  for (int w = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); w < kTileRows / 8 * (DP / 16);
+  for (int w = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); w < kRows / 8 * (DP / 16);
        w += gridDim.y * (kJoinThreads / 32)) {
     const int r = w / (DP / 16) * 8 + (lane & 7), c = w % (DP / 16) * 4 + (lane >> 3);  // row, four channels
     if (r >= cnt) continue;
@@ -948,8 +978,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv_chunk_join_kernel(const __gri
       for (int u = 0; u < kAhead; ++u) {
         const int i = min(i0 + u, op.parts);
         const long long part = 2LL * (me + i) + (i == 0 ? 1 : 0);
-        ml[u] = ws.ml[part * kTileRows + r];
-        x[u] = ws.o[(part * (DP / 4) + c) * kTileRows + r];
+        ml[u] = ws.ml[part * kRows + r];
+        x[u] = ws.o[(part * (DP / 4) + c) * kRows + r];
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
@@ -1015,7 +1045,6 @@ cudaError_t go(const ChunkLaunch& L, int sms, cudaStream_t s) {
 
 bool kv_chunk_geometry(const AttnArgs& a, ChunkGeo* g) {
   const int ps = a.c.page_size;
-  if (a.c.D > 128) return false;
   g->box_rows = ps >= kBlock ? kBlock : (ps + 7) / 8 * 8;
   g->parts = ps > kBlock ? (ps + kBlock - 1) / kBlock : 1;
   g->pages = g->parts > 1 ? 1 : kBlock / g->box_rows;
@@ -1024,13 +1053,15 @@ bool kv_chunk_geometry(const AttnArgs& a, ChunkGeo* g) {
 }
 
 long long kv_chunk_workspace(const AttnArgs& a, int sms) {
-  const int DP = a.c.D <= 64 ? 64 : 128;
-  return row_tiles(a) * (long long)sizeof(RowTile) + (long long)sms * (sizeof(Open) + 2 * kTileRows * (sizeof(float2) + (size_t)DP * sizeof(float)));
+  const int DP = a.c.D <= 64 ? 64 : a.c.D <= 128 ? 128 : 256;
+  return row_tiles(a) * (long long)sizeof(RowTile) + (long long)sms * (sizeof(Open) + 2 * tile_rows(DP) * (sizeof(float2) + (size_t)DP * sizeof(float)));
 }
 
 cudaError_t launch_kv_chunk(const ChunkLaunch& L, int sms, cudaStream_t s) {
-  if (L.a.c.elem == 1) return L.a.c.D <= 64 ? go<__nv_bfloat16, 64>(L, sms, s) : go<__nv_bfloat16, 128>(L, sms, s);
-  return L.a.c.D <= 64 ? go<__half, 64>(L, sms, s) : go<__half, 128>(L, sms, s);
+  const bool bf16 = L.a.c.elem == 1;
+  if (L.a.c.D <= 64) return bf16 ? go<__nv_bfloat16, 64>(L, sms, s) : go<__half, 64>(L, sms, s);
+  if (L.a.c.D <= 128) return bf16 ? go<__nv_bfloat16, 128>(L, sms, s) : go<__half, 128>(L, sms, s);
+  return bf16 ? go<__nv_bfloat16, 256>(L, sms, s) : go<__half, 256>(L, sms, s);
 }
 
 }  // namespace wan

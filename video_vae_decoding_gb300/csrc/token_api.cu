@@ -100,6 +100,10 @@ constexpr int kChunkRows = 64;
 bool chunk_rows(const AttnArgs& a, ChunkGeo* g) {
   return (int64_t)a.b.T * a.group >= (int64_t)kChunkRows * a.b.B && kv_chunk_geometry(a, g);
 }
+int64_t workspace_of(const AttnArgs& a, bool chunk, int sms) {
+  const int64_t split = kv_attention_workspace(a, sms);
+  return chunk ? std::max<int64_t>(split, kv_chunk_workspace(a, sms)) : split;
+}
 
 // Tensor map over a cache: channels, then rows, heads and pages in the order of
 // their strides.  False if the strides cannot be described.
@@ -320,7 +324,7 @@ wan_status wan_kv_attention(const wan_kv_cache* cache, const wan_kv_batch* batch
     WAN_TRY(sm_count(&sms));
     ChunkLaunch L;
     bool chunk = chunk_rows(a, &L.geo);
-    const int64_t bytes = chunk ? kv_chunk_workspace(a, sms) : kv_attention_workspace(a, sms);
+    const int64_t bytes = workspace_of(a, chunk, sms);
     if (!workspace || ((uintptr_t)workspace & 15) || workspace_bytes < bytes)
       return fail(WAN_ERR_INVALID_ARG, "workspace of %lld bytes, 16-byte aligned, needed (%lld given)", (long long)bytes,
                   (long long)workspace_bytes);
@@ -330,7 +334,7 @@ wan_status wan_kv_attention(const wan_kv_cache* cache, const wan_kv_batch* batch
     a.workspace = workspace;
     if (chunk) {
       // k and v may order their dimensions differently; then, and where a map cannot be made, the split kernel runs
-      // (its workspace is the smaller one)
+      // (there is room for either)
       ChunkGeo gk = L.geo;
       chunk = cache_map(a.c, a.c.k, a.c.k_page, a.c.k_head, a.c.k_row, &gk, &L.k) &&
               cache_map(a.c, a.c.v, a.c.v_page, a.c.v_head, a.c.v_row, &L.geo, &L.v) && gk.dim_row == L.geo.dim_row &&
@@ -348,7 +352,7 @@ int64_t wan_kv_attention_workspace(const wan_kv_cache* cache, const wan_kv_batch
     int sms = 0;
     if (attention_args(cache, batch, q_heads, &a) != WAN_OK || sm_count(&sms) != WAN_OK) return -1;
     ChunkGeo g;
-    return chunk_rows(a, &g) ? kv_chunk_workspace(a, sms) : kv_attention_workspace(a, sms);
+    return workspace_of(a, chunk_rows(a, &g), sms);
   } catch (...) {
     fail(WAN_ERR_INTERNAL, "unexpected C++ exception");
     return -1;
