@@ -8,24 +8,31 @@
 //                            when a block exceeds it by 8 (O is then rescaled)
 //   O_t += P_t V_j           P_t read from tensor memory
 // and O_t / l at the end.  A softmax reads S into registers at once, so that the
-// tensor cores form its next S while it works.  TMEM: S, P_0 and P_1 of 64 columns
-// each, O_0 and O_1 of DP; at DP = 64 each half has an S of its own (128 columns),
-// at 128 there is room for one, which the halves, half a period apart, take in
-// turn.  What else was tried at D = 128, cycles per block of 128 keys and 256 rows
-// (2048 of them products):
+// tensor cores form the next S while it works.  TMEM has 512 columns: S takes 128,
+// which the halves, half a period apart, take in turn; a P 64 and an O_t DP.
+//  D <= 64    two P for each half: its P V has a block's time more.  (An S for each
+//             half instead: 280 key blocks of 512 rows take 154 us instead of 134.)
+//  D <= 128   one P for each half
+//  D <= 256   one half of 128 rows
+// What else was tried at D = 128, cycles per block of 128 keys and 256 rows (2048 of
+// them products):
 //   S_t for each half with P_t in its place    3100, and P V has to be waited for
 //                                               before the next Q K
 //   64 keys, two S buffers a half              4300: with N = 64 the first operand's
 //                                               way from shared memory, 64 cycles
 //                                               an instruction, bounds Q K
 //   one S, 16 softmax warps                    4000: they starve the issuing warps
+//   weights kept until P's room is free        2900: they do not fit the registers
 //   this                                       2600
 // A tile of at most 128 rows puts its rows in both halves, which take the key
 // blocks in turn, and adds the halves up at the end.
 //
 // Bound: the tensor cores, 4 D operations per row and key; K and V come through
-// a ring each and serve both halves, so a block of 128
-// keys asks 64 KB (D = 128) for 33.6 MFLOP.
+// a ring each and serve both halves, so a block of 128 keys asks 64 KB (D = 128) for
+// 33.6 MFLOP.  880 tokens of 16 heads of 128 against 27,280 keys take 173 us, 1.13
+// PFLOP/s (59% of a large library product's); with heads of 64 134 us, where the
+// softmax bounds, and with 8 heads of 256 252 us: 128 KB a block for 16.8 MFLOP is 8
+// TB/s from the L2.
 // V is taken as it lies in the cache, [key][channel]: the MMA's second operand
 // with its N dimension contiguous, so nothing is transposed on the way.
 //
@@ -37,6 +44,8 @@
 // The line of (sequence, row tile, head, key block) is cut into equal pieces,
 // one per SM, as in the split kernel (weighed by what a block costs in a larger
 // and in a smaller tile); the join adds up what a cut divides.
+#include <type_traits>
+
 #include "kv_common.cuh"
 #include "kv_chunk.h"
 
@@ -61,14 +70,15 @@ struct Cfg {
   static constexpr bool kOne = DP > 128;  // one half (warps 8-11 have nothing to do)
   static constexpr int kRows = tile_rows(DP);
   static constexpr int ND = DP / 64;
-  // K or V of a block fill a slot; at 256 channels a slot holds 64 of them and a block takes as many as it has channels
-  static constexpr int kBoxes = kOne ? 1 : ND;  // 64-channel boxes of a slot
-  static constexpr int kSlot = kBoxes * kBoxBytes;
+  // K or V of a block fill a slot; above 128 channels a slot holds 64 of K's or 128 of V's (a product with fewer
+  // columns of V takes no less time)
+  static constexpr int kKeyBoxes = kOne ? 1 : ND, kValBoxes = kOne ? 2 : ND;  // 64-channel boxes of a slot
+  static constexpr int kKeySlot = kKeyBoxes * kBoxBytes, kValSlot = kValBoxes * kBoxBytes;
   // K and V have a ring each: a barrier is then waited for by one warp, phase by phase, and a parity never stands for
   // another lap of the ring than the next
-  static constexpr int kKeySlots = DP == 128 ? 2 : 5, kStages = DP == 128 ? 5 : 10;
+  static constexpr int kKeySlots = DP == 64 ? 5 : DP == 128 ? 2 : 4, kValSlots = DP == 64 ? 5 : 3;
   static constexpr int kQ = (kOne ? 1 : 2) * ND * kBoxBytes;
-  static constexpr int kSmem = kQ + kStages * kSlot + 1024 + 1024;
+  static constexpr int kSmem = kQ + kKeySlots * kKeySlot + kValSlots * kValSlot + 1024 + 1024;
 };
 
 // Weights 2^(x - m) reach 2^kSlack; in float16 they are taken 2^7 times larger
@@ -250,7 +260,7 @@ __host__ __device__ inline long long row_tiles(const AttnArgs& a) {
 // block kPairUnits, or kSingleUnits in a tile of at most 128 rows.  They stand for what these cost: with 20 for a run two
 // chunks of 1300 causal tokens of 48 heads take 217 us, with 45 187, with 60 175, with 80 174.  (A smaller tile does half the arithmetic, but asks for K and V as
 // fast as a larger one would at twice the speed.)
-constexpr int kPairUnits = 5, kSingleUnits = 4, kRunUnits = 50;
+constexpr int kPairUnits = 5, kSingleUnits = 4, kRunUnits = 60;
 __device__ __forceinline__ int tile_weight(const AttnArgs& a, const Seq& s, int rt) {
   return a.c.D <= 128 && s.n * a.group - rt * tile_rows(a.c.D) <= kHalfRows ? kSingleUnits : kPairUnits;
 }
@@ -332,21 +342,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     kv_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                     const __grid_constant__ AttnArgs a, const __grid_constant__ ChunkGeo geo) {
   using C = Cfg<DP>;
-  constexpr int S = C::kStages, SK = C::kKeySlots, SV = S - SK, ND = C::ND, NB = C::kBoxes, kRows = C::kRows;
+  constexpr int SK = C::kKeySlots, SV = C::kValSlots, S = SK + SV, ND = C::ND, kRows = C::kRows;
   constexpr bool kOne = C::kOne;
   constexpr int kSoftEnd = kOne ? 8 : 12;  // softmax warps are 4 up to this one
   // the only shared memory of the kernel, so it starts on a 1024-byte boundary, as the swizzled boxes must
   extern __shared__ __align__(1024) uint8_t smem[];
-  static_assert(sizeof(Run) + 8 * (2 * S + 10) + 8 + 128 + 16 <= 1024, "barriers and the run's description");
+  static_assert(sizeof(Run) + 8 * (2 * S + 14) + 8 + 128 + 16 <= 1024, "barriers and the run's description");
   uint8_t* sQ = smem;  // [half][64-channel box][128 rows]
-  uint8_t* sR = sQ + C::kQ;  // SK slots of K, SV of V
-  uint64_t* full = reinterpret_cast<uint64_t*>(sR + S * C::kSlot);
+  uint8_t *sK = sQ + C::kQ, *sV = sK + SK * C::kKeySlot;  // SK slots of K, SV of V; their barriers in this order
+  uint64_t* full = reinterpret_cast<uint64_t*>(sV + SV * C::kValSlot);
   uint64_t* empty = full + S;
   uint64_t* s_full = empty + S;   // [2] a block's S of half t in TMEM
   uint64_t* s_free = s_full + 2;  // [2] 128 arrivals: it has been read
-  uint64_t* p_full = s_free + 2;  // [2] 128 arrivals: P_t in TMEM (and O_t rescaled)
-  uint64_t* o_done = p_full + 2;  // [2] O_t += P_t V_j complete
-  uint64_t* done = o_done + 2;    // [2] all products issued by warp 1, and by warp 2, complete
+  uint64_t* p_full = s_free + 2;  // [half][P buffer] 128 arrivals: P_t in TMEM (and O_t rescaled)
+  uint64_t* o_done = p_full + 4;  // [half][P buffer] O_t += P_t V_j complete
+  uint64_t* done = o_done + 4;    // [2] all products issued by warp 1, and by warp 2, complete
   if (smem_u32(smem) & 1023) {
     if (a.b.status) atomicCAS(a.b.status, 0, (int)kDevTimeoutFull);
     return;
@@ -371,8 +381,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(&s_full[t]), 1);
       mbar_init(smem_u32(&s_free[t]), 128);
-      mbar_init(smem_u32(&p_full[t]), 128);
       mbar_init(smem_u32(&done[t]), 1);
+    }
+    for (int t = 0; t < 4; ++t) {
+      mbar_init(smem_u32(&p_full[t]), 128);
       mbar_init(smem_u32(&o_done[t]), 1);
     }
     *stop = 0;
@@ -382,8 +394,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // rows of a slot that no box fills stay zero: their weights are zero, and 0 times a stray NaN would not be
   if (geo.pages * geo.box_rows < kBlock) {
-    for (int i = threadIdx.x; i < S * C::kSlot / 16; i += kThreads)
-      reinterpret_cast<uint4*>(sR)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < (SK * C::kKeySlot + SV * C::kValSlot) / 16; i += kThreads)
+      reinterpret_cast<uint4*>(sK)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   }
   if (warp == 3) {
@@ -402,9 +414,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  constexpr bool kTwoS = DP == 64;  // an S of its own for each half
-  // half t: S at tS (+ 128 t if it has its own), P at tP + 64 t, O at tO + DP t
-  const uint32_t tS = tmem, tP = tmem + (kTwoS ? 256 : 128), tO = tP + 128;
+  // S at tS; half t's block number c (of all its blocks so far): P at p_at(t, c), its barriers number bar_of(t, c), phase
+  // phase_of(c); O at tO + DP t.  With two P buffers a half's P V has a block's time more.
+  constexpr int kTwoP = DP == 64 ? 1 : 0;
+  const uint32_t tS = tmem, tO = tmem + (kTwoP ? 384 : 256);
+  auto p_at = [&](int t, int c) { return tmem + 128 + (kTwoP ? 128 * t + 64 * (c & 1) : 64 * t); };
+  auto bar_of = [&](int t, int c) { return 2 * t + (kTwoP ? c & 1 : 0); };
+  auto phase_of = [&](int c) { return (kTwoP ? c >> 1 : c) & 1; };
 
   int i = pc.b;
   long long at = pc.at;
@@ -517,16 +533,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nb = max(0, j1 - j0);
     // blocks of each half
     const int nh[2] = {split ? (nb + 1) / 2 : nb, kOne ? 0 : split ? nb / 2 : nb};
-    const int pb = kOne ? (a.c.D + 63) / 64 : 1;  // slots of a block
+    const int boxes = (a.c.D + 63) / 64;                                       // of a page's rows
+    const int pk = kOne ? boxes : 1, pv = kOne ? (boxes + 1) / 2 : 1;  // slots of a block
     bool ok = true;
 
-    if (warp == 0 || warp == 3) {
-      // ------------------------------------------------ loads: K, and V
-      const bool ofK = warp == 0;
+    // -------------------------------------------------- loads: K, and V
+    auto loads = [&](auto which) {
+      constexpr bool ofK = decltype(which)::value;
       const CUtensorMap* map = ofK ? &mapK : &mapV;
       const int* table = a.b.pages + run->b * a.b.page_stride;
       const int held = (s.len + page_size - 1) / page_size;  // pages of the sequence
-      const int bytes = geo.parts == 1 ? geo.pages * geo.box_rows * 128 * NB : C::kSlot;
+      const int box = geo.parts == 1 ? geo.pages * geo.box_rows * 128 : kBoxBytes;  // bytes
+      constexpr int per = ofK ? C::kKeyBoxes : C::kValBoxes, slot_bytes = ofK ? C::kKeySlot : C::kValSlot;
+      const int pb = ofK ? pk : pv;
+      uint8_t* const ring = ofK ? sK : sV;
       // All counted along: a division here would queue behind the softmax's exponentials.  The lane's page of block
       // j: its place `idx` in the table and the rows `off` of it that come first; asked for two blocks ahead.
       int idx = geo.parts == 1 ? j0 * geo.pages + lane : j0 / geo.parts, part = geo.parts == 1 ? 0 : j0 - idx * geo.parts;
@@ -542,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return e;
       };
       int page = entry(0), next = entry(1);
-      const int slots = ofK ? SK : SV, first = ofK ? 0 : SK;
+      constexpr int slots = ofK ? SK : SV, first = ofK ? 0 : SK;
       int slot = it * pb % slots, lap = it * pb / slots;
       for (int n = 0; n < nb && ok; ++n) {
         const int after = entry(n + 2);
@@ -558,11 +578,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) hole[(j0 + n) & 31] = nones;
         }
         for (int u = 0; u < pb && ok; ++u) {
+          const int count = kOne ? min(per, boxes - u * per) : per;  // (each has a channel: D > DP - 64)
           int good = 1;
           if (lane == 0) {
             if (lap > 0) good = wait_phase(&empty[first + slot], (lap - 1) & 1, err, kDevTimeoutEmpty);
             if (*stop) good = 0;
-            if (good) mbar_arrive_expect_tx(smem_u32(&full[first + slot]), bytes);
+            if (good) mbar_arrive_expect_tx(smem_u32(&full[first + slot]), count * box);
           }
           ok = __shfl_sync(0xffffffffu, good, 0);
           if (!ok) break;
@@ -571,10 +592,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             c[geo.dim_row] = off;
             c[geo.dim_head] = h;
             c[geo.dim_page] = page;
-            const uint32_t d = smem_u32(sR + (first + slot) * C::kSlot) + lane * geo.box_rows * 128;
+            const uint32_t d = smem_u32(ring + slot * slot_bytes) + lane * geo.box_rows * 128;
 #pragma unroll
-            for (int v = 0; v < NB; ++v)
-              tma_load_4d(d + v * kBoxBytes, map, smem_u32(&full[first + slot]), 64 * (u * NB + v), c[0], c[1], c[2]);
+            for (int v = 0; v < per; ++v)
+              if (v < count)
+                tma_load_4d(d + v * kBoxBytes, map, smem_u32(&full[first + slot]), 64 * (u * per + v), c[0], c[1], c[2]);
           }
           if (++slot == slots) slot = 0, ++lap;
         }
@@ -582,6 +604,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         next = after;
       }
       if (!ok) *stop = 1;
+    };
+    if (warp == 0) {
+      loads(std::true_type());
+    } else if (warp == 3) {
+      loads(std::false_type());
     } else if ((warp == 1 || warp == 2) && nb > 0) {
       // ------------------------------------------------- products: Q K, and P V
       // A whole warp walks the steps (what it computes stays in uniform
@@ -595,38 +622,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int steps = turns ? 2 * nb : nb;
       if (warp == 1) {
         const uint32_t idS = idesc(Pack<T>::kFormat, false, kBlock);
-        const uint32_t q0 = desc_k(smem_u32(sQ)), kd0 = desc_k(smem_u32(sR));
-        int slot = it * pb % SK, phase = (it * pb / SK) & 1;
+        const uint32_t q0 = desc_k(smem_u32(sQ)), kd0 = desc_k(smem_u32(sK));
+        int slot = it * pk % SK, phase = (it * pk / SK) & 1;
         uint32_t there = 0;  // the block's K (its first slot) is known to be there (asked a step ahead)
         for (int g = 0; g < steps; ++g) {
           const int t = kOne ? 0 : g & 1;
           const bool starts = !turns || t == 0, ends = !turns || t == 1;  // the block's first and last step
           if (starts && !__all_sync(0xffffffffu, there)) ok = wait_phase(&full[slot], phase, err, kDevTimeoutFull);
           // the S buffer, once the step that used it last (the half's own, or the other's) has been read
-          if (kTwoS) {
-            if (g > 1 && ok) ok = wait_phase(&s_free[t], (ns[t] + (g >> 1) - 1) & 1, err, kDevTimeoutAccum);
-          } else if (kOne) {
+          if (kOne) {
             if (g > 0 && ok) ok = wait_phase(&s_free[0], (ns[0] + g - 1) & 1, err, kDevTimeoutAccum);
           } else {
             if (g > 0 && ok) ok = wait_phase(&s_free[t ^ 1], (ns[t ^ 1] + ((g - 1) >> 1)) & 1, err, kDevTimeoutAccum);
           }
           if (!ok) break;
           tc_fence_after();
-          const uint32_t q = q0 + t * (ND * kBoxBytes >> 4), s_at = tS + (kTwoS ? 128 * t : 0);
-          for (int u = 0; u < pb; ++u) {
+          const uint32_t q = q0 + t * (ND * kBoxBytes >> 4), s_at = tS;
+          for (int u = 0; u < pk; ++u) {
             if (kOne && u > 0) {
               ok = wait_phase(&full[slot], phase, err, kDevTimeoutFull);
               if (!ok) break;
               tc_fence_after();
             }
-            const uint32_t k = kd0 + slot * (C::kSlot >> 4), qu = q + u * (kBoxBytes >> 4);
+            const uint32_t k = kd0 + slot * (C::kKeySlot >> 4), qu = q + u * (kBoxBytes >> 4);
             if (one) {
 #pragma unroll
-              for (int e = 0; e < 4 * NB; ++e)
+              for (int e = 0; e < 4 * C::kKeyBoxes; ++e)
                 if (4 * u + e < dn)
                   umma_ss(s_at, qu + (e >> 2) * (kBoxBytes >> 4) + 2 * (e & 3), k + (e >> 2) * (kBoxBytes >> 4) + 2 * (e & 3),
                           idS, u > 0 || e > 0);
-              if (u == pb - 1) umma_commit(smem_u32(&s_full[t]));
+              if (u == pk - 1) umma_commit(smem_u32(&s_full[t]));
               if (ends) umma_commit(smem_u32(&empty[slot]));
             }
             if (ends && ++slot == SK) slot = 0, phase ^= 1;
@@ -635,34 +660,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ends) there = g + 1 < steps && ask_phase(&full[slot], phase);
         }
       } else {
-        const uint32_t vd0 = desc_v(smem_u32(sR));
-        int slot = SK + it * pb % SV, phase = (it * pb / SV) & 1;
+        const uint32_t vd0 = desc_v(smem_u32(sV)), id0 = idesc(Pack<T>::kFormat, true, 16 * min(4 * C::kValBoxes, dn));
+        int slot = it * pv % SV, phase = (it * pv / SV) & 1;
         uint32_t there = 0;
         for (int g = 0; g < steps; ++g) {
           const int t = kOne ? 0 : g & 1, i = kOne ? g : g >> 1;
           const bool starts = !turns || t == 0, ends = !turns || t == 1;
-          if (starts && !__all_sync(0xffffffffu, there)) ok = wait_phase(&full[slot], phase, err, kDevTimeoutFull);
-          if (ok) ok = wait_phase(&p_full[t], (ns[t] + i) & 1, err, kDevTimeoutAccum);
+          if (starts && !__all_sync(0xffffffffu, there)) ok = wait_phase(&full[SK + slot], phase, err, kDevTimeoutFull);
+          const int c = ns[t] + i;
+          if (ok) ok = wait_phase(&p_full[bar_of(t, c)], phase_of(c), err, kDevTimeoutAccum);
           if (!ok) break;
           tc_fence_after();
-          for (int u = 0; u < pb; ++u) {
+          for (int u = 0; u < pv; ++u) {
             if (kOne && u > 0) {
-              ok = wait_phase(&full[slot], phase, err, kDevTimeoutFull);
+              ok = wait_phase(&full[SK + slot], phase, err, kDevTimeoutFull);
               if (!ok) break;
               tc_fence_after();
             }
-            const uint32_t v = vd0 + slot * (C::kSlot >> 4), p = tP + 64 * t;
-            const uint32_t idO = idesc(Pack<T>::kFormat, true, 16 * min(4 * NB, dn - 4 * u));
+            const uint32_t v = vd0 + slot * (C::kValSlot >> 4), p = p_at(t, c);
+            const uint32_t idO = u == 0 ? id0 : idesc(Pack<T>::kFormat, true, 16 * (dn - 4 * C::kValBoxes));
             if (one) {
 #pragma unroll
-              for (int e = 0; e < kBlock / 16; ++e) umma_ts(tO + DP * t + 64 * u, p + 8 * e, v + 128 * e, idO, i > 0 || e > 0);
-              if (u == pb - 1) umma_commit(smem_u32(&o_done[t]));
-              if (ends) umma_commit(smem_u32(&empty[slot]));
+              for (int e = 0; e < kBlock / 16; ++e) umma_ts(tO + DP * t + 64 * C::kValBoxes * u, p + 8 * e, v + 128 * e, idO, i > 0 || e > 0);
+              if (u == pv - 1) umma_commit(smem_u32(&o_done[bar_of(t, c)]));
+              if (ends) umma_commit(smem_u32(&empty[SK + slot]));
             }
-            if (ends && ++slot == S) slot = SK, phase ^= 1;
+            if (ends && ++slot == SV) slot = 0, phase ^= 1;
           }
           if (!ok) break;
-          if (ends) there = g + 1 < steps && ask_phase(&full[slot], phase);
+          if (ends) there = g + 1 < steps && ask_phase(&full[SK + slot], phase);
         }
       }
       ok = __all_sync(0xffffffffu, ok);
@@ -670,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (softmax) {
       // -------------------------------------------------------- softmax, output
       const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-      const uint32_t myS = tS + (kTwoS ? 128 * half : 0) + lane_off, myP = tP + 64 * half + lane_off, myO = tO + DP * half + lane_off;
+      const uint32_t myS = tS + lane_off, myO = tO + DP * half + lane_off;
       const float sc = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
       const int n0 = ns[half], mine = nh[half], step = split ? 2 : 1;
       const int all_lo = run->all_lo[half], all_hi = run->all_hi[half];
@@ -698,8 +724,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         float x[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(myS + 32 * c, x[c]);
-        // P's room, and O: free once O += P V of the block before is complete
-        const uint32_t o_there = i > 0 ? ask_phase(&o_done[half], (n0 + i - 1) & 1) : 1u;
+        // P's room is free once its last P V is complete (as is O then, with one P)
+        const int c = n0 + i, held = c - 1 - kTwoP;
+        const uint32_t o_there = i > kTwoP ? ask_phase(&o_done[bar_of(half, held)], phase_of(held)) : 1u;
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(smem_u32(&s_free[half]));
@@ -729,15 +756,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           // among their values must not meet a weight of zero.  Such values leave
           // the block here, and the rows that see them get them at the end.
           if (base < all_lo || base + rows > all_hi) {
-            const int at_v = (it + j - j0) * pb;
+            const int at_v = (it + j - j0) * pv;
             // (this half's last P V has read its V, so every lap of the ring before this block's is known to be there)
-            if (i > 0) ok = wait_phase(&o_done[half], (n0 + i - 1) & 1, err, kDevTimeoutAccum);
-            for (int u = 0; u < pb && ok; ++u) ok = wait_phase(&full[SK + (at_v + u) % SV], ((at_v + u) / SV) & 1, err, kDevTimeoutFull);
+            if (i > 0) ok = wait_phase(&o_done[bar_of(half, c - 1)], phase_of(c - 1), err, kDevTimeoutAccum);
+            for (int u = 0; u < pv && ok; ++u) ok = wait_phase(&full[SK + (at_v + u) % SV], ((at_v + u) / SV) & 1, err, kDevTimeoutFull);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            for (int u = 0; u < pb; ++u) {
-              uint4* v = reinterpret_cast<uint4*>(sR + (SK + (at_v + u) % SV) * C::kSlot);
-              for (int e = hrow; e < C::kSlot / 16; e += kHalfRows) {
+            for (int u = 0; u < pv; ++u) {
+              uint4* v = reinterpret_cast<uint4*>(sV + (at_v + u) % SV * C::kValSlot);
+              for (int e = hrow; e < C::kValSlot / 16; e += kHalfRows) {
                 const uint4 w = v[e];
                 if (odd32<T>(w.x) || odd32<T>(w.y) || odd32<T>(w.z) || odd32<T>(w.w)) {
                   atomicMin(&run->odd_lo, j);
@@ -762,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
         if (__builtin_expect(__any_sync(0xffffffffu, mb > m + kSlack || !o_there || !ok), 0)) {
-          if (ok && i > 0) ok = wait_phase(&o_done[half], (n0 + i - 1) & 1, err, kDevTimeoutAccum);
+          if (ok && i > 0) ok = wait_phase(&o_done[bar_of(half, c - 1)], phase_of(c - 1), err, kDevTimeoutAccum);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -787,30 +814,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float2 sc2 = make_float2(sc, sc), nr2 = make_float2(-ref, -ref);
+        const uint32_t myP = p_at(half, c) + lane_off;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int q = 0; q < 4; ++q) {
           uint32_t p[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            float2 e = fma2(make_float2(x[c][2 * k], x[c][2 * k + 1]), sc2, nr2);
+            float2 e = fma2(make_float2(x[q][2 * k], x[q][2 * k + 1]), sc2, nr2);
             e.x = ex2(e.x);
             e.y = ex2(e.y);
             sum[k & 1] = add2(sum[k & 1], e);
             p[k] = Pack<T>::two(e.x, e.y);
           }
-          tmem_st16(myP + 16 * c, p);
+          tmem_st16(myP + 16 * q, p);
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(smem_u32(&p_full[half]));
+        mbar_arrive(smem_u32(&p_full[bar_of(half, c)]));
         s_there = ask_phase(&s_full[half], (n0 + i + 1) & 1);
         sum[0] = add2(sum[0], sum[1]);
         l += sum[0].x + sum[0].y;
       }
       if (ok && mine > 0)
         ok = __all_sync(0xffffffffu,
-                        wait_phase(&o_done[half], (n0 + mine - 1) & 1, err, kDevTimeoutAccum));
+                        wait_phase(&o_done[bar_of(half, n0 + mine - 1)], phase_of(n0 + mine - 1), err, kDevTimeoutAccum));
       if (!ok) *stop = 1;
       tc_fence_after();
       const bool whole = k0 == run->first && k1 == run->last;
