@@ -267,8 +267,11 @@ def test_append_leaves_out_what_is_not_there(wv):
 
 
 # ---------------------------------------------------------------- attention
-def _attention_case(wv, lens, hk, g, D, size, dtype, new=None, ranges=None, seed=0, scale=None, fill=None, spare=3):
+def _attention_case(wv, lens, hk, g, D, size, dtype, new=None, ranges=None, seed=0, scale=None, fill=None, spare=3, room=40_000):
     pages, lengths, n_pages = ref.tables(lens, size, seed=seed, spare=spare)
+    # tables with room for more keys than any sequence has (calls of many tokens take another way where there is little)
+    more = max(0, -(-room // size) - pages.shape[1])
+    pages = torch.cat([pages, torch.full((len(lens), more), -1, dtype=torch.int32, device="cuda")], 1)
     new = [1] * len(lens) if new is None else new
     cu = torch.tensor([sum(new[:i]) for i in range(len(new) + 1)], dtype=torch.int32)
     T = int(cu[-1])
@@ -330,9 +333,10 @@ def _ranges(kind, lens, new):
 
 @pytest.mark.parametrize("dtype", HALVES, ids=str)
 @pytest.mark.parametrize("case", CHUNK, ids=lambda c: "t{}n{}h{}g{}d{}p{}{}".format(sum(c[1]), max(c[0]), *c[2:6], c[6] or ""))
-def test_attention_of_many_tokens(wv, case, dtype):
+@pytest.mark.parametrize("room", [0, 40_000], ids=["tight", "roomy"])
+def test_attention_of_many_tokens(wv, case, dtype, room):
     lens, new, hk, g, D, size, mask = case
-    q, kc, vc, pages, lengths, cu = _attention_case(wv, lens, hk, g, D, size, dtype, new=new, fill=math.nan)
+    q, kc, vc, pages, lengths, cu = _attention_case(wv, lens, hk, g, D, size, dtype, new=new, fill=math.nan, room=room)
     ranges = _ranges(mask, lens, new)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     # two rows behind the last sequence stay as they are
@@ -359,7 +363,7 @@ WIDE = [
 @pytest.mark.parametrize("dtype", HALVES, ids=str)
 @pytest.mark.parametrize("case", WIDE, ids=lambda c: "t{}n{}h{}g{}d{}p{}{}".format(sum(c[1]), max(c[0]), *c[2:6], c[6] or ""))
 def test_attention_of_wide_heads(wv, case, dtype):
-    test_attention_of_many_tokens(wv, case, dtype)
+    test_attention_of_many_tokens(wv, case, dtype, 40_000)
 
 
 @pytest.mark.parametrize("new", [[1, 1], [3, 2], [150, 200]], ids=str)

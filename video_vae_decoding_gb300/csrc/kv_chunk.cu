@@ -11,7 +11,7 @@
 // tensor cores form the next S while it works.  TMEM has 512 columns: S takes 128,
 // which the halves, half a period apart, take in turn; a P 64 and an O_t DP.
 //  D <= 64    two P for each half: its P V has a block's time more.  (An S for each
-//             half instead: 280 key blocks of 512 rows take 154 us instead of 134.)
+//             half instead: 154 us below instead of 134.)
 //  D <= 128   one P for each half
 //  D <= 256   one half of 128 rows
 // What else was tried at D = 128, cycles per block of 128 keys and 256 rows (2048 of

@@ -93,12 +93,17 @@ wan_status sm_count(int* n) {
   return WAN_OK;
 }
 
-// Rows of a sequence (tokens x query heads of a key head), on average, from
-// which the tensor-core kernel takes over from the split kernel.
+// Where the kernel for many tokens takes over from the split kernel: from kChunkRows rows of a sequence (tokens x query
+// heads of a key head) on average, unless the call is so small that its longer start counts: fewer than kChunkWork
+// products of a row with a key, by the keys that the tables have room for.  us with split / many tokens: 34 tokens of 4
+// heads a key head (136 rows) against 1300 keys of 16 heads 49 / 37, 170 tokens against 600 keys of 4 heads 17 / 21,
+// 13 tokens of 2 rows against 1500 keys 17 / 26.
 constexpr int kChunkRows = 64;
+constexpr double kChunkWork = 6e5;
 
 bool chunk_rows(const AttnArgs& a, ChunkGeo* g) {
-  return (int64_t)a.b.T * a.group >= (int64_t)kChunkRows * a.b.B && kv_chunk_geometry(a, g);
+  return (int64_t)a.b.T * a.group >= (int64_t)kChunkRows * a.b.B &&
+         (double)a.b.T * a.q_heads * a.b.max_pages * a.c.page_size >= kChunkWork && kv_chunk_geometry(a, g);
 }
 int64_t workspace_of(const AttnArgs& a, bool chunk, int sms) {
   const int64_t split = kv_attention_workspace(a, sms);

@@ -357,11 +357,11 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
 
 
 @functools.lru_cache(maxsize=1024)
-def _workspace(dtype, heads, size, D, B, T, q_heads, device_index) -> int:
+def _workspace(dtype, heads, size, D, columns, B, T, q_heads, device_index) -> int:
     """Bytes of workspace of a call of these sizes (wan_kv_attention_workspace), whatever the addresses."""
     step = 8 * -(-D // 8)
     c = _pack_cache(16, 16, dtype, heads, size, D, 1, step, step, step, step, step, step)
-    n = load().wan_kv_attention_workspace(c, _pack_batch(16, 1, 1, B, 16, 16, T, 0), q_heads)
+    n = load().wan_kv_attention_workspace(c, _pack_batch(16, columns, columns, B, 16, 16, T, 0), q_heads)
     if n < 0:
         msg = load().wan_vae_last_error()
         raise ValueError(msg.decode())
@@ -417,7 +417,7 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
             raise ValueError(f"out is {tuple(out.shape)}, not {tuple(shape)}")
         _rows_of(out, "out")
         os = out.stride()
-    n = _workspace(_CODES[dt], heads, size, D, B, T, H, dev.index)
+    n = _workspace(_CODES[dt], heads, size, D, pages.shape[1], B, T, H, dev.index)
     ws = torch.empty(n, dtype=torch.uint8, device=dev)
     lse, lp = None, None
     if return_lse:
