@@ -659,3 +659,66 @@ def test_refusals_are_the_same_on_both_ways(wv, way):
         wv.rotary(wrap(q), _positions(2, 1), (33,))
     with pytest.raises(ValueError, match="out is"):
         wv.rotary(wrap(q), _positions(2, 1), (32,), out=torch.empty(2, 4, 64, device="cuda"))
+
+
+def test_attention_of_many_short_sequences(wv):
+    """More row tiles than the card has SMs, some sequences without a key or a token."""
+    g = torch.Generator().manual_seed(5)
+    lens = [int(n) for n in torch.randint(0, 300, (130,), generator=g)]
+    lens[3] = lens[77] = 0
+    new = [min(n, int(m)) for n, m in zip(lens, torch.randint(0, 40, (130,), generator=g))]
+    for D, dtype in (64, torch.bfloat16), (128, torch.float16), (256, torch.bfloat16):
+        q, kc, vc, pages, lengths, cu = _attention_case(wv, lens, 2, 8, D, 16, dtype, new=new, fill=math.nan)
+        ranges = _ranges("causal", lens, new)
+        got, lse = wv.kv_attention(q, kc, vc, pages, lengths, cu, ranges, return_lse=True)
+        ref.check_attention(got, lse, ref.attention(q, kc, vc, pages, lengths, cu, ranges))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_chunks_in_graphs(wv, D):
+    """A step of many tokens, captured, replayed with other lengths, token ranges and masks in place, on two streams."""
+    hq, hk, size, B, T = 8, 2, 16, 2, 120
+    pages, lengths, n_pages = ref.tables([900] * B, size)
+    pages = torch.cat([pages, torch.full((B, 2000), -1, dtype=torch.int32, device="cuda")], 1)
+    state = []
+    for i in range(2):
+        state.append(dict(
+            q=_randn(T, hq, D, dtype=torch.bfloat16, seed=i), k=_randn(T, hk, D, dtype=torch.bfloat16, seed=2 + i),
+            v=_randn(T, hk, D, dtype=torch.bfloat16, seed=4 + i), kc=_randn(n_pages, hk, size, D, dtype=torch.bfloat16, seed=6 + i),
+            vc=_randn(n_pages, hk, size, D, dtype=torch.bfloat16, seed=8 + i), cu=torch.tensor([0, 60, T], dtype=torch.int32).cuda(),
+            lengths=torch.tensor([600, 300], dtype=torch.int32).cuda(), pos=_positions(T, 1, seed=i),
+            ranges=torch.tensor([[0, 900]] * T, dtype=torch.int32).cuda()))
+
+    def step(s):
+        q = wv.kv_append(s["k"], s["v"], s["kc"], s["vc"], pages, s["lengths"], s["cu"], s["pos"], (D // 2,), q=s["q"])
+        return wv.kv_attention(q, s["kc"], s["vc"], pages, s["lengths"], s["cu"], s["ranges"])
+
+    side = torch.cuda.Stream()
+    graphs, outs = [], []
+    for s in state:
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step(s)
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(step(s))
+        graphs.append(graph)
+    for lens, cut in ([600, 300], 60), ([119, 900], 119), ([30, 90], 30):
+        new = [cut, T - cut]
+        for s in state:
+            s["lengths"].copy_(torch.tensor(lens))
+            s["cu"].copy_(torch.tensor([0, cut, T]))
+            s["ranges"].copy_(_ranges("causal", lens, new))
+        torch.cuda.synchronize()
+        a, b = torch.cuda.Stream(), torch.cuda.Stream()
+        with torch.cuda.stream(a):
+            graphs[0].replay()
+        with torch.cuda.stream(b):
+            graphs[1].replay()
+        torch.cuda.synchronize()
+        for s, o in zip(state, outs):
+            got = o.clone()
+            assert torch.equal(got, step(s))
+            q = wv.rotary(s["q"], s["pos"], (D // 2,))
+            ref.check_attention(got, None, ref.attention(q, s["kc"], s["vc"], pages, s["lengths"], s["cu"], s["ranges"]))

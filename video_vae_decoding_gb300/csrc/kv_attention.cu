@@ -20,8 +20,11 @@
 //  - a row tile that a cut divides leaves partial (m, l, o) in the workspace,
 //    and a second kernel, launched to start as the first drains, joins them in
 //    the order of the keys: the result does not depend on timing.
-// (With a block's four warps on one row tile, merged through shared memory at its
-// end, a batch of 64 ragged sequences took 182 us instead of 180.)
+// Two sequences of up to 131k keys, 64 heads of 128 on 8, take 151 us, 6.6 TB/s
+// (0.98 of a plain copy's rate); 64 ragged ones of up to 8000 keys, 32 heads on 8,
+// 180 us, 6.1 TB/s; one of 1000 keys 10 us, of which the keys take 2.  (With a
+// block's four warps on one row tile, merged through shared memory at its end, the
+// first two took 162 and 182 us.)
 // Sums, maxima and outputs are held in 32 bits; how the weights are rounded is
 // told at Weights.
 #include <algorithm>
