@@ -220,6 +220,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// q is in shared memory, and what all rows of a half see is known: the softmax's warps and warp 1 (named barrier 2).
+template <int THREADS>
+__device__ __forceinline__ void q_sync() { asm volatile("bar.sync 2, %0;" ::"n"(THREADS) : "memory"); }
 // The 256 softmax threads (named barrier 1).
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
@@ -331,10 +334,16 @@ struct alignas(16) Run {
   int b, h, row0, cnt;
   int k0, k1;
   int first, last;           // of the tile's blocks [first, last)
-  int units;                 // what it takes of the line
-  int lo, hi;                // keys that some row sees
+  int blocks;                // k1 - k0; 0: the piece has no more runs
   int all_lo[2], all_hi[2];  // per half: keys that every row sees
   int odd_lo, odd_hi;        // blocks whose values were cleaned (below)
+};
+
+// Where thread 0 stands on the line (in shared memory: the softmax has no register to spare).
+struct alignas(16) Cursor {
+  Piece pc;
+  long long line, at;  // the next unit of the line, and of row tile i
+  int i;
 };
 
 template <typename T, int DP>
@@ -347,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kSoftEnd = kOne ? 8 : 12;  // softmax warps are 4 up to this one
   // the only shared memory of the kernel, so it starts on a 1024-byte boundary, as the swizzled boxes must
   extern __shared__ __align__(1024) uint8_t smem[];
-  static_assert(sizeof(Run) + 8 * (2 * S + 14) + 8 + 128 + 16 <= 1024, "barriers and the run's description");
+  static_assert(2 * sizeof(Run) + sizeof(Cursor) + 8 * (2 * S + 14) + 8 + 128 + 16 <= 1024, "barriers and the run's description");
   uint8_t* sQ = smem;  // [half][64-channel box][128 rows]
   uint8_t *sK = sQ + C::kQ, *sV = sK + SK * C::kKeySlot;  // SK slots of K, SV of V; their barriers in this order
   uint64_t* full = reinterpret_cast<uint64_t*>(sV + SV * C::kValSlot);
@@ -363,9 +372,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 2);
   volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint32_t* hole = tmem_slot + 2;  // [32]: bit i of hole[j % 32]: page i of block j is none of the cache's
-  Run* run = reinterpret_cast<Run*>((reinterpret_cast<uintptr_t>(hole + 32) + 15) & ~uintptr_t(15));
-  float* half_ml = reinterpret_cast<float*>(run + 1);  // [2][128] reference and sum of half 1, handed to half 0
+  uint32_t* hole = tmem_slot + 2;  // [32]: bit i of hole[c % 32]: page i of the c-th block is none of the cache's
+  Run* runs = reinterpret_cast<Run*>((reinterpret_cast<uintptr_t>(hole + 32) + 15) & ~uintptr_t(15));  // [2]
+  Cursor* cursor = reinterpret_cast<Cursor*>(runs + 2);
+  float* half_ml = reinterpret_cast<float*>(cursor + 1);  // [2][128] reference and sum of half 1, handed to half 0
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int G = gridDim.x, me = blockIdx.x;
@@ -405,11 +415,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // for the plan
   auto units = [&](const RowTile& t, int w) { return (long long)(kRunUnits + w * (t.k1 - t.k0)); };
-  const Piece pc = cut_line<kThreads / 32, 1>((int)row_tiles(a), kLeast, reinterpret_cast<long long*>(half_ml), [&](int i) {
+  const Piece cut = cut_line<kThreads / 32, 1>((int)row_tiles(a), kLeast, reinterpret_cast<long long*>(half_ml), [&](int i) {
     const RowTile t = ws.tiles[i];
     return t.b < 0 ? 0 : a.c.heads * units(t, tile_weight(a, sequence(a, t.b, false), t.rt));
   });
-  if (threadIdx.x == 0) ws.open[me].parts = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -422,14 +431,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar_of = [&](int t, int c) { return 2 * t + (kTwoP ? c & 1 : 0); };
   auto phase_of = [&](int c) { return (kTwoP ? c >> 1 : c) & 1; };
 
-  int i = pc.b;
-  long long at = pc.at;
   int it = 0;                 // blocks so far (all roles count alike)
   int ns[2] = {0, 0};         // blocks of each half so far
 
-  for (long long line = pc.beg; line < pc.end;) {
-    // ------------------------------------------------------------- the next run
-    if (threadIdx.x == 0) {
+  // The piece's next run (thread 0).
+  auto describe = [&](Run* run) {
+    const Piece& pc = cursor->pc;
+    long long line = cursor->line, at = cursor->at;
+    int i = cursor->i;
+    run->blocks = 0;
+    while (line < pc.end && run->blocks == 0) {
       RowTile t = ws.tiles[i];
       Seq s{0, 0, 0};
       long long n = 0;  // units of a head
@@ -442,14 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (at < a.c.heads * n) break;
           at -= a.c.heads * n;
         }
-        if (++i >= row_tiles(a)) break;  // (the tables changed under the call)
+        if (++i >= row_tiles(a)) return;  // (the tables changed under the call)
         t = ws.tiles[i];
-      }
-      if (i >= row_tiles(a)) {
-        t = RowTile{0, 0, 0, 0};
-        at = 0;
-        n = pc.end - line;
-        w = 1;
       }
       const int h = (int)quotient(at, n), u0 = (int)(at - h * n), u1 = (int)min(n, u0 + (pc.end - line));
       run->s = s;
@@ -462,29 +467,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a block belongs to the piece that holds its last unit
       run->k0 = t.k0 + max(0, u0 - kRunUnits) / w;
       run->k1 = t.k0 + max(0, u1 - kRunUnits) / w;
-      run->units = u1 - u0;
-      run->lo = 0x7fffffff;
-      run->hi = 0;
+      run->blocks = run->k1 - run->k0;
       for (int t = 0; t < 2; ++t) {
         run->all_lo[t] = 0;
         run->all_hi[t] = 0x7fffffff;
       }
       run->odd_lo = 0x7fffffff;
       run->odd_hi = -1;
-      at += u1 - u0;
       if (run->k0 == t.k0 && run->k1 > t.k0 && run->k1 < t.k1)
         ws.open[me] = Open{pc.holder(line + n - u0 - 1) - me, h, run->row0, run->cnt, s, 0};
+      at += u1 - u0;
+      line += u1 - u0;
     }
-    __syncthreads();
+    cursor->line = line;
+    cursor->at = at;
+    cursor->i = i;
+  };
+  if (threadIdx.x == 0) {
+    ws.open[me].parts = 0;
+    cursor->pc = cut;
+    cursor->line = cut.beg;
+    cursor->at = cut.at;
+    cursor->i = cut.b;
+    describe(&runs[0]);
+  }
+  __syncthreads();
+
+  for (int r = 0; runs[r & 1].blocks > 0; ++r) {
+    Run* const run = &runs[r & 1];
     const int h = run->h, row0 = run->row0, cnt = run->cnt, k0 = run->k0, k1 = run->k1;
     const Seq s = run->s;
     const bool split = !kOne && cnt <= kHalfRows;  // both halves hold the same rows and take the blocks in turn
     const int half = (warp - 4) >> 2;     // softmax warps
-    line += run->units;
-    if (k0 == k1) {  // only units of a block that the next piece holds
-      __syncthreads();
-      continue;
-    }
     // softmax threads: the row (TMEM lane) in their half, and the keys that it sees
     const int hrow = 32 * (warp & 3) + lane;
     const int row = (split ? 0 : half * kHalfRows) + hrow;
@@ -493,10 +507,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (softmax) {
       if (real) {
         seen_range(a, s.r0 + (row0 + row) / a.group, s.len, &lo, &hi);
-        if (lo < hi) {
-          atomicMin(&run->lo, lo);
-          atomicMax(&run->hi, hi);
-        }
         if (lo > 0) atomicMax(&run->all_lo[half], lo);
         atomicMin(&run->all_hi[half], hi);
       }
@@ -527,10 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
     }
-    __syncthreads();
-    const int j0 = run->hi > 0 ? max(k0, block_of_key(geo, page_size, run->lo)) : k1;
-    const int j1 = run->hi > 0 ? min(k1, block_of_key(geo, page_size, run->hi - 1) + 1) : k1;
-    const int nb = max(0, j1 - j0);
+    if (softmax || warp == 1) q_sync<kOne ? 160 : 288>();
+    const int j0 = k0, nb = k1 - k0;
     // blocks of each half
     const int nh[2] = {split ? (nb + 1) / 2 : nb, kOne ? 0 : split ? nb / 2 : nb};
     const int boxes = (a.c.D + 63) / 64;                                       // of a page's rows
@@ -538,11 +546,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
 
     // -------------------------------------------------- loads: K, and V
-    auto loads = [&](auto which) {
+    // blocks [n0, n1) of a run whose first block is the it-th
+    auto loads = [&](auto which, const Run* run, int it, int n0, int n1) {
       constexpr bool ofK = decltype(which)::value;
+      const int h = run->h, j0 = run->k0 + n0;
       const CUtensorMap* map = ofK ? &mapK : &mapV;
       const int* table = a.b.pages + run->b * a.b.page_stride;
-      const int held = (s.len + page_size - 1) / page_size;  // pages of the sequence
+      const int held = (run->s.len + page_size - 1) / page_size;  // pages of the sequence
       const int box = geo.parts == 1 ? geo.pages * geo.box_rows * 128 : kBoxBytes;  // bytes
       constexpr int per = ofK ? C::kKeyBoxes : C::kValBoxes, slot_bytes = ofK ? C::kKeySlot : C::kValSlot;
       const int pb = ofK ? pk : pv;
@@ -557,14 +567,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (++p == geo.parts) p = 0, ++i;
       };
       auto entry = [&](int n) {
-        const int e = n < nb && idx2 < wide ? table[idx2] : (int)a.c.pages;  // past the cache, which reads as zeros
+        const int e = n < n1 && idx2 < wide ? table[idx2] : (int)a.c.pages;  // past the cache, which reads as zeros
         advance(idx2, part2);
         return e;
       };
-      int page = entry(0), next = entry(1);
+      int page = entry(n0), next = entry(n0 + 1);
       constexpr int slots = ofK ? SK : SV, first = ofK ? 0 : SK;
-      int slot = it * pb % slots, lap = it * pb / slots;
-      for (int n = 0; n < nb && ok; ++n) {
+      int slot = (it + n0) * pb % slots, lap = (it + n0) * pb / slots;
+      for (int n = n0; n < n1 && ok; ++n) {
         const int after = entry(n + 2);
         const int off = part * kBlock;
         const bool none = idx < wide && (page < 0 || page >= a.c.pages);
@@ -575,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ofK) {
           const uint32_t nones = __ballot_sync(0xffffffffu, none);
-          if (lane == 0) hole[(j0 + n) & 31] = nones;
+          if (lane == 0) hole[(it + n) & 31] = nones;
         }
         for (int u = 0; u < pb && ok; ++u) {
           const int count = kOne ? min(per, boxes - u * per) : per;  // (each has a channel: D > DP - 64)
@@ -606,10 +616,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) *stop = 1;
     };
     if (warp == 0) {
-      loads(std::true_type());
+      // K of the first blocks of the next run is asked for before this one ends (as many as surely find room: their
+      // slots held blocks of this run or an earlier one, whose products wait for nothing of this warp)
+      const int kAhead = SK / pk;
+      loads(std::true_type(), run, it, r > 0 ? min(nb, kAhead) : 0, nb);
+      Run* const next = &runs[(r + 1) & 1];
+      if (lane == 0) describe(next);
+      __syncwarp();
+      if (ok && next->blocks > 0) loads(std::true_type(), next, it + nb, 0, min(next->blocks, kAhead));
     } else if (warp == 3) {
-      loads(std::false_type());
-    } else if ((warp == 1 || warp == 2) && nb > 0) {
+      loads(std::false_type(), run, it, 0, nb);
+    } else if (warp == 1 || warp == 2) {
       // ------------------------------------------------- products: Q K, and P V
       // A whole warp walks the steps (what it computes stays in uniform
       // registers, which the instructions take their operands from); one thread
@@ -720,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!__all_sync(0xffffffffu, s_there)) ok = wait_phase(&s_full[half], (n0 + i) & 1, err, kDevTimeoutAccum);
         __syncwarp();
         tc_fence_after();
-        const uint32_t nones = hole[j & 31];
+        const uint32_t nones = hole[(it + j - j0) & 31];
         float x[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(myS + 32 * c, x[c]);
@@ -882,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!split || half == 0) {
         const float rl = l == 0.f ? 0.f : 1.f / l;
-        const int odd_lo = max(run->odd_lo, j0), odd_hi = min(run->odd_hi, j1 - 1);
+        const int odd_lo = max(run->odd_lo, j0), odd_hi = min(run->odd_hi, k1 - 1);
         T* dst = real ? out_row<T>(a, s, h, row0 + row) : nullptr;
 #pragma unroll 1
         for (int c = 0; c < DP / 16; ++c) {

@@ -124,6 +124,37 @@ __device__ __forceinline__ Piece cut_line(int B, int least, long long* scratch, 
   static_assert(PIECES == 1 || PIECES == WARPS, "a piece for the block, or one for each warp");
   long long *s_scan = scratch, *s_b = scratch + WARPS, *s_at = s_b + PIECES;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Piece p;
+  p.beg = p.end = 0;
+  p.b = 0;
+  p.at = 0;
+  const long long my_q = (long long)blockIdx.x * PIECES + (PIECES == 1 ? 0 : warp);
+  long long total = 0;
+  auto cut = [&] {
+    p.live = min((long long)gridDim.x * PIECES, max(quotient(total, least), total > 0 ? 1LL : 0LL));
+    p.size = total > 0 ? quotient(total, p.live) : 1;
+    p.longer = total - p.size * p.live;
+  };
+  if (B <= 32) {
+    // a sequence per lane, each warp for itself: no barrier (one sequence of 1000 keys 9.1 us, 9.9 with them)
+    const long long mine = lane < B ? of(lane) : 0;
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    total = __shfl_sync(0xffffffffu, incl, 31);
+    cut();
+    if (my_q < p.live) {
+      p.beg = p.start(my_q);
+      p.end = p.start(my_q + 1);
+      const uint32_t here = __ballot_sync(0xffffffffu, p.beg >= incl - mine && p.beg < incl);
+      p.b = __ffs(here) - 1;
+      p.at = p.beg - __shfl_sync(0xffffffffu, incl - mine, p.b);
+    }
+    return p;
+  }
   const int chunk = (B + 32 * WARPS - 1) / (32 * WARPS);
   const int b_lo = min(B, (int)threadIdx.x * chunk), b_hi = min(B, b_lo + chunk);
   long long mine = 0;
@@ -136,20 +167,13 @@ __device__ __forceinline__ Piece cut_line(int B, int least, long long* scratch, 
   }
   if (lane == 31) s_scan[warp] = incl;
   __syncthreads();
-  Piece p;
   long long before = incl - mine;
-  long long total = 0;
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) {
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
-  p.live = min((long long)gridDim.x * PIECES, max(quotient(total, least), total > 0 ? 1LL : 0LL));
-  p.size = total > 0 ? quotient(total, p.live) : 1;
-  p.longer = total - p.size * p.live;
-  p.beg = p.end = 0;
-  p.b = 0;
-  p.at = 0;
+  cut();
 #pragma unroll 1
   for (int w = 0; w < PIECES; ++w) {
     const long long q = (long long)blockIdx.x * PIECES + w;
@@ -169,10 +193,9 @@ __device__ __forceinline__ Piece cut_line(int B, int least, long long* scratch, 
   }
   __syncthreads();
   const int w = PIECES == 1 ? 0 : warp;
-  const long long q = (long long)blockIdx.x * PIECES + w;
-  if (q < p.live) {
-    p.beg = p.start(q);
-    p.end = p.start(q + 1);
+  if (my_q < p.live) {
+    p.beg = p.start(my_q);
+    p.end = p.start(my_q + 1);
     p.b = (int)s_b[w];
     p.at = s_at[w];
   }
