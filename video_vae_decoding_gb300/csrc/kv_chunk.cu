@@ -29,9 +29,9 @@
 //
 // Bound: the tensor cores, 4 D operations per row and key; K and V come through
 // a ring each and serve both halves, so a block of 128 keys asks 64 KB (D = 128) for
-// 33.6 MFLOP.  880 tokens of 16 heads of 128 against 27,280 keys take 173 us, 1.13
-// PFLOP/s (59% of a large library product's); with heads of 64 134 us, where the
-// softmax bounds, and with 8 heads of 256 252 us: 128 KB a block for 16.8 MFLOP is 8
+// 33.6 MFLOP.  880 tokens of 16 heads of 128 against 27,280 keys take 171 us, 1.15
+// PFLOP/s (60% of a large library product's); with heads of 64 136 us, where the
+// softmax bounds, and with 8 heads of 256 251 us: 128 KB a block for 16.8 MFLOP is 8
 // TB/s from the L2.
 // V is taken as it lies in the cache, [key][channel]: the MMA's second operand
 // with its N dimension contiguous, so nothing is transposed on the way.
@@ -260,9 +260,9 @@ __host__ __device__ inline long long row_tiles(const AttnArgs& a) {
 }
 
 // What a row tile with a head takes of the line: kRunUnits (start, end and the blocks at a mask's edge), and for each
-// block kPairUnits, or kSingleUnits in a tile of at most 128 rows.  They stand for what these cost: with 20 for a run two
-// chunks of 1300 causal tokens of 48 heads take 217 us, with 45 187, with 60 175, with 80 174.  (A smaller tile does half the arithmetic, but asks for K and V as
-// fast as a larger one would at twice the speed.)
+// block kPairUnits, or kSingleUnits in a tile of at most 128 rows.  They stand for what these cost: two chunks of 1300
+// causal tokens of 48 heads take 184 us with 30 for a run, 173 with 45, 162 with 60, 164 with 80.  (A smaller tile does
+// half the arithmetic, but asks for K and V as fast as a larger one would at twice the speed.)
 constexpr int kPairUnits = 5, kSingleUnits = 4, kRunUnits = 60;
 __device__ __forceinline__ int tile_weight(const AttnArgs& a, const Seq& s, int rt) {
   return a.c.D <= 128 && s.n * a.group - rt * tile_rows(a.c.D) <= kHalfRows ? kSingleUnits : kPairUnits;
@@ -345,6 +345,41 @@ struct alignas(16) Cursor {
   long long line, at;  // the next unit of the line, and of row tile i
   int i;
 };
+
+// Keys that some row of a half does not see: an infinity or a NaN among their
+// values must not meet a weight of zero.  Such values leave the block here (V in
+// `count` slots from the ring's number `at` on, read by the half's 128 threads), and
+// the rows that see them get them at the end.  Not inline: the softmax's loop needs
+// the registers (two chunks of 1300 causal tokens of 48 heads 159 us, 162 inline).
+template <typename T, int DP>
+__device__ __noinline__ bool clean_values(uint8_t* ring, uint64_t* full, int at, int count, int thread, int block, Run* run,
+                                          int* err) {
+  using C = Cfg<DP>;
+  constexpr int SV = C::kValSlots;
+  bool odd = false;
+  for (int u = at; u < at + count; ++u) {
+    if (!wait_phase(&full[u % SV], (u / SV) & 1, err, kDevTimeoutFull)) return false;
+    const uint4* v = reinterpret_cast<const uint4*>(ring + u % SV * C::kValSlot);
+#pragma unroll 8
+    for (int e = thread; e < C::kValSlot / 16; e += kHalfRows) {
+      const uint4 w = v[e];
+      odd |= odd32<T>(w.x) || odd32<T>(w.y) || odd32<T>(w.z) || odd32<T>(w.w);
+    }
+  }
+  if (odd) {
+    atomicMin(&run->odd_lo, block);
+    atomicMax(&run->odd_hi, block);
+    __threadfence_block();
+    for (int u = at; u < at + count; ++u) {
+      uint16_t* v = reinterpret_cast<uint16_t*>(ring + u % SV * C::kValSlot);
+      for (int e = thread; e < C::kValSlot / 16; e += kHalfRows)
+        for (int k = 0; k < 8; ++k)
+          if (odd16<T>(v[8 * e + k])) v[8 * e + k] = 0;
+    }
+  }
+  fence_proxy_async_smem();
+  return true;
+}
 
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -732,8 +767,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t s_there = 0;  // S of block i is known to be there
       for (int i = 0; i < mine; ++i) {
         const int j = j0 + (split ? 2 * i + half : i);
-        const bool plain = j >= plain_lo && j < plain_hi && behind != 0;
+        const bool inside = j >= plain_lo && j < plain_hi, plain = inside && behind != 0;
         if (tails && geo.parts > 1) behind = behind >= step ? behind - step : behind - step + geo.parts;
+        const int c = n0 + i;
         if (!__all_sync(0xffffffffu, s_there)) ok = wait_phase(&s_full[half], (n0 + i) & 1, err, kDevTimeoutAccum);
         __syncwarp();
         tc_fence_after();
@@ -742,17 +778,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(myS + 32 * c, x[c]);
         // P's room is free once its last P V is complete (as is O then, with one P)
-        const int c = n0 + i, held = c - 1 - kTwoP;
+        const int held = c - 1 - kTwoP;
         const uint32_t o_there = i > kTwoP ? ask_phase(&o_done[bar_of(half, held)], phase_of(held)) : 1u;
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(smem_u32(&s_free[half]));
         if (__builtin_expect(!plain || nones != 0, 0)) {
-          int base, rows;
-          block_keys(geo, page_size, j, &base, &rows);
-          const int d0 = lo - base, d1 = min(rows, hi - base);  // columns [d0, d1) are keys of this row
-          // by groups of 16 columns, if some row of this half does not see them all
-          const int u0 = all_lo - base, u1 = min(rows, all_hi - base);
+          // columns [d0, d1) are keys of this row, [u0, u1) of all rows of this half; in the last part of a page that all
+          // see, the page's rows (without block_keys' division)
+          int d0 = 0, d1 = plain ? kBlock : page_size - (geo.parts - 1) * kBlock, u0 = d0, u1 = d1;
+          bool hidden = false;  // some row does not see some key of the block
+          if (!inside) {
+            int base, rows;
+            block_keys(geo, page_size, j, &base, &rows);
+            d0 = lo - base, d1 = min(rows, hi - base);
+            u0 = all_lo - base, u1 = min(rows, all_hi - base);
+            hidden = base < all_lo || base + rows > all_hi;
+          }
+          // by groups of 16 columns, if some row does not see them all
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             if (u0 > 16 * q || u1 < 16 * q + 16) {
@@ -769,31 +812,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 32; ++e)
                 if (32 * c + e >= p0 && 32 * c + e < p0 + per) x[c][e] = -INFINITY;
           }
-          // Keys that some row of this half does not see: an infinity or a NaN
-          // among their values must not meet a weight of zero.  Such values leave
-          // the block here, and the rows that see them get them at the end.
-          if (base < all_lo || base + rows > all_hi) {
-            const int at_v = (it + j - j0) * pv;
-            // (this half's last P V has read its V, so every lap of the ring before this block's is known to be there)
-            if (i > 0) ok = wait_phase(&o_done[bar_of(half, c - 1)], phase_of(c - 1), err, kDevTimeoutAccum);
-            for (int u = 0; u < pv && ok; ++u) ok = wait_phase(&full[SK + (at_v + u) % SV], ((at_v + u) / SV) & 1, err, kDevTimeoutFull);
+          if (hidden) {
+            // The lap of the ring before this block's has to be known to be there: the P V before the last one of this
+            // half is, which is enough where both halves take all blocks and a block one slot.
+            if (i > 0 && (split || kOne)) ok = wait_phase(&o_done[bar_of(half, c - 1)], phase_of(c - 1), err, kDevTimeoutAccum);
+            ok = ok && clean_values<T, DP>(sV, full + SK, (it + j - j0) * pv, pv, hrow, j, run, err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            for (int u = 0; u < pv; ++u) {
-              uint4* v = reinterpret_cast<uint4*>(sV + (at_v + u) % SV * C::kValSlot);
-              for (int e = hrow; e < C::kValSlot / 16; e += kHalfRows) {
-                const uint4 w = v[e];
-                if (odd32<T>(w.x) || odd32<T>(w.y) || odd32<T>(w.z) || odd32<T>(w.w)) {
-                  atomicMin(&run->odd_lo, j);
-                  atomicMax(&run->odd_hi, j);
-                  __threadfence_block();
-                  uint16_t* h16 = reinterpret_cast<uint16_t*>(v + e);
-                  for (int k = 0; k < 8; ++k)
-                    if (odd16<T>(h16[k])) h16[k] = 0;
-                }
-              }
-            }
-            fence_proxy_async_smem();
           }
         }
         float mx[4];
