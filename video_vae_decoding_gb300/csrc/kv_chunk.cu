@@ -102,13 +102,14 @@ struct Pack<__half> {
 };
 
 // mbar_wait_bounded with few instructions per try (the waiting warps share the
-// issue slots with the working ones) and tries counted instead of timed: a try
-// takes about 50 cycles, so 2^26 of them are about two seconds.
+// issue slots with the working ones) and tries counted instead of timed: a try that
+// fails takes 50 cycles or more, so 2^24 of them are half a second at least.  (What
+// is waited for takes microseconds.)
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* err, int code) {
   uint32_t done;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, 67108864;\n"
+      "mov.u32 n, 16777216;\n"
       "WAIT_%=:\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "@p bra DONE_%=;\n\t"

@@ -75,8 +75,8 @@ __device__ __forceinline__ void seen_range(const AttnArgs& a, int t, int len, in
   *first = 0;
   *last = len;
   if (a.ranges) {
-    *first = max(0, a.ranges[2 * t]);
-    *last = min(len, a.ranges[2 * t + 1]);
+    *first = max(0, a.ranges[2LL * t]);
+    *last = min(len, a.ranges[2LL * t + 1]);
     if (*first >= *last) *first = *last = 0;
   }
 }
@@ -87,8 +87,8 @@ __device__ __forceinline__ void put_empty(const AttnArgs& a, int me, int G) {
   for (int b = me; b < a.b.B; b += G) {
     const Seq s = sequence(a, b, true);
     if (s.len > 0) continue;
-    for (int i = threadIdx.x; i < s.n * a.q_heads; i += blockDim.x) {
-      const int t = i / a.q_heads, h = i - t * a.q_heads;
+    for (long long i = threadIdx.x; i < (long long)s.n * a.q_heads; i += blockDim.x) {
+      const int t = (int)(i / a.q_heads), h = (int)(i - (long long)t * a.q_heads);
       T* o = (T*)a.out + (long long)(s.r0 + t) * a.o_t + (long long)h * a.o_h;
       for (int c = 0; c < a.c.D; ++c) o[c] = round_to<T>(0.f);
       if (a.lse) a.lse[(long long)(s.r0 + t) * a.q_heads + h] = -INFINITY;

@@ -33,8 +33,6 @@ struct RotaryPlan {
   int inverse;      // opposite angles
 };
 
-// Widest access that pointers and strides allow, in elements (a power of two
-// whose bytes divide all of them), up to 16 bytes.
 struct RotaryArgs {
   RotaryPlan plan;
   const void* x;
@@ -45,7 +43,7 @@ struct RotaryArgs {
   long long pos_b;  // positions' batch stride (values)
   int B, S, H, D;
   int elem;   // 0 fp32, 1 bf16, 2 fp16
-  int width;  // elements per access that alignment allows
+  int width;  // elements per access that pointers and strides allow (a power of two, 16 bytes at most)
 };
 cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t s);
 
