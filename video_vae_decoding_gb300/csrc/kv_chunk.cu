@@ -29,8 +29,8 @@
 //
 // Bound: the tensor cores, 4 D operations per row and key; K and V come through
 // a ring each and serve both halves, so a block of 128 keys asks 64 KB (D = 128) for
-// 33.6 MFLOP.  880 tokens of 16 heads of 128 against 27,280 keys take 171 us, 1.15
-// PFLOP/s (60% of a large library product's); with heads of 64 136 us, where the
+// 33.6 MFLOP.  880 tokens of 16 heads of 128 against 27,280 keys take 169 us, 1.17
+// PFLOP/s (61% of a large library product's); with heads of 64 136 us, where the
 // softmax bounds, and with 8 heads of 256 251 us: 128 KB a block for 16.8 MFLOP is 8
 // TB/s from the L2.
 // V is taken as it lies in the cache, [key][channel]: the MMA's second operand
