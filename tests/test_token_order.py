@@ -1,0 +1,25 @@
+"""Ordering rules of the tensor-core attention kernel that no result can show
+reliably (a rule broken gives a right answer almost always): read off its source."""
+
+import os
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def source():
+    with open(os.path.join(ROOT, "video_vae_decoding_gb300", "csrc", "kv_chunk.cu")) as f:
+        return f.read()
+
+
+def test_weights_are_stored_behind_a_fence(source):
+    """The softmax learns from a barrier, asked ahead, that the product which read the weights' room is complete:
+    a tcgen05 fence has to stand between that answer and the stores, on every way."""
+    asked = source.index("const uint32_t o_there")
+    store = source.index("tmem_st16(myP", asked)
+    loop = source.rindex("for (int q = 0; q < 4; ++q)", asked, store)
+    slow = source.index("if (__builtin_expect(__any_sync(0xffffffffu, mb > m + kSlack", asked)
+    behind = source.index("const float2 sc2", slow)  # the slow way, which has a fence of its own, is over
+    assert "tc_fence_after();" in source[source.rindex("}\n", slow, behind):loop]

@@ -856,6 +856,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_wait();
           }
         }
+        // the P V that read P's room last was seen complete (asked ahead, or awaited above): its reads come before the stores
+        tc_fence_after();
         const float2 sc2 = make_float2(sc, sc), nr2 = make_float2(-ref, -ref);
         const uint32_t myP = p_at(half, c) + lane_off;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
