@@ -23,3 +23,11 @@ def test_weights_are_stored_behind_a_fence(source):
     slow = source.index("if (__builtin_expect(__any_sync(0xffffffffu, mb > m + kSlack", asked)
     behind = source.index("const float2 sc2", slow)  # the slow way, which has a fence of its own, is over
     assert "tc_fence_after();" in source[source.rindex("}\n", slow, behind):loop]
+
+
+def test_products_are_committed_by_the_thread_that_issued_them(source):
+    """A commit speaks of the products of its own thread: the last one, ahead of giving tensor memory back, has to be
+    made by the elected thread, as the products are."""
+    assert "const bool one = elect();" in source
+    last = source.index("umma_commit(smem_u32(&done[")
+    assert "elect()" in source[source.rindex("if (", 0, last):last]

@@ -157,7 +157,7 @@ __device__ __forceinline__ constexpr uint32_t idesc(uint32_t format, bool b_mn, 
 constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
 __device__ __forceinline__ uint32_t desc_v(uint32_t saddr) { return (saddr >> 4) | ((uint32_t)(kBoxBytes >> 4) << 16); }
-// One thread of the calling warp.
+// One thread of the calling warp (converged; the same one at each call, but not lane 0 by any rule).
 __device__ __forceinline__ bool elect() {
   uint32_t r;
   asm volatile(
@@ -1010,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_bounded(smem_u32(&full[s]), 1, err, kDevTimeoutFull, 20000000);
     }
   }
-  if ((warp == 1 || warp == 2) && lane == 0) {
+  if ((warp == 1 || warp == 2) && elect()) {  // the thread that issued them: a commit speaks of its own thread's products
     umma_commit(smem_u32(&done[warp - 1]));
     mbar_wait_bounded(smem_u32(&done[warp - 1]), 0, err, kDevTimeoutAccum);
   }
