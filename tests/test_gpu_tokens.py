@@ -722,3 +722,28 @@ def test_chunks_in_graphs(wv, D):
             assert torch.equal(got, step(s))
             q = wv.rotary(s["q"], s["pos"], (D // 2,))
             ref.check_attention(got, None, ref.attention(q, s["kc"], s["vc"], pages, s["lengths"], s["cu"], s["ranges"]))
+
+
+@pytest.mark.parametrize("heads", [1, 40])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", HALVES, ids=str)
+def test_attention_odd_values_of_a_block_that_half_a_tile_sees(wv, dtype, D, heads):
+    """A window that moves inside a tile of 256 rows: its first 128 rows see a whole block of keys, the others only
+    its later part.  Infinities there reach the rows that see them, however small (2^-43) their weights, the same in
+    every call: none is taken away while a product reads it."""
+    n, T = 512, 256
+    q, kc, vc, pages, lengths, cu = _attention_case(wv, [n], heads, 1, D, 16, dtype, new=[T])
+    q.fill_(1.0)
+    kc.zero_()
+    place = lambda i: (int(pages[0, i // 16]), slice(None), i % 16)  # noqa: E731
+    for i, c, value in (100, 3, math.inf), (100, D - 1, -math.inf), (101, 5, math.nan), (10, 7, math.inf), (300, 3, math.inf):
+        vc[place(i)][..., c] = value
+    kc[place(100)] = -30.0 / D                                  # a score of -30 at a scale of one, all others 0
+    ranges = torch.tensor([[0, n]] * 128 + [[40, n]] * 128, dtype=torch.int32).cuda()
+    got, lse = wv.kv_attention(q, kc, vc, pages, lengths, cu, ranges, scale=1.0, return_lse=True)
+    want = ref.attention(q, kc, vc, pages, lengths, cu, ranges, scale=1.0)
+    assert bool(torch.isinf(want[0][:128, :, 7]).all()) and bool(torch.isfinite(want[0][128:, :, 7]).all())
+    ref.check_attention(got, lse, want)
+    for _ in range(20):
+        again = wv.kv_attention(q, kc, vc, pages, lengths, cu, ranges, scale=1.0)
+        assert torch.equal(again.nan_to_num(0.5, 1.5, 2.5), got.nan_to_num(0.5, 1.5, 2.5))

@@ -31,3 +31,13 @@ def test_products_are_committed_by_the_thread_that_issued_them(source):
     assert "const bool one = elect();" in source
     last = source.index("umma_commit(smem_u32(&done[")
     assert "elect()" in source[source.rindex("if (", 0, last):last]
+
+
+def test_one_half_cleans_the_values_that_both_read(source):
+    """Where both halves of a tile read a block's values, only the half whose product comes first may change them, and
+    it decides by what the rows of either half see."""
+    decided = source.index("if (cleans) hidden = ")
+    line = source[decided:source.index("\n", decided)]
+    for name in "all_lo[0]", "all_lo[1]", "all_hi[0]", "all_hi[1]":
+        assert name in line
+    assert "cleans = !turns || half == 0" in source

@@ -347,10 +347,12 @@ struct alignas(16) Cursor {
   int i;
 };
 
-// Keys that some row of a half does not see: an infinity or a NaN among their
+// Keys that some row of a tile does not see: an infinity or a NaN among their
 // values must not meet a weight of zero.  Such values leave the block here (V in
-// `count` slots from the ring's number `at` on, read by the half's 128 threads), and
-// the rows that see them get them at the end.  Not inline: the softmax's loop needs
+// `count` slots from the ring's number `at` on, read by a half's 128 threads), and
+// the rows that see them get them at the end.  Where both halves' products read the
+// slot, half 0 does this for both, ahead of its weights and so of either product: no
+// product reads a value while it changes.  Not inline: the softmax's loop needs
 // the registers (two chunks of 1300 causal tokens of 48 heads 159 us, 162 inline).
 template <typename T, int DP>
 __device__ __noinline__ bool clean_values(uint8_t* ring, uint64_t* full, int at, int count, int thread, int block, Run* run,
@@ -760,9 +762,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // after the block in its page.
       int plain_lo = 0x7fffffff, plain_hi = 0, behind = 1;
       const bool tails = geo.parts > 1 ? page_size % kBlock != 0 : geo.pages * page_size != kBlock;
+      // Where both halves take every block, half 0, whose product comes first, cleans a block's values (below) for both:
+      // its blocks are plain if all rows of the tile see them.
+      const bool turns = !split && !kOne, cleans = !turns || half == 0;
       if (mine > 0 && !(geo.parts == 1 && tails)) {
-        plain_lo = all_lo > 0 ? block_of_key(geo, page_size, all_lo - 1) + 1 : 0;
-        plain_hi = block_of_key(geo, page_size, min(all_hi, s.len));
+        const int p_lo = turns && cleans ? max(all_lo, run->all_lo[1]) : all_lo;
+        const int p_hi = turns && cleans ? min(all_hi, run->all_hi[1]) : all_hi;
+        plain_lo = p_lo > 0 ? block_of_key(geo, page_size, p_lo - 1) + 1 : 0;
+        plain_hi = block_of_key(geo, page_size, min(p_hi, s.len));
       }
       if (tails) behind = geo.parts - 1 - (j0 + (split ? half : 0)) % geo.parts;
       uint32_t s_there = 0;  // S of block i is known to be there
@@ -788,13 +795,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           // columns [d0, d1) are keys of this row, [u0, u1) of all rows of this half; in the last part of a page that all
           // see, the page's rows (without block_keys' division)
           int d0 = 0, d1 = plain ? kBlock : page_size - (geo.parts - 1) * kBlock, u0 = d0, u1 = d1;
-          bool hidden = false;  // some row does not see some key of the block
+          bool hidden = false;  // some row does not see some key of the block, whose values this half cleans
           if (!inside) {
             int base, rows;
             block_keys(geo, page_size, j, &base, &rows);
             d0 = lo - base, d1 = min(rows, hi - base);
             u0 = all_lo - base, u1 = min(rows, all_hi - base);
-            hidden = base < all_lo || base + rows > all_hi;
+            if (cleans) hidden = base < max(run->all_lo[0], run->all_lo[1]) || base + rows > min(run->all_hi[0], run->all_hi[1]);
           }
           // by groups of 16 columns, if some row does not see them all
 #pragma unroll
