@@ -485,7 +485,10 @@ wan_status wan_kv_append(const wan_kv_cache* cache, const wan_kv_batch* batch, c
  * nothing).  Scores, sums and outputs are held in fp32; weights enter the
  * product with v as 16-bit values.  workspace: device memory of at least
  * wan_kv_attention_workspace bytes, 16-byte aligned, not used by any other
- * work until this call's is done (its contents need not be kept).
+ * work until this call's is done (its contents need not be kept).  If a wait
+ * inside the kernel for many tokens runs out (after about a second; none does
+ * in ordinary work), all rows of sequences with keys are NaN, lse too, and the
+ * batch's status word, if there is one, holds a code.
  * Errors: WAN_ERR_INVALID_ARG, WAN_ERR_DTYPE, WAN_ERR_UNSUPPORTED, WAN_ERR_CUDA. */
 wan_status wan_kv_attention(const wan_kv_cache* cache, const wan_kv_batch* batch, const void* q, int32_t q_heads,
                             int64_t q_token, int64_t q_head, const int32_t* ranges, float scale, void* out,
@@ -494,6 +497,16 @@ wan_status wan_kv_attention(const wan_kv_cache* cache, const wan_kv_batch* batch
 /* Bytes of workspace that wan_kv_attention needs for these sizes on the
  * current device (-1 and an error message if it would refuse them). */
 int64_t wan_kv_attention_workspace(const wan_kv_cache* cache, const wan_kv_batch* batch, int32_t q_heads);
+
+/* Failure-detection self test of wan_kv_attention's kernel for many tokens, in
+ * the form of wan_selftest_attention_timeout: a small call (bf16, zeros in) at
+ * this head dim (a multiple of 8 up to 256) whose loader withholds the first
+ * block of keys; once with a status word and once without, a second or so
+ * each.  Blocks until done.  Returns WAN_ERR_INTERNAL and the code (1..3) in
+ * *device_code when the timeout was detected and reported and every row of the
+ * sequence with keys was NaN both times, WAN_ERR_INTERNAL and no code if a row
+ * was not, WAN_OK if no code was reported; the context stays usable. */
+wan_status wan_selftest_kv_attention_timeout(int32_t head_dim, int32_t* device_code, wan_cuda_stream stream);
 
 #ifdef __cplusplus
 }

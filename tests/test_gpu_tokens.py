@@ -2,7 +2,9 @@
 and their gradient, the append to a paged cache, attention over it, and the
 steps of a streaming model made of them."""
 
+import ctypes
 import math
+import time
 
 import pytest
 import torch
@@ -747,3 +749,22 @@ def test_attention_odd_values_of_a_block_that_half_a_tile_sees(wv, dtype, D, hea
     for _ in range(20):
         again = wv.kv_attention(q, kc, vc, pages, lengths, cu, ranges, scale=1.0)
         assert torch.equal(again.nan_to_num(0.5, 1.5, 2.5), got.nan_to_num(0.5, 1.5, 2.5))
+
+
+@pytest.mark.parametrize("D", [64, 128, 200])
+def test_attention_bounded_wait_expires_and_is_reported(wv, D):
+    """A block of keys that is never loaded (no fault: the wait for it runs out after a second): the code is reported,
+    the rows are NaN with or without a status word, soon enough, and the context stays usable."""
+    code = ctypes.c_int32(0)
+    start = time.monotonic()
+    status = wv.load().wan_selftest_kv_attention_timeout(D, ctypes.byref(code), None)
+    message = wv.load().wan_vae_last_error()
+    # two calls of one second each (some waits follow others): the limit is one in time, not only in tries
+    assert time.monotonic() - start < 10
+    assert status == 9 and code.value in (1, 2, 3), (status, code.value, message)
+    assert b"bounded wait" in message
+    q, kc, vc, pages, lengths, cu = _attention_case(wv, [300, 500], 2, 2, D, 64, torch.bfloat16, new=[100, 290])
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got, lse = wv.kv_attention(q, kc, vc, pages, lengths, cu, return_lse=True, status=word)
+    wv.kv_status(word)
+    ref.check_attention(got, lse, ref.attention(q, kc, vc, pages, lengths, cu))

@@ -208,3 +208,10 @@ def test_binding_refusals():
         wv.kv_attention(k[..., :4], kc, kc, pages, lens)
     with pytest.raises(ValueError, match="autograd"):
         wv.kv_attention(k.clone().requires_grad_(), kc, kc, pages, lens)
+
+
+def test_selftest_refusal(lib):
+    code = ctypes.c_int32(7)
+    for D in 0, 60, 264:
+        assert lib.wan_selftest_kv_attention_timeout(D, ctypes.byref(code), None) == 1
+        assert code.value == 0 and lib.wan_vae_last_error()

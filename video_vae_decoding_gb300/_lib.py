@@ -138,6 +138,7 @@ SIGNATURES = {
     "wan_kv_attention": (_i32, [_vp, _vp, _vp, _i32, _i64, _i64, _vp,
                                 ctypes.c_float, _vp, _i64, _i64, _vp, _vp, _i64, _vp]),
     "wan_kv_attention_workspace": (_i64, [_vp, _vp, _i32]),
+    "wan_selftest_kv_attention_timeout": (_i32, [_i32, ctypes.POINTER(_i32), _vp]),
 }
 
 _lib = None

@@ -101,15 +101,16 @@ struct Pack<__half> {
   }
 };
 
-// mbar_wait_bounded with few instructions per try (the waiting warps share the
-// issue slots with the working ones) and tries counted instead of timed: a try that
-// fails takes 50 cycles or more, so 2^24 of them are half a second at least.  (What
-// is waited for takes microseconds.)
+// Waits for the phase of `parity` to complete; false, and `code` in the status word if
+// there is one, if it has not after 2^18 tries.  A try that fails sleeps for 3.7 us (the
+// self test measures a second for all of them); what is waited for takes microseconds.
+// Tries are counted, not timed as in mbar_wait_bounded: a clock read in the loop, behind
+// however many tries, costs 2 to 10% of a call at 64 channels and 1 to 5% at 128.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* err, int code) {
   uint32_t done;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, 16777216;\n"
+      "mov.u32 n, 262144;\n"
       "WAIT_%=:\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "@p bra DONE_%=;\n\t"
@@ -269,7 +270,9 @@ __device__ __forceinline__ int tile_weight(const AttnArgs& a, const Seq& s, int 
   return a.c.D <= 128 && s.n * a.group - rt * tile_rows(a.c.D) <= kHalfRows ? kSingleUnits : kPairUnits;
 }
 
+constexpr int kFaultBytes = 16;
 struct Space {
+  int* fault;  // a wait ran out: no row of the call is to be believed
   RowTile* tiles;
   Open* open;
   float2* ml;  // [2 G][rows of a tile]
@@ -278,7 +281,8 @@ struct Space {
 template <int DP>
 __host__ __device__ inline Space space(const AttnArgs& a, int G) {
   Space s;
-  s.tiles = (RowTile*)a.workspace;
+  s.fault = (int*)a.workspace;
+  s.tiles = (RowTile*)((char*)a.workspace + kFaultBytes);
   s.open = (Open*)(s.tiles + row_tiles(a));
   s.ml = (float2*)(s.open + G);
   s.o = (float4*)(s.ml + (size_t)2 * G * Cfg<DP>::kRows);
@@ -327,6 +331,7 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
     break;
   }
   if (lane == 0) space<64>(a, 0).tiles[place] = t;
+  if (place == 0 && lane == 0) *space<64>(a, 0).fault = 0;
 }
 
 // A run: blocks [k0, k1) of one row tile and head.
@@ -405,6 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* o_done = p_full + 4;  // [half][P buffer] O_t += P_t V_j complete
   uint64_t* done = o_done + 4;    // [2] all products issued by warp 1, and by warp 2, complete
   if (smem_u32(smem) & 1023) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (threadIdx.x == 0) *space<DP>(a, gridDim.x).fault = 1;
     if (a.b.status) atomicCAS(a.b.status, 0, (int)kDevTimeoutFull);
     return;
   }
@@ -625,17 +632,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t nones = __ballot_sync(0xffffffffu, none);
           if (lane == 0) hole[(it + n) & 31] = nones;
         }
+        const bool withheld = ofK && it + n + 1 == a.stall_at1;  // (the failure self test)
         for (int u = 0; u < pb && ok; ++u) {
           const int count = kOne ? min(per, boxes - u * per) : per;  // (each has a channel: D > DP - 64)
           int good = 1;
           if (lane == 0) {
             if (lap > 0) good = wait_phase(&empty[first + slot], (lap - 1) & 1, err, kDevTimeoutEmpty);
             if (*stop) good = 0;
-            if (good) mbar_arrive_expect_tx(smem_u32(&full[first + slot]), count * box);
+            if (good && !withheld) mbar_arrive_expect_tx(smem_u32(&full[first + slot]), count * box);
           }
           ok = __shfl_sync(0xffffffffu, good, 0);
           if (!ok) break;
-          if (lane < geo.pages) {  // one box per lane, of the page that the lane holds
+          if (lane < geo.pages && !withheld) {  // one box per lane, of the page that the lane holds
             int c[3];
             c[geo.dim_row] = off;
             c[geo.dim_head] = h;
@@ -823,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (hidden) {
             // The lap of the ring before this block's has to be known to be there: the P V before the last one of this
             // half is, which is enough where both halves take all blocks and a block one slot.
-            if (i > 0 && (split || kOne)) ok = wait_phase(&o_done[bar_of(half, c - 1)], phase_of(c - 1), err, kDevTimeoutAccum);
+            if (ok && i > 0 && (split || kOne)) ok = wait_phase(&o_done[bar_of(half, c - 1)], phase_of(c - 1), err, kDevTimeoutAccum);
             ok = ok && clean_values<T, DP>(sV, full + SK, (it + j - j0) * pv, pv, hrow, j, run, err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -1023,6 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (*stop && threadIdx.x == 0) *ws.fault = 1;  // for the join, which tells the caller
   if (warp == 3) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -1040,8 +1049,11 @@ __global__ void __launch_bounds__(kJoinThreads) kv_chunk_join_kernel(const __gri
   const int me = blockIdx.x;
   const Space ws = space<DP>(a, G);
   const Open op = ws.open[me];
-  if (blockIdx.y == 0) put_empty<T>(a, me, G);  // rows of sequences without a key get their zeros here
-  if (op.parts == 0) return;
+  // Rows of sequences without a key get their zeros here.  Where a wait ran out the other rows, written or not, become
+  // NaN: the call may have no status word to tell it.
+  const bool fault = *ws.fault != 0;
+  if (blockIdx.y == 0) put_empty<T>(a, me, G, fault);
+  if (op.parts == 0 || fault) return;
   const int row0 = op.row0, cnt = op.cnt;
   const int lane = threadIdx.x & 31;
   for (int w = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); w < kRows / 8 * (DP / 16);
@@ -1134,7 +1146,7 @@ bool kv_chunk_geometry(const AttnArgs& a, ChunkGeo* g) {
 
 long long kv_chunk_workspace(const AttnArgs& a, int sms) {
   const int DP = a.c.D <= 64 ? 64 : a.c.D <= 128 ? 128 : 256;
-  return row_tiles(a) * (long long)sizeof(RowTile) + (long long)sms * (sizeof(Open) + 2 * tile_rows(DP) * (sizeof(float2) + (size_t)DP * sizeof(float)));
+  return kFaultBytes + row_tiles(a) * (long long)sizeof(RowTile) + (long long)sms * (sizeof(Open) + 2 * tile_rows(DP) * (sizeof(float2) + (size_t)DP * sizeof(float)));
 }
 
 cudaError_t launch_kv_chunk(const ChunkLaunch& L, int sms, cudaStream_t s) {

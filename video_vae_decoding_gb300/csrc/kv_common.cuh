@@ -80,18 +80,19 @@ __device__ __forceinline__ void seen_range(const AttnArgs& a, int t, int len, in
     if (*first >= *last) *first = *last = 0;
   }
 }
-// Zeros for the rows of sequences without a key: block `me` of `G` takes every
-// G-th sequence.
+// Zeros for the rows of sequences without a key, and NaN for all others if `fault`:
+// block `me` of `G` takes every G-th sequence.
 template <typename T>
-__device__ __forceinline__ void put_empty(const AttnArgs& a, int me, int G) {
+__device__ __forceinline__ void put_empty(const AttnArgs& a, int me, int G, bool fault = false) {
   for (int b = me; b < a.b.B; b += G) {
     const Seq s = sequence(a, b, true);
-    if (s.len > 0) continue;
+    if (s.len > 0 && !fault) continue;
+    const float x = s.len > 0 ? __int_as_float(0x7fffffff) : 0.f, z = s.len > 0 ? x : -INFINITY;
     for (long long i = threadIdx.x; i < (long long)s.n * a.q_heads; i += blockDim.x) {
       const int t = (int)(i / a.q_heads), h = (int)(i - (long long)t * a.q_heads);
       T* o = (T*)a.out + (long long)(s.r0 + t) * a.o_t + (long long)h * a.o_h;
-      for (int c = 0; c < a.c.D; ++c) o[c] = round_to<T>(0.f);
-      if (a.lse) a.lse[(long long)(s.r0 + t) * a.q_heads + h] = -INFINITY;
+      for (int c = 0; c < a.c.D; ++c) o[c] = round_to<T>(x);
+      if (a.lse) a.lse[(long long)(s.r0 + t) * a.q_heads + h] = z;
     }
   }
 }

@@ -11,8 +11,9 @@
 
 namespace wan {
 
-// Every device-side wait gives up after this many SM clocks (about 2 s at
-// 2 GHz), records an error code and lets the kernel finish.
+// Every device-side wait gives up, records an error code and lets the kernel
+// finish: mbar_wait_bounded after this many SM clocks (about 2 s at 2 GHz), the
+// paged attention's wait_phase after a number of tries (about a second).
 constexpr long long kWaitLimitCycles = 4000000000LL;
 
 // Error codes a kernel can leave in the device error word.

@@ -4,6 +4,7 @@
 #include <cmath>
 #include <set>
 #include <utility>
+#include <vector>
 
 #include "host.h"
 #include "kv_chunk.h"
@@ -145,6 +146,15 @@ bool cache_map(const KvCache& c, const void* base, long long page, long long hea
                           const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The tensor maps of a call by the kernel for many tokens; false if there is none, or if k and v order their dimensions
+// differently.
+bool chunk_maps(const AttnArgs& a, ChunkLaunch* L) {
+  ChunkGeo gk = L->geo;
+  return cache_map(a.c, a.c.k, a.c.k_page, a.c.k_head, a.c.k_row, &gk, &L->k) &&
+         cache_map(a.c, a.c.v, a.c.v_page, a.c.v_head, a.c.v_row, &L->geo, &L->v) && gk.dim_row == L->geo.dim_row &&
+         gk.dim_head == L->geo.dim_head && gk.dim_page == L->geo.dim_page;
 }
 
 wan_status check_heads(const KvCache& c, int q_heads) {
@@ -306,6 +316,7 @@ static wan_status attention_args(const wan_kv_cache* cache, const wan_kv_batch* 
   if ((int64_t)a->b.T * q_heads > 0x7fffffffLL) return fail(WAN_ERR_UNSUPPORTED, "%d tokens of %d heads", a->b.T, q_heads);
   a->q_heads = q_heads;
   a->group = q_heads / a->c.heads;
+  a->stall_at1 = 0;
   return WAN_OK;
 }
 
@@ -338,12 +349,7 @@ wan_status wan_kv_attention(const wan_kv_cache* cache, const wan_kv_batch* batch
     a.scale_log2 = (float)(scale * 1.4426950408889634);
     a.workspace = workspace;
     if (chunk) {
-      // k and v may order their dimensions differently; then, and where a map cannot be made, the split kernel runs
-      // (there is room for either)
-      ChunkGeo gk = L.geo;
-      chunk = cache_map(a.c, a.c.k, a.c.k_page, a.c.k_head, a.c.k_row, &gk, &L.k) &&
-              cache_map(a.c, a.c.v, a.c.v_page, a.c.v_head, a.c.v_row, &L.geo, &L.v) && gk.dim_row == L.geo.dim_row &&
-              gk.dim_head == L.geo.dim_head && gk.dim_page == L.geo.dim_page;
+      chunk = chunk_maps(a, &L);  // without them the split kernel runs (there is room for either)
       L.a = a;
     }
     CUDA_TRY(chunk ? launch_kv_chunk(L, sms, (cudaStream_t)stream) : launch_kv_attention(a, sms, (cudaStream_t)stream));
@@ -362,6 +368,88 @@ int64_t wan_kv_attention_workspace(const wan_kv_cache* cache, const wan_kv_batch
     fail(WAN_ERR_INTERNAL, "unexpected C++ exception");
     return -1;
   }
+}
+
+wan_status wan_selftest_kv_attention_timeout(int32_t head_dim, int32_t* device_code, wan_cuda_stream stream) {
+  API_GUARD({
+    if (device_code) *device_code = 0;
+    if (head_dim < 8 || head_dim % 8 || head_dim > kMaxHeadDim)
+      return fail(WAN_ERR_INVALID_ARG, "head dim %d (a multiple of 8 up to 256)", head_dim);
+    cudaStream_t s = (cudaStream_t)stream;
+    // 290 tokens of 4 query heads against 500 keys of 2 heads, 10 tokens without a key, and 10 rows behind them
+    constexpr int kHeads = 2, kQHeads = 4, kPage = 64, kPages = 8, kSeqs = 2, kNew = 290, kOwned = 300, kRows = 310;
+    const int32_t tables[2 * kPages + kSeqs + kSeqs + 1] = {0, 1, 2, 3, 4, 5, 6, 7, 0, 0, 0, 0, 0, 0, 0, 0,
+                                                            500, 0, 0, kNew, kOwned};
+    const int64_t plane = (int64_t)kPage * head_dim, cache_bytes = kPages * kHeads * plane * 2;
+    const int64_t row = (int64_t)kQHeads * head_dim, out_n = kRows * row, lse_n = (int64_t)kRows * kQHeads;
+    wan_kv_cache c{(void*)16, (void*)16, WAN_BF16, kHeads, kPage, head_dim, kPages, kHeads * plane, plane, head_dim,
+                   kHeads * plane, plane, head_dim};
+    wan_kv_batch b{(int32_t*)16, kPages, kPages, kSeqs, (int32_t*)16, (int32_t*)16, kRows, nullptr};
+    AttnArgs a;
+    int sms = 0;
+    WAN_TRY(attention_args(&c, &b, kQHeads, &a));
+    WAN_TRY(sm_count(&sms));
+    ChunkLaunch L;
+    if (!kv_chunk_geometry(a, &L.geo)) return fail(WAN_ERR_INTERNAL, "the kernel for many tokens does not take the case");
+    // one allocation: K, V, q | out | lse | tables | status word | workspace, each on a 256-byte boundary
+    const int64_t sizes[6] = {2 * cache_bytes + out_n * 2, out_n * 2, lse_n * 4, (int64_t)sizeof(tables), 4,
+                              kv_chunk_workspace(a, sms)};
+    int64_t at[7] = {0};
+    for (int i = 0; i < 6; ++i) at[i + 1] = (at[i] + sizes[i] + 255) / 256 * 256;
+    std::vector<uint16_t> out(out_n);
+    std::vector<float> lse(lse_n);
+    struct Mem {
+      char* p = nullptr;
+      cudaStream_t s;
+      ~Mem() {
+        if (p) cudaFreeAsync(p, s);
+      }
+    } mem;
+    mem.s = s;
+    CUDA_TRY(cudaMallocAsync((void**)&mem.p, at[6], s));
+    a.c.k = mem.p;
+    a.c.v = mem.p + cache_bytes;
+    a.q = mem.p + 2 * cache_bytes;
+    a.out = mem.p + at[1];
+    a.lse = (float*)(mem.p + at[2]);
+    int* table = (int*)(mem.p + at[3]);
+    a.b.pages = table;
+    a.b.lengths = table + 2 * kPages;
+    a.b.cu = table + 2 * kPages + kSeqs;
+    int* word = (int*)(mem.p + at[4]);
+    a.workspace = mem.p + at[5];
+    a.ranges = nullptr;
+    a.q_t = a.o_t = row;
+    a.q_h = a.o_h = head_dim;
+    a.scale_log2 = 1.f;
+    a.stall_at1 = 1;  // each SM's first block of keys is never loaded
+    if (!chunk_maps(a, &L)) return fail(WAN_ERR_INTERNAL, "no tensor map of the case");
+    int code = 0;
+    for (int told = 1; told >= 0; --told) {  // with a status word, and without
+      a.b.status = told ? word : nullptr;
+      L.a = a;
+      CUDA_TRY(cudaMemsetAsync(mem.p, 0, at[1], s));
+      CUDA_TRY(cudaMemsetAsync(mem.p + at[1], 0x11, at[6] - at[1], s));
+      CUDA_TRY(cudaMemsetAsync(word, 0, 4, s));
+      CUDA_TRY(cudaMemcpyAsync(table, tables, sizeof(tables), cudaMemcpyHostToDevice, s));
+      CUDA_TRY(launch_kv_chunk(L, sms, s));
+      if (told) CUDA_TRY(cudaMemcpyAsync(&code, word, 4, cudaMemcpyDeviceToHost, s));
+      CUDA_TRY(cudaMemcpyAsync(out.data(), a.out, out_n * 2, cudaMemcpyDeviceToHost, s));
+      CUDA_TRY(cudaMemcpyAsync(lse.data(), a.lse, lse_n * 4, cudaMemcpyDeviceToHost, s));
+      CUDA_TRY(cudaStreamSynchronize(s));
+      for (int64_t i = 0; i < out_n; ++i) {
+        const int64_t r = i / row;
+        const uint16_t e = out[i];
+        if (r < kNew ? (e & 0x7fff) <= 0x7f80 : e != (r < kOwned ? 0 : 0x1111))
+          return fail(WAN_ERR_INTERNAL, "row %lld holds %#x after a wait that ran out", (long long)r, e);
+      }
+      for (int64_t i = 0; i < kNew * kQHeads; ++i)
+        if (!std::isnan(lse[i])) return fail(WAN_ERR_INTERNAL, "lse %lld is a number after a wait that ran out", (long long)i);
+    }
+    if (device_code) *device_code = code;
+    if (code) return fail(WAN_ERR_INTERNAL, "a token kernel reported error %d (a bounded wait expired)", code);
+    return WAN_OK;
+  })
 }
 
 }  // extern "C"

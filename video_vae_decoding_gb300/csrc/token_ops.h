@@ -94,6 +94,7 @@ struct AttnArgs {
   int q_heads, group;
   float scale_log2;  // scale * log2(e)
   void* workspace;
+  int stall_at1;  // failure self test: 1-based block of keys that is never loaded (0: none)
 };
 // Bytes of workspace of a call (a bound from host-side sizes alone).
 long long kv_attention_workspace(const AttnArgs& a, int sms);

@@ -380,7 +380,8 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     past its last (None: all); a token that sees nothing gets zeros.  scale:
     1 / sqrt(head_dim) by default.  out: like q (new memory by default, where
     rows behind the last sequence stay uninitialised).  return_lse: also the
-    fp32 logarithms of the sums, [tokens, q_heads]."""
+    fp32 logarithms of the sums, [tokens, q_heads].  Rows of NaN throughout
+    mean that a wait inside the kernels ran out (status then holds a code)."""
     short = _short or _short_way()
     if stream is None:
         got = short.attention(q, k_cache, v_cache, pages, lengths, cu_tokens, ranges, scale, out, return_lse, status)
