@@ -482,7 +482,7 @@ wan_status wan_kv_append(const wan_kv_cache* cache, const wan_kv_batch* batch, c
  * q, out: [tokens][q_heads][head_dim] of the cache's dtype with token and head
  * strides; lse (optional): fp32 [tokens][q_heads] contiguous, the natural
  * logarithm of the sum of exp(scale * q . k) (-inf for a token that sees
- * nothing).  Scores, sums and outputs are held in fp32; weights enter the
+ * nothing).  scale: finite, below 2^127 in size.  Scores, sums and outputs are held in fp32; weights enter the
  * product with v as 16-bit values.  workspace: device memory of at least
  * wan_kv_attention_workspace bytes, 16-byte aligned, not used by any other
  * work until this call's is done (its contents need not be kept).  If a wait

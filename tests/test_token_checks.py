@@ -215,3 +215,10 @@ def test_selftest_refusal(lib):
     for D in 0, 60, 264:
         assert lib.wan_selftest_kv_attention_timeout(D, ctypes.byref(code), None) == 1
         assert code.value == 0 and lib.wan_vae_last_error()
+
+
+def test_attention_refuses_a_scale_that_overflows(lib):
+    """A finite scale whose product with log2(e) is no finite float: every score would become NaN or infinite."""
+    for scale in 2.5e38, -3.4e38:
+        assert _attend(lib, scale=scale) == 1, scale
+        assert b"scale" in lib.wan_vae_last_error()

@@ -327,7 +327,8 @@ wan_status wan_kv_attention(const wan_kv_cache* cache, const wan_kv_batch* batch
   API_GUARD({
     AttnArgs a;
     WAN_TRY(attention_args(cache, batch, q_heads, &a));
-    if (!std::isfinite(scale)) return fail(WAN_ERR_INVALID_ARG, "the scale is not finite");
+    a.scale_log2 = (float)(scale * 1.4426950408889634);  // log2(e)
+    if (!std::isfinite(a.scale_log2)) return fail(WAN_ERR_INVALID_ARG, "the scale is not finite, or too large");
     const int T = a.b.T;
     if (q_token < 0 || q_head < 0) return fail(WAN_ERR_INVALID_ARG, "negative stride");
     if ((T > 1 && out_token <= 0) || (q_heads > 1 && out_head <= 0))
@@ -346,7 +347,6 @@ wan_status wan_kv_attention(const wan_kv_cache* cache, const wan_kv_batch* batch
                   (long long)workspace_bytes);
     a.q = q, a.out = out, a.lse = lse, a.ranges = ranges;
     a.q_t = q_token, a.q_h = q_head, a.o_t = out_token, a.o_h = out_head;
-    a.scale_log2 = (float)(scale * 1.4426950408889634);
     a.workspace = workspace;
     if (chunk) {
       chunk = chunk_maps(a, &L);  // without them the split kernel runs (there is room for either)
