@@ -222,3 +222,29 @@ def test_attention_refuses_a_scale_that_overflows(lib):
     for scale in 2.5e38, -3.4e38:
         assert _attend(lib, scale=scale) == 1, scale
         assert b"scale" in lib.wan_vae_last_error()
+
+
+def test_sizes_past_32_bits_are_refused_by_name(lib):
+    """Not cut to their lower half on the way to C (2^32 + 3 tokens of a broadcast tensor cost no memory)."""
+    import video_vae_decoding_gb300 as wv
+    big = 2 ** 32 + 3
+    b = torch.bfloat16
+    kc, pages, lens = torch.zeros(5, 2, 16, 8, dtype=b), torch.zeros(1, 2, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    k = torch.zeros(1, 2, 8, dtype=b).expand(big, 2, 8)
+    with pytest.raises(ValueError, match="4294967299 tokens"):
+        wv.rotary(k, torch.zeros(3, 1, dtype=torch.int32), (4,))
+    with pytest.raises(ValueError, match="4294967299 tokens"):
+        wv.kv_append(k, k, kc, kc, pages, lens)
+    with pytest.raises(ValueError, match="4294967299 tokens"):
+        wv.kv_attention(k, kc, kc, pages, lens)
+    with pytest.raises(ValueError, match="4294967299 heads"):
+        wv.kv_attention(torch.zeros(1, 1, 8, dtype=b).expand(1, big, 8), kc, kc, pages, lens)
+    with pytest.raises(ValueError, match="4294967299 heads"):
+        wv.rotary(torch.zeros(1, 1, 8).expand(1, big, 8), torch.zeros(1, 1, dtype=torch.int32), (4,))
+    wide = torch.zeros(5, 2, 1, 8, dtype=b).expand(5, 2, big, 8)
+    with pytest.raises(ValueError, match="page size"):
+        wv.kv_attention(torch.zeros(1, 2, 8, dtype=b), wide, wide, pages, lens)
+    with pytest.raises(ValueError, match="page size"):
+        wv.kv_check(pages, lens, 2 ** 32 + 16, 5)
+    with pytest.raises(ValueError, match="tokens"):
+        wv.kv_check(pages, lens, 16, 5, tokens=2 ** 32 + 1)

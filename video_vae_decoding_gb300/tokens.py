@@ -98,6 +98,12 @@ def _rows_of(t: torch.Tensor, name: str):
         raise ValueError(f"{name}: the channels of a head must be contiguous")
 
 
+def _int32(n: int, what: str):
+    """Refuses a size that the library's 32-bit argument cannot hold (ctypes would cut it)."""
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{n} {what}: more than 32 bits hold")
+
+
 class _Guard:
     """Makes the tensors' device and the caller's stream current (allocations then belong to that stream)."""
 
@@ -158,6 +164,8 @@ def _turn(x, positions, sections, theta, interleaved, out, stream, inverse):
         B, (T, H, D), xs = 1, shape, (0, *xs)
     else:
         raise ValueError(f"x must be [tokens, heads, head_dim] or [batch, tokens, heads, head_dim], not {tuple(shape)}")
+    for n, what in (B, "sequences"), (T, "tokens"), (H, "heads"), (D, "channels"):
+        _int32(n, what)
     _refuse_grad(x, out)
     rot = _rotation(sections, theta, interleaved)
     dev = x.device
@@ -237,6 +245,8 @@ def _cache(k_cache, v_cache, dev):
         _rows_of(k_cache, "k_cache")
         _rows_of(v_cache, "v_cache")
     pages, heads, size, D = shape
+    for n, what in (heads, "heads"), (size, "keys as page size"), (D, "channels"):
+        _int32(n, what)
     return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), _CODES[dt], heads, size, D, pages, k0, k1, k2, v0, v1,
                        v2), heads, size, D
 
@@ -249,6 +259,8 @@ def _batch(dev, pages, lengths, cu_tokens, tokens, status):
         _on(pages, dev, "pages", _INT32, 2)
         _on(lengths, dev, "lengths", _INT32, 1)
     B, n = pages.shape
+    for m, what in (B, "sequences"), (n, "pages a sequence"), (tokens, "tokens"):
+        _int32(m, what)
     if lengths.shape[0] != B:
         raise ValueError(f"pages has {B} rows for {lengths.shape[0]} sequences")
     p0, p1 = pages.stride()
@@ -334,6 +346,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     else:
         _on(q, dev, "q", (dt,), 3)
         qshape, qs = q.shape, q.stride()
+        _int32(qshape[1], "heads")
         if qshape[0] != T or qshape[2] != D:
             raise ValueError(f"q is {tuple(qshape)}, not [{T}, heads, {D}]")
         if qs[2] != 1:
@@ -395,6 +408,7 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     if q.dtype is not dt or q.device != dev or len(shape) != 3:
         _on(q, dev, "q", (dt,), 3)
     T, H, qD = shape
+    _int32(H, "heads")
     if qD != D:
         raise ValueError(f"q is {tuple(shape)}, the cache's head dim {D}")
     if qs[2] != 1:
@@ -438,6 +452,7 @@ def kv_check(pages: torch.Tensor, lengths: torch.Tensor, page_size: int, n_pages
     cpu = torch.device("cpu")
     if tokens is None:
         tokens = int(cu_tokens[-1]) if cu_tokens is not None else lengths.shape[0]
+    _int32(page_size, "keys as page size")
     b, _ = _batch(cpu, pages, lengths, cu_tokens, tokens, None)
     check(load().wan_kv_check(b, page_size, n_pages, append))
 
