@@ -768,3 +768,20 @@ def test_attention_bounded_wait_expires_and_is_reported(wv, D):
     got, lse = wv.kv_attention(q, kc, vc, pages, lengths, cu, return_lse=True, status=word)
     wv.kv_status(word)
     ref.check_attention(got, lse, ref.attention(q, kc, vc, pages, lengths, cu))
+
+
+@pytest.mark.parametrize("way", ["plain", "subclass"])
+def test_dual_tensors_are_refused_on_both_ways(wv, way):
+    wrap = (lambda t: t) if way == "plain" else (lambda t: t.as_subclass(_Strange))
+    fwd = torch.autograd.forward_ad
+    kc = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    pages = torch.arange(4, dtype=torch.int32).reshape(2, 2).cuda()
+    lens = torch.tensor([3, 5], dtype=torch.int32).cuda()
+    q = wrap(_randn(2, 2, 64, dtype=torch.bfloat16))
+    with fwd.dual_level():
+        dual = fwd.make_dual(q, torch.ones_like(q))
+        for call in (lambda: wv.rotary(dual, _positions(2, 1), (32,)), lambda: wv.kv_append(dual, q, kc, kc.clone(), pages, lens),
+                     lambda: wv.kv_append(q, q, kc, kc.clone(), pages, lens, q=dual), lambda: wv.kv_attention(dual, kc, kc, pages, lens)):
+            with pytest.raises(ValueError, match="autograd"):
+                call()
+        wv.kv_attention(q, kc, kc, pages, lens)

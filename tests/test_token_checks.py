@@ -248,3 +248,24 @@ def test_sizes_past_32_bits_are_refused_by_name(lib):
         wv.kv_check(pages, lens, 2 ** 32 + 16, 5)
     with pytest.raises(ValueError, match="tokens"):
         wv.kv_check(pages, lens, 16, 5, tokens=2 ** 32 + 1)
+
+
+def test_dual_tensors_are_refused(lib):
+    """A tangent would be dropped in silence: the operators are not recorded, forward or backward."""
+    import video_vae_decoding_gb300 as wv
+    fwd = torch.autograd.forward_ad
+    pos = torch.zeros(3, 1, dtype=torch.int32)
+    kc, pages, lens = torch.zeros(5, 2, 16, 8).bfloat16(), torch.zeros(3, 2, dtype=torch.int32), torch.ones(3, dtype=torch.int32)
+    with fwd.dual_level():
+        x = fwd.make_dual(torch.zeros(3, 2, 8), torch.ones(3, 2, 8))
+        k = fwd.make_dual(torch.zeros(3, 2, 8).bfloat16(), torch.ones(3, 2, 8).bfloat16())
+        plain = torch.zeros(3, 2, 8).bfloat16()
+        for call in (lambda: wv.rotary(x, pos, (4,)), lambda: wv.rotary_grad(x, pos, (4,)),
+                     lambda: wv.kv_append(k, plain, kc, kc, pages, lens), lambda: wv.kv_append(plain, k, kc, kc, pages, lens),
+                     lambda: wv.kv_attention(k, kc, kc, pages, lens)):
+            with pytest.raises(ValueError, match="autograd"):
+                call()
+            with torch.no_grad(), pytest.raises(ValueError, match="autograd"):
+                call()
+        with pytest.raises(ValueError, match="CUDA"):            # a plain tensor inside a dual level is none
+            wv.rotary(torch.zeros(3, 2, 8), pos, (4,))

@@ -26,11 +26,12 @@ decltype(&wan_kv_append) f_append;
 decltype(&wan_kv_attention) f_attention;
 decltype(&wan_kv_attention_workspace) f_workspace;
 
-// A plain tensor (no subclass) that needs no gradient; null for anything else.
+// A plain tensor (no subclass) that needs no gradient and carries no tangent; null for anything else.
 const at::Tensor* tensor(PyObject* o) {
   if (!THPVariable_CheckExact(o)) return nullptr;
   const at::Tensor& t = THPVariable_Unpack(o);
-  if (t.layout() != at::kStrided || (t.requires_grad() && at::GradMode::is_enabled())) return nullptr;
+  if (t.layout() != at::kStrided || (t.requires_grad() && at::GradMode::is_enabled()) || t._fw_grad(0).defined())
+    return nullptr;
   return &t;
 }
 

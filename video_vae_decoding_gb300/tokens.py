@@ -11,8 +11,8 @@ turns into frames (wan_rotary, wan_kv_append, wan_kv_attention of
 Work goes to the current stream of the tensors' device, or to ``stream``;
 results and workspaces made here are allocated on that stream.  No call
 waits for the device.  Calls are not recorded by autograd: they refuse tensors
-that require a gradient while gradients are enabled; ``rotary_grad`` is
-``rotary``'s backward pass.
+that require a gradient while gradients are enabled, and dual tensors;
+``rotary_grad`` is ``rotary``'s backward pass.
 """
 
 from __future__ import annotations
@@ -23,6 +23,7 @@ import math
 import struct
 
 import torch
+from torch.autograd import forward_ad
 
 from ._lib import WAN_BF16, WAN_F16, WAN_F32, WanRotation, check, load
 
@@ -82,6 +83,8 @@ def _refuse_grad(*tensors):
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
         raise ValueError("the token operators are not recorded by autograd: detach the tensors (rotary_grad is "
                          "rotary's backward pass)")
+    if any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise ValueError("the token operators are not recorded by autograd: a dual tensor's tangent would be lost")
 
 
 def _on(t: torch.Tensor, device: torch.device, name: str, dtypes=None, dim: int = 0):
