@@ -785,3 +785,38 @@ def test_dual_tensors_are_refused_on_both_ways(wv, way):
             with pytest.raises(ValueError, match="autograd"):
                 call()
         wv.kv_attention(q, kc, kc, pages, lens)
+
+
+@pytest.mark.parametrize("way", ["plain", "subclass"])
+def test_tensors_written_in_place_are_known_to_autograd(wv, way):
+    """A tensor that a call writes to counts a version on, so autograd's check finds what it saved changed; new results
+    and refused calls count none."""
+    wrap = (lambda t: t) if way == "plain" else (lambda t: t.as_subclass(_Strange))
+    kc, vc = (torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pages = torch.arange(4, dtype=torch.int32).reshape(2, 2).cuda()
+    lens = torch.tensor([3, 5], dtype=torch.int32).cuda()
+    q = wrap(_randn(2, 2, 64, dtype=torch.bfloat16))
+    pos, out = _positions(2, 1), torch.empty(2, 2, 64, dtype=torch.bfloat16, device="cuda")
+    versions = lambda: [t._version for t in (q, kc, vc, out, pos, pages)]  # noqa: E731
+    for call, written in ((lambda: wv.rotary(q, pos, (32,), out=out), [0, 0, 0, 1, 0, 0]),
+                          (lambda: wv.rotary_grad(q, pos, (32,), out=q), [1, 0, 0, 0, 0, 0]),
+                          (lambda: wv.kv_append(q, q, kc, vc, pages, lens), [0, 1, 1, 0, 0, 0]),
+                          (lambda: wv.kv_append(q, q, kc, vc, pages, lens, q=q), [0, 1, 1, 0, 0, 0]),
+                          (lambda: wv.kv_append(q, q, kc, vc, pages, lens, q=q, q_out=out), [0, 1, 1, 1, 0, 0]),
+                          (lambda: wv.kv_attention(q, kc, vc, pages, lens, out=out), [0, 0, 0, 1, 0, 0]),
+                          (lambda: wv.kv_attention(q, kc, vc, pages, lens), [0, 0, 0, 0, 0, 0])):
+        before = versions()
+        call()
+        assert [b - a for a, b in zip(before, versions())] == written
+    before = versions()
+    with pytest.raises((ValueError, wv.WanError)):
+        wv.rotary(q, pos, (33,), out=out)
+    assert versions() == before
+    x = torch.ones(2, 2, 64, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    y = (x * out).sum()                                         # saves out
+    wv.rotary(q, pos, (32,), out=out)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():                                # tensors made here have no counter
+        buffer = torch.empty_like(out)
+    assert wv.rotary(q, pos, (32,), out=wrap(buffer)) is not None

@@ -67,8 +67,13 @@ bool result(PyObject* out, const at::Tensor& t, at::Tensor* r) {
   *r = *o;
   return true;
 }
+// Counts the version of a tensor that a call wrote to, for autograd's check of what it saved.
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
 PyObject* give(PyObject* out, at::Tensor&& r) {
   if (out == Py_None) return THPVariable_Wrap(std::move(r));
+  written(r);
   Py_INCREF(out);
   return out;
 }
@@ -193,6 +198,8 @@ PyObject* append(PyObject* const* a) {
                q ? out.data_ptr() : nullptr, q ? out.stride(0) : 0, q ? out.stride(1) : 0, rot, p ? p->data_ptr() : nullptr,
                p && p->scalar_type() == at::kLong, s) != WAN_OK)
     return nullptr;
+  written(*kc);
+  written(*vc);
   if (!q) Py_RETURN_TRUE;
   return give(a[11], std::move(out));
 }

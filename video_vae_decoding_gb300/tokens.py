@@ -107,6 +107,13 @@ def _int32(n: int, what: str):
         raise ValueError(f"{n} {what}: more than 32 bits hold")
 
 
+def _written(*tensors):
+    """Counts the version of tensors that a call wrote to, for autograd's check of what it saved."""
+    for t in tensors:
+        if not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 class _Guard:
     """Makes the tensors' device and the caller's stream current (allocations then belong to that stream)."""
 
@@ -184,7 +191,8 @@ def _turn(x, positions, sections, theta, interleaved, out, stream, inverse):
     if _elsewhere(dev, stream):
         with _Guard(dev, stream):
             return _turn(x, positions, rot, theta, interleaved, out, None, inverse)
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty(shape, dtype=x.dtype, device=dev)
         os = (T * H * D, H * D, D)
     else:
@@ -200,6 +208,8 @@ def _turn(x, positions, sections, theta, interleaved, out, stream, inverse):
                                rot._ref, inverse, _raw_stream(dev.index))
     if status:
         check(status)
+    if given:
+        _written(out)
     return out
 
 
@@ -342,6 +352,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         with _Guard(dev, stream):
             return kv_append(k, v, k_cache, v_cache, pages, lengths, cu_tokens, positions, sections, theta, interleaved, q,
                              q_out, status)
+    given = q_out is not None
     if q is None:
         if q_out is not None:
             raise ValueError("q_out needs q")
@@ -369,6 +380,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
                                   _raw_stream(dev.index))
     if status:
         check(status)
+    _written(k_cache, v_cache, *([q_out] if given else []))
     return q_out
 
 
@@ -426,7 +438,8 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     if _elsewhere(dev, stream):
         with _Guard(dev, stream):
             return kv_attention(q, k_cache, v_cache, pages, lengths, cu_tokens, ranges, scale, out, return_lse, status)
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty(shape, dtype=dt, device=dev)
         os = (H * D, D)
     else:
@@ -445,6 +458,8 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
                                      out.data_ptr(), os[0], os[1], lp, ws.data_ptr(), n, _raw_stream(dev.index))
     if status:
         check(status)
+    if given:
+        _written(out)
     return (out, lse) if return_lse else out
 
 
