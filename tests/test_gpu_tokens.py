@@ -820,3 +820,9 @@ def test_tensors_written_in_place_are_known_to_autograd(wv, way):
     with torch.inference_mode():                                # tensors made here have no counter
         buffer = torch.empty_like(out)
     assert wv.rotary(q, pos, (32,), out=wrap(buffer)) is not None
+
+
+def test_ordinary_calls_are_marshalled_in_cpp(wv):
+    from video_vae_decoding_gb300 import _tokens, tokens
+    wv.rotary(_randn(2, 4, 64), _positions(2, 1), (32,))
+    assert tokens._short is _tokens

@@ -21,6 +21,7 @@ import ctypes
 import functools
 import math
 import struct
+import warnings
 
 import torch
 from torch.autograd import forward_ad
@@ -148,15 +149,35 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+class _Absent:
+    """In the place of _tokens where it is not there: takes no call, so all are marshalled in Python."""
+
+    @staticmethod
+    def _none(*args):
+        return None
+
+    rotary = append = attention = _none
+
+
 def _short_way():
-    """The C++ marshalling of ordinary calls (_tokens), made at the first call: None where it does not take one."""
+    """The C++ marshalling of ordinary calls (_tokens), made at the first call: its functions return None for a call
+    that they do not take."""
     global _short
-    from . import _tokens
+    from . import build
 
     lib = load()
-    _tokens.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-        lib.wan_rotary, lib.wan_kv_append, lib.wan_kv_attention, lib.wan_kv_attention_workspace)))
-    _short = _tokens
+    try:
+        if not build.binding_fits():
+            raise ImportError("it is missing, or made for another Python or torch")
+        from . import _tokens
+
+        _tokens.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.wan_rotary, lib.wan_kv_append, lib.wan_kv_attention, lib.wan_kv_attention_workspace)))
+        _short = _tokens
+    except ImportError as e:
+        warnings.warn(f"the token operators are marshalled in Python, which takes three times the host's time: _tokens.so "
+                      f"cannot be used ({e}); build.build() makes it", RuntimeWarning)
+        _short = _Absent
     return _short
 
 
