@@ -826,3 +826,17 @@ def test_ordinary_calls_are_marshalled_in_cpp(wv):
     from video_vae_decoding_gb300 import _tokens, tokens
     wv.rotary(_randn(2, 4, 64), _positions(2, 1), (32,))
     assert tokens._short is _tokens
+
+
+@pytest.mark.parametrize("group", [1, 8, 9, 16])
+@pytest.mark.parametrize("lens", [[64], [40, 64, 17, 1], [130, 100]], ids=str)
+def test_weights_of_few_rows_lose_nothing(wv, lens, group):
+    """The few-row kernel's weights enter the product with v in two parts, in float16 as in bfloat16: the bound is that
+    of 32-bit weights (the form for float32 queries), twice over for the parts' 2^-21, and what the least float16 value
+    and its half add for each key, 1.5 * 2^-36 of the largest weight."""
+    q, kc, vc, pages, lengths, cu = _attention_case(wv, lens, 4, group, 64, 16, torch.float16)
+    q = (q / 8).half()                                          # scores of about one: many weights count
+    got, lse = wv.kv_attention(q, kc, vc, pages, lengths, return_lse=True)
+    out, err, z, zerr = ref.attention(q.float(), kc, vc, pages, lengths)
+    floor = max(lens) * 1.5 * 2.0 ** -36 * vc.abs().max().double()
+    ref.check_attention(got, lse, (out, 2 * err + floor, z, zerr))
