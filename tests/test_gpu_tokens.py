@@ -840,3 +840,35 @@ def test_weights_of_few_rows_lose_nothing(wv, lens, group):
     out, err, z, zerr = ref.attention(q.float(), kc, vc, pages, lengths)
     floor = max(lens) * 1.5 * 2.0 ** -36 * vc.abs().max().double()
     ref.check_attention(got, lse, (out, 2 * err + floor, z, zerr))
+
+
+def test_inputs_outlive_a_call_on_another_stream(wv):
+    """Tensors of the current stream handed to a call on another one and dropped at once: their memory goes to nobody
+    else before that stream has read them."""
+    s = torch.cuda.Stream()
+    kc, vc = (_randn(8, 2, 16, 64, dtype=torch.bfloat16, seed=i) for i in (1, 2))
+    pages = torch.arange(8, dtype=torch.int32).reshape(1, 8).cuda()
+    lens, cu = torch.tensor([100], dtype=torch.int32).cuda(), torch.tensor([0, 40], dtype=torch.int32).cuda()
+    keep = [_randn(40, 2, 64, dtype=torch.bfloat16, seed=i) for i in (3, 4, 5)]
+    pos = _positions(40, 1)
+    want_rot = wv.rotary(keep[0], pos, (32,))
+    want_out = wv.kv_attention(keep[0], kc, vc, pages, lens, cu)
+    k2, v2 = kc.clone(), vc.clone()
+    want_q = wv.kv_append(keep[1], keep[2], k2, v2, pages, lens, cu, pos, (32,), q=keep[0])
+
+    def overwritten(call):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)                        # 10 ms: s starts after all below is done
+        got = call()
+        junk = [torch.full((40, 2, 64), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(64)]
+        junk += [torch.full((40, 1), 9, dtype=torch.int32, device="cuda") for _ in range(64)]
+        torch.cuda.synchronize()
+        del junk
+        return got
+    copy = lambda i: keep[i].clone()  # noqa: E731  in memory that only the call holds
+    assert torch.equal(overwritten(lambda: wv.rotary(copy(0), pos.clone(), (32,), stream=s)), want_rot)
+    assert torch.equal(overwritten(lambda: wv.kv_attention(copy(0), kc, vc, pages.clone(), lens.clone(), cu.clone(), stream=s)), want_out)
+    assert torch.equal(overwritten(lambda: wv.kv_append(copy(1), copy(2), kc, vc, pages, lens.clone(), cu.clone(), pos.clone(), (32,),
+                                                        q=copy(0), stream=s)), want_q)
+    assert torch.equal(kc, k2) and torch.equal(vc, v2)

@@ -8,8 +8,9 @@ turns into frames (wan_rotary, wan_kv_append, wan_kv_attention of
     q = kv_append(k, v, k_cache, v_cache, pages, lengths, cu_tokens=cu, positions=pos, sections=(22, 21, 21), q=q)
     out = kv_attention(q, k_cache, v_cache, pages, lengths, cu_tokens=cu)
 
-Work goes to the current stream of the tensors' device, or to ``stream``;
-results and workspaces made here are allocated on that stream.  No call
+Work goes to the current stream of the tensors' device, or to ``stream``
+(which has to wait for what makes the tensors; they may be dropped after the
+call); results and workspaces made here are allocated on that stream.  No call
 waits for the device.  Calls are not recorded by autograd: they refuse tensors
 that require a gradient while gradients are enabled, and dual tensors;
 ``rotary_grad`` is ``rotary``'s backward pass.
@@ -116,12 +117,14 @@ def _written(*tensors):
 
 
 class _Guard:
-    """Makes the tensors' device and the caller's stream current (allocations then belong to that stream)."""
+    """Makes the tensors' device and the caller's stream current (allocations then belong to that stream).  The memory of
+    `tensors` is not given to other work before the stream is done with the call, even if the caller drops them."""
 
-    __slots__ = ("_guards",)
+    __slots__ = ("_guards", "_stream", "_tensors")
 
-    def __init__(self, device: torch.device, stream):
+    def __init__(self, device: torch.device, stream, *tensors):
         self._guards = [torch.cuda.device(device)]
+        self._stream, self._tensors = stream, tensors
         if stream is not None:
             if stream.device != device:
                 raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
@@ -132,6 +135,10 @@ class _Guard:
             g.__enter__()
 
     def __exit__(self, *exc):
+        if self._stream is not None:
+            for t in self._tensors:
+                if t is not None:
+                    t.record_stream(self._stream)
         for g in reversed(self._guards):
             g.__exit__(*exc)
         return False
@@ -210,7 +217,7 @@ def _turn(x, positions, sections, theta, interleaved, out, stream, inverse):
     if xs[3] != 1:
         _rows_of(x, "x")
     if _elsewhere(dev, stream):
-        with _Guard(dev, stream):
+        with _Guard(dev, stream, x, positions, out):
             return _turn(x, positions, rot, theta, interleaved, out, None, inverse)
     given = out is not None
     if not given:
@@ -370,7 +377,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     elif positions is not None:
         raise ValueError("positions need sections")
     if _elsewhere(dev, stream):
-        with _Guard(dev, stream):
+        with _Guard(dev, stream, k, v, k_cache, v_cache, pages, lengths, cu_tokens, positions, q, q_out, status):
             return kv_append(k, v, k_cache, v_cache, pages, lengths, cu_tokens, positions, sections, theta, interleaved, q,
                              q_out, status)
     given = q_out is not None
@@ -457,7 +464,7 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
             raise ValueError(f"ranges must be contiguous [{T}, 2], not {tuple(ranges.shape)}")
         rp = ranges.data_ptr()
     if _elsewhere(dev, stream):
-        with _Guard(dev, stream):
+        with _Guard(dev, stream, q, k_cache, v_cache, pages, lengths, cu_tokens, ranges, out, status):
             return kv_attention(q, k_cache, v_cache, pages, lengths, cu_tokens, ranges, scale, out, return_lse, status)
     given = out is not None
     if not given:
