@@ -389,7 +389,8 @@ wan_status wan_causal_conv3d_noalloc(const void* x, int32_t B, int32_t n_hist, i
  * channels (j, j + pairs).  Channels past 2 * pairs pass through.  freq and
  * axis are HOST arrays of `pairs` values, read during the call.  Angles are
  * formed modulo one turn in 64-bit integers, so positions may be negative or
- * far: the angle is off by the rounding of freq to 2^-52 times the position. */
+ * far: an angle is off by pi 2^-25 radians, and by the position times the
+ * rounding of freq to 2^-52 of itself. */
 typedef struct {
   int32_t pairs;        /* 1 .. 128 */
   int32_t axes;         /* coordinates per position, 1 .. 4 */

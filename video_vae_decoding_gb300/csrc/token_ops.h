@@ -22,9 +22,9 @@ enum TokenError : int {
 };
 
 // Pair j turns by position[axis[j]] * turn[j], in units of 2^-64 of a full
-// turn: the 64-bit product wraps exactly as the angle does, so the angle keeps
-// 2^-32 of a turn however far the position is, without any 64-bit floating
-// point and without a table.
+// turn: the 64-bit product wraps exactly as the angle does, without any 64-bit
+// floating point and without a table.  What a far position loses is the
+// frequency's own rounding (2^-52 of itself, and 2^-64 of a turn) times it.
 struct RotaryPlan {
   uint64_t turn[kMaxRotaryPairs];
   uint8_t axis[kMaxRotaryPairs];
