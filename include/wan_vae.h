@@ -436,7 +436,9 @@ typedef struct {
  * status: an int32 in device memory, or NULL.  A page number outside the
  * cache, a length that the table cannot hold, or token ranges that are no
  * ranges of the `tokens` rows, are left out by the kernels (no access, a key
- * that nobody sees, no tokens) and leave a code there if it was 0. */
+ * that nobody sees, no tokens) and leave a code there if it was 0.  Ranges
+ * behind one that is none may overlap earlier ones: such rows hold one
+ * sequence's results or the other's, or nothing. */
 typedef struct {
   const int32_t* pages;
   int64_t page_stride;
@@ -483,8 +485,18 @@ wan_status wan_kv_append(const wan_kv_cache* cache, const wan_kv_batch* batch, c
  * q, out: [tokens][q_heads][head_dim] of the cache's dtype with token and head
  * strides; lse (optional): fp32 [tokens][q_heads] contiguous, the natural
  * logarithm of the sum of exp(scale * q . k) (-inf for a token that sees
- * nothing).  scale: finite, below 2^127 in size.  Scores, sums and outputs are held in fp32; weights enter the
- * product with v as 16-bit values.  workspace: device memory of at least
+ * nothing).  scale: finite, below 2^127 in size.  out may be q.
+ * Scores, sums and outputs are held in fp32.  Two kernels share the calls, and
+ * their results differ in the last bits.  In the one for few rows weights enter
+ * the product with v in two 16-bit parts: the result is off by its own rounding
+ * alone.  The one for many rows rounds them once, to the cache's type: the
+ * result is off by 1.2 to 1.4 times that (in float16 a weight under 2^-31 of its
+ * row's largest is lost).  It is taken from 64 rows a sequence on average
+ * (tokens * q_heads / heads rows) in calls of 6e5 products or more (tokens *
+ * q_heads * the keys that the table has room for); it takes pages of a multiple
+ * of 8 keys, or of more than 64, and k and v with their dimensions in one order.
+ * Other calls of many rows go by the first one and take ten times as long.
+ * workspace: device memory of at least
  * wan_kv_attention_workspace bytes, 16-byte aligned, not used by any other
  * work until this call's is done (its contents need not be kept).  If a wait
  * inside the kernel for many tokens runs out (after about a second; none does

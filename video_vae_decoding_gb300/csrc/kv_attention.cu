@@ -20,11 +20,11 @@
 //  - a row tile that a cut divides leaves partial (m, l, o) in the workspace,
 //    and a second kernel, launched to start as the first drains, joins them in
 //    the order of the keys: the result does not depend on timing.
-// Two sequences of up to 131k keys, 64 heads of 128 on 8, take 151 us, 6.6 TB/s
-// (0.98 of a plain copy's rate); 64 ragged ones of up to 8000 keys, 32 heads on 8,
-// 180 us, 6.1 TB/s; one of 1000 keys 10 us, of which the keys take 2.  (With a
+// Two sequences of up to 131k keys, 64 heads of 128 on 8 (0.96 GB), take 154 us, 6.2
+// TB/s (0.92 of a plain copy's rate); 64 ragged ones of up to 8000 keys, 32 heads on 8
+// (1.04 GB), 177 us, 5.9 TB/s; one of 1000 keys 9 us, of which the keys take 2.  (With a
 // block's four warps on one row tile, merged through shared memory at its end, the
-// first two took 162 and 182 us.)
+// first two took 11 and 2 us more.)
 // Sums, maxima and outputs are held in 32 bits; how the weights are rounded is
 // told at Weights.
 #include <algorithm>
@@ -39,8 +39,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRows = 16;    // rows of a tile: the MMA's M
 constexpr int kKeys = 16;    // keys of a tile
-// Least tiles of a piece.  One, since a warp's wait for its next tile costs more than a further part in the join: one
-// sequence of 1000 keys takes 10.1 us, with two tiles 12.2; long ones never come to the limit.
+// Least tiles of a piece.  One, since a warp's wait for its next tile costs more than a further part in the join: with
+// two, one sequence of 1000 keys takes 2.1 us more; long ones never come to the limit.
 constexpr int kLeast = 1;
 
 template <int DP>

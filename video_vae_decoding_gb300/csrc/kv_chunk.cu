@@ -29,9 +29,9 @@
 //
 // Bound: the tensor cores, 4 D operations per row and key; K and V come through
 // a ring each and serve both halves, so a block of 128 keys asks 64 KB (D = 128) for
-// 33.6 MFLOP.  880 tokens of 16 heads of 128 against 27,280 keys take 169 us, 1.17
-// PFLOP/s (61% of a large library product's); with heads of 64 136 us, where the
-// softmax bounds, and with 8 heads of 256 251 us: 128 KB a block for 16.8 MFLOP is 8
+// 33.6 MFLOP.  880 tokens of 16 heads of 128 against 27,280 keys take 171 us, 1.15
+// PFLOP/s (60% of a large library product's); with heads of 64 135 us, where the
+// softmax bounds, and with 8 heads of 256 248 us: 128 KB a block for 16.8 MFLOP is 8
 // TB/s from the L2.
 // V is taken as it lies in the cache, [key][channel]: the MMA's second operand
 // with its N dimension contiguous, so nothing is transposed on the way.
@@ -81,8 +81,12 @@ struct Cfg {
   static constexpr int kSmem = kQ + kKeySlots * kKeySlot + kValSlots * kValSlot + 1024 + 1024;
 };
 
-// Weights 2^(x - m) reach 2^kSlack; in float16 they are taken 2^7 times larger
-// (65504 is the end), so that keys down to 2^-31 of the largest still count.
+// Weights 2^(x - m) are rounded once to the operands' type: a second part would add
+// half to the products, which bound this kernel, and TMEM has no room for it at 128
+// channels.  880 tokens against 27,280 keys in bfloat16 are then off by 2.3e-3 (1.7e-3
+// is the result's rounding alone), ragged chunks in float16 by 2.9e-4 (2.1e-4).
+// Weights reach 2^kSlack; in float16 they are taken 2^7 times larger (65504 is the
+// end), so that keys down to 2^-31 of the largest still count.
 template <typename T>
 struct Pack;
 template <>

@@ -434,10 +434,17 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     q [tokens, q_heads, head_dim]; caches, pages, lengths, cu_tokens, status as
     in kv_append.  ranges [tokens, 2] int32: the first key a token sees and one
     past its last (None: all); a token that sees nothing gets zeros.  scale:
-    1 / sqrt(head_dim) by default.  out: like q (new memory by default, where
-    rows behind the last sequence stay uninitialised).  return_lse: also the
+    1 / sqrt(head_dim) by default.  out: like q, or q itself (new memory by
+    default, where rows behind the last sequence stay uninitialised).  return_lse: also the
     fp32 logarithms of the sums, [tokens, q_heads].  Rows of NaN throughout
-    mean that a wait inside the kernels ran out (status then holds a code)."""
+    mean that a wait inside the kernels ran out (status then holds a code).
+
+    Calls of few rows (tokens * q_heads / kv_heads; under 64 a sequence on
+    average, or a small call) give results off by their own rounding alone; the
+    tensor-core kernel for more rows rounds the weights to 16 bits, so its results
+    are off by 1.2 to 1.4 times that.  It takes page sizes that are multiples of 8
+    or above 64, and caches whose k and v order their dimensions alike; with
+    others, calls of many rows take ten times as long."""
     short = _short or _short_way()
     if stream is None:
         got = short.attention(q, k_cache, v_cache, pages, lengths, cu_tokens, ranges, scale, out, return_lse, status)
