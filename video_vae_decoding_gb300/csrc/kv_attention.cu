@@ -20,9 +20,9 @@
 //  - a row tile that a cut divides leaves partial (m, l, o) in the workspace,
 //    and a second kernel, launched to start as the first drains, joins them in
 //    the order of the keys: the result does not depend on timing.
-// Two sequences of up to 131k keys, 64 heads of 128 on 8 (0.96 GB), take 154 us, 6.2
+// Two sequences of up to 131k keys, 64 heads of 128 on 8 (0.96 GB), take 153 us, 6.3
 // TB/s (0.92 of a plain copy's rate); 64 ragged ones of up to 8000 keys, 32 heads on 8
-// (1.04 GB), 177 us, 5.9 TB/s; one of 1000 keys 9 us, of which the keys take 2.  (With a
+// (1.04 GB), 176 us, 5.9 TB/s; one of 1000 keys 9 us, of which the keys take 2.  (With a
 // block's four warps on one row tile, merged through shared memory at its end, the
 // first two took 11 and 2 us more.)
 // Sums, maxima and outputs are held in 32 bits; how the weights are rounded is

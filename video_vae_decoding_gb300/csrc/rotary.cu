@@ -16,14 +16,14 @@
 // itself is.  A product in 32-bit floating point loses the fraction of a turn from a
 // few thousand positions on, and 64-bit floating point runs at a small
 // fraction of the rate here.
-// 27,280 tokens of 16 heads of 128 in bf16 take 35.7 us, 6.3 TB/s (0.93 of a plain
-// copy's rate); the gradient of 16,380 tokens of 12 heads of 80 in fp32 20.7 us
-// (0.90).  (Cosines and sines formed once per block in shared memory, with a
+// 27,280 tokens of 16 heads of 128 in bf16 take 35.7 us, 6.3 TB/s (0.92 of a plain
+// copy's rate); the gradient of 16,380 tokens of 12 heads of 80 in fp32 20.8 us
+// (0.89).  (Cosines and sines formed once per block in shared memory, with a
 // barrier for each group of tokens: 43 us; eight heads' loads with the tables of
 // several tokens in registers: 62 us, at 121 registers.)
 // The append is bound by the chain token range -> length -> page -> store at three
 // waves of blocks: 3520 tokens with queries 16.4 us (0.78 of the copy's rate), seven
-// ragged prompts, whose tokens search for their sequence, 22.4 us (0.66).  (Looked up
+// ragged prompts, whose tokens search for their sequence, 22.5 us (0.69).  (Looked up
 // once per block through shared memory: 17.8 and 26.5; ahead of the angles: 16.1 and
 // 23.3.)
 #include <cuda_bf16.h>
