@@ -872,3 +872,19 @@ def test_inputs_outlive_a_call_on_another_stream(wv):
     assert torch.equal(overwritten(lambda: wv.kv_append(copy(1), copy(2), kc, vc, pages, lens.clone(), cu.clone(), pos.clone(), (32,),
                                                         q=copy(0), stream=s)), want_q)
     assert torch.equal(kc, k2) and torch.equal(vc, v2)
+
+
+def test_refusals_on_another_stream_keep_their_words(wv):
+    s = torch.cuda.Stream()
+    kc = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    pages = torch.arange(4, dtype=torch.int32).reshape(2, 2).cuda()
+    lens = torch.tensor([3, 5], dtype=torch.int32).cuda()
+    q = _randn(2, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="q is on cpu"):
+        wv.kv_append(q, q, kc, kc.clone(), pages, lens, q=q.cpu(), stream=s)
+    with pytest.raises(ValueError, match="out is on cpu"):
+        wv.kv_attention(q, kc, kc, pages, lens, out=q.cpu(), stream=s)
+    with pytest.raises(ValueError, match="out is on cpu"):
+        wv.rotary(q, _positions(2, 1), (32,), out=q.cpu(), stream=s)
+    with pytest.raises(ValueError, match="on cuda|CUDA|cpu"):
+        wv.kv_attention(q.cpu(), kc, kc, pages, lens, stream=s)

@@ -135,7 +135,7 @@ class _Guard:
             g.__enter__()
 
     def __exit__(self, *exc):
-        if self._stream is not None:
+        if self._stream is not None and exc[0] is None:
             for t in self._tensors:
                 if t is not None:
                     t.record_stream(self._stream)
