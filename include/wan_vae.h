@@ -511,6 +511,79 @@ wan_status wan_kv_attention(const wan_kv_cache* cache, const wan_kv_batch* batch
  * current device (-1 and an error message if it would refuse them). */
 int64_t wan_kv_attention_workspace(const wan_kv_cache* cache, const wan_kv_batch* batch, int32_t q_heads);
 
+/* Attention as wan_kv_attention's, of tokens that are the last keys of their
+ * sequences (as wan_kv_append leaves them: a sequence of n keys and m new tokens
+ * has them at places n - m .. n - 1), each seeing keys by its place.
+ *
+ * window: the first `sinks` keys and a window of whole frames of `frame` keys: a
+ * token at place p, in frame f = p / frame, sees the keys of frames f - window + 1
+ * .. f that the sequence has (its own frame's later keys too).  frame 1: the
+ * last `window` keys up to its own.  window, frame: 1 or more; sinks: 0 or more.
+ *
+ * tree: the keys ahead of the sequence's new tokens, and of the new tokens itself
+ * and its ancestors.  parents: device int32 [tokens], the place of a token's
+ * parent among its sequence's new tokens (0 for the first), which comes before
+ * it, or -1 for none.  One that does not come before its child counts as none
+ * and leaves a code in the batch's status word.  A row's mask is found by a walk
+ * up the tree, so a call takes time by its depth; what is a chain throughout is
+ * better a range.
+ *
+ * A sequence with more new tokens than keys gets zeros and leaves a code in the
+ * status word.  Pages that hold no key that any token sees (between the first
+ * keys and the windows) are not read, and their numbers in the table may be
+ * anything.  Precision, kernels, errors and the other arguments are those of
+ * wan_kv_attention; workspace: wan_kv_masked_attention_workspace bytes. */
+wan_status wan_kv_window_attention(const wan_kv_cache* cache, const wan_kv_batch* batch, const void* q, int32_t q_heads,
+                                   int64_t q_token, int64_t q_head, int32_t window, int32_t sinks, int32_t frame,
+                                   float scale, void* out, int64_t out_token, int64_t out_head, float* lse,
+                                   void* workspace, int64_t workspace_bytes, wan_cuda_stream stream);
+wan_status wan_kv_tree_attention(const wan_kv_cache* cache, const wan_kv_batch* batch, const void* q, int32_t q_heads,
+                                 int64_t q_token, int64_t q_head, const int32_t* parents, float scale, void* out,
+                                 int64_t out_token, int64_t out_head, float* lse, void* workspace,
+                                 int64_t workspace_bytes, wan_cuda_stream stream);
+/* Bytes of workspace that either needs for these sizes on the current device
+ * (-1 and an error message if they would be refused). */
+int64_t wan_kv_masked_attention_workspace(const wan_kv_cache* cache, const wan_kv_batch* batch, int32_t q_heads);
+
+/* Sequences become copies of others.  pages ([sequences] rows of max_pages
+ * numbers, page_stride apart) and lengths [sequences] are the cache's tables, in
+ * device memory, and are written.  For i = 0 .. forks - 1, with n the keys of
+ * sequence sources[i] (as lengths has them before the call): the first numbers of
+ * row targets[i], one for each page of the n keys, become
+ *   share 1: those of row sources[i] for whole pages, and fresh[i * fresh_stride]
+ *            for the last page if it is partly filled, whose keys are copied
+ *            there (later tokens then go to pages of each sequence's own);
+ *   share 0: fresh[i * fresh_stride ..], and all keys are copied;
+ * and lengths[targets[i]] becomes n.  Only the n keys' rows of the fresh pages
+ * are written; numbers behind them stay.  Fresh pages belong to nobody else: the
+ * cache's pages are the caller's to hand out and to take back.  sources,
+ * targets [forks], fresh [forks] rows of fresh_pages numbers: device int32.  A
+ * fork is left out, with a code in status, if its sequences or the source's
+ * length are none of the table's, if fresh_pages are too few, or if its target
+ * is a source of the call, or the target of an earlier fork.  A page number
+ * outside the cache: what it would hold is not copied, and a code is left.
+ * forks: up to 1024.  Errors: WAN_ERR_INVALID_ARG, WAN_ERR_DTYPE,
+ * WAN_ERR_UNSUPPORTED, WAN_ERR_CUDA. */
+wan_status wan_kv_fork(const wan_kv_cache* cache, int32_t* pages, int64_t page_stride, int32_t max_pages,
+                       int32_t sequences, int32_t* lengths, const int32_t* sources, const int32_t* targets,
+                       const int32_t* fresh, int64_t fresh_stride, int32_t fresh_pages, int32_t forks, int32_t share,
+                       int32_t* status, wan_cuda_stream stream);
+
+/* Moves the keys and values that are kept together, in place.  In the batch,
+ * lengths[b] = f counts the first keys of sequence b that stay where they are,
+ * and cu_tokens (not NULL) its range of keep (`tokens` numbers, device int32):
+ * the key at place keep[cu_tokens[b] + j] moves to place f + j, all as if at
+ * once, and lengths[b], the call's result, becomes f plus their count.  A key
+ * moves ahead or stays: one with keep[..] < f + j, or one that the table has no
+ * page for, is left out (place f + j keeps what it had) with a code in the
+ * batch's status word; so is a sequence whose f, range or result the table
+ * cannot hold (none of its keys move, and its result is f, or 0 where f is none).
+ * Several sequences of a call must not share a page that the call writes to or
+ * that one of them reads from and another writes.  lengths: device int32, not in
+ * the memory that the call reads.  heads: up to 1000.  Errors: as above. */
+wan_status wan_kv_compact(const wan_kv_cache* cache, const wan_kv_batch* batch, const int32_t* keep, int32_t* lengths,
+                          wan_cuda_stream stream);
+
 /* Failure-detection self test of wan_kv_attention's kernel for many tokens, in
  * the form of wan_selftest_attention_timeout: a small call (bf16, zeros in) at
  * this head dim (a multiple of 8 up to 256) whose loader withholds the first

@@ -27,7 +27,8 @@ import ctypes
 import torch
 
 from ._lib import PROFILE_KINDS, WAN_BF16, WAN_F32, WanError, WanProfile, WanTensor, check, load  # noqa: F401
-from .tokens import Rotation, kv_append, kv_attention, kv_check, kv_status, rotary, rotary_grad
+from .tokens import (Rotation, kv_append, kv_attention, kv_check, kv_compact, kv_fork, kv_status, kv_tree_attention,
+                     kv_window_attention, rotary, rotary_grad)
 
 __all__ = ["Model", "DecodeStream", "decode", "attention_block", "causal_conv3d", "out_frames", "WanError",
            "Rotation", "rotary", "rotary_grad", "kv_append", "kv_attention", "kv_check", "kv_status"]

@@ -143,9 +143,20 @@ struct Tiles {
   int key_tiles;
   long long all;
 };
+// With X (rows see by their place) a row tile's key tiles are those that some row of it sees, numbered without the
+// gap between the first keys and the window; as many as the widest row tile can have stand on the line, the others
+// leave their last ones empty.
+template <bool X>
 __device__ __forceinline__ Tiles tiles_of(const AttnArgs& a, const Seq& s) {
   Tiles t;
   t.key_tiles = (s.len + kKeys - 1) / kKeys;
+  if (X && a.mask == kMaskWindow) {
+    // the tokens of 16 rows reach over 15 / group + 1 steps at most, each of which can begin a frame
+    const uint32_t steps = s.n > 1 ? min((uint32_t)(s.n - 1), (uint32_t)((kRows - 1) / a.group + 1)) : 0;
+    const uint32_t reach = steps == 0 ? 0 : a.frame >= steps ? a.frame : ((steps - 1) / a.frame + 1) * a.frame;
+    const uint32_t most = (a.span + reach) / kKeys + 2 + ((uint32_t)a.sinks + kKeys - 1) / kKeys;
+    t.key_tiles = (int)min((uint32_t)t.key_tiles, most);
+  }
   t.all = ((long long)s.n * a.group + kRows - 1) / kRows * a.c.heads * t.key_tiles;
   return t;
 }
@@ -167,7 +178,7 @@ long long space_bytes(int DP, int G) {
   return (long long)G * (sizeof(Open) + 2 * kRows * (sizeof(float2) + (size_t)DP * sizeof(float)));
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool X>
 __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
     kv_split_kernel(const __grid_constant__ AttnArgs a) {
   using C = Cfg<DP>;
@@ -190,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
   asm volatile("griddepcontrol.wait;" ::: "memory");  // for what came before on the stream
 
   const Piece pc = cut_line<kWarps, kWarps>(a.b.B, kLeast, s_line,
-                                            [&](int b) { return tiles_of(a, sequence(a, b, false)).all; });
+                                            [&](int b) { return tiles_of<X>(a, sequence(a, b, false)).all; });
   if (lane == 0) ws.open[me].parts = 0;
   int b = pc.b;
   long long at = pc.at;
@@ -199,11 +210,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
 
   for (long long line = pc.beg; line < pc.end;) {
     Seq s = sequence(a, b, false);
-    Tiles tl = tiles_of(a, s);
+    Tiles tl = tiles_of<X>(a, s);
     while (at >= tl.all) {  // the next sequence with a tile
       at -= tl.all;
       s = sequence(a, ++b, false);
-      tl = tiles_of(a, s);
+      tl = tiles_of<X>(a, s);
     }
     // the run: key tiles [kt0, kt1) of one row tile and head
     const int seg = (int)quotient(at, tl.key_tiles), kt0 = (int)(at - (long long)seg * tl.key_tiles);
@@ -216,36 +227,70 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
     // the keys that this thread's two rows see, and those that any row does
     const int r_a = lane >> 2, r_b = r_a + 8;
     int lo_a = 0, hi_a = 0, lo_b = 0, hi_b = 0, lo = 0, hi = s.len;
-    if (!a.ranges) {
-      if (r_a < cnt) hi_a = hi;
-      if (r_b < cnt) hi_b = hi;
+    // rows of one token, or of tokens that see the same keys, see all that is fetched: they need no mask of their own
+    bool mixed = false;
+    // with X: lane r's row sees `mine`; some row of the tile [0, c) and [lo, hi), all of them [0, c_all) and [lo_all,
+    // hi_all); key tiles of the first keys, and how many are skipped behind them
+    Sight mine{0, 0, 0};
+    int c = 0, c_all = 0, lo_all = 0, hi_all = 0, first_tiles = 0, skip = 0;
+    int w0, w1;
+    if constexpr (X) {
+      const int row = row0 + min(lane, cnt - 1), ahead = row0 / a.group;
+      mine = sight(a, s, row / a.group);
+      mixed = ahead != (row0 + cnt - 1) / a.group;
+      c = c_all = mine.c;
+      lo = lo_all = mine.lo;
+      hi = hi_all = mine.hi;
+      if (mixed) {
+        c = __reduce_max_sync(0xffffffffu, c), c_all = __reduce_min_sync(0xffffffffu, c_all);
+        lo = __reduce_min_sync(0xffffffffu, lo), lo_all = __reduce_max_sync(0xffffffffu, lo_all);
+        hi = __reduce_max_sync(0xffffffffu, hi), hi_all = __reduce_min_sync(0xffffffffu, hi_all);
+      }
+      if (a.mask == kMaskTree) {  // all drafts are fetched, whoever sees them: even a single row has a mask
+        hi = s.len;
+        mixed = true;
+      }
+      if (lo <= c) c = lo = 0;
+      first_tiles = (c + kKeys - 1) / kKeys;
+      const int from = max(lo / kKeys, first_tiles);
+      skip = from - first_tiles;
+      w0 = kt0, w1 = min(kt1, (hi + kKeys - 1) / kKeys - skip);
     } else {
-      int f = 0, e = 0;  // lane r holds row r's
-      if (lane < cnt) seen_range(a, s.r0 + (row0 + lane) / a.group, s.len, &f, &e);
-      lo_a = __shfl_sync(0xffffffffu, f, r_a), hi_a = __shfl_sync(0xffffffffu, e, r_a);
-      lo_b = __shfl_sync(0xffffffffu, f, r_b), hi_b = __shfl_sync(0xffffffffu, e, r_b);
-      lo = __reduce_min_sync(0xffffffffu, f < e ? f : 0x7fffffff);
-      hi = __reduce_max_sync(0xffffffffu, e);
+      if (!a.ranges) {
+        if (r_a < cnt) hi_a = hi;
+        if (r_b < cnt) hi_b = hi;
+      } else {
+        int f = 0, e = 0;  // lane r holds row r's
+        if (lane < cnt) seen_range(a, s.r0 + (row0 + lane) / a.group, s.len, &f, &e);
+        lo_a = __shfl_sync(0xffffffffu, f, r_a), hi_a = __shfl_sync(0xffffffffu, e, r_a);
+        lo_b = __shfl_sync(0xffffffffu, f, r_b), hi_b = __shfl_sync(0xffffffffu, e, r_b);
+        lo = __reduce_min_sync(0xffffffffu, f < e ? f : 0x7fffffff);
+        hi = __reduce_max_sync(0xffffffffu, e);
+      }
+      const bool differ = (r_a < cnt && (lo_a != lo || hi_a != hi)) || (r_b < cnt && (lo_b != lo || hi_b != hi));
+      mixed = __any_sync(0xffffffffu, differ);
+      w0 = hi > 0 ? max(kt0, lo / kKeys) : kt1, w1 = min(kt1, (hi + kKeys - 1) / kKeys);
     }
-    // rows of one token, or of tokens that see the same keys, need no mask of their own
-    const bool differ = (r_a < cnt && (lo_a != lo || hi_a != hi)) || (r_b < cnt && (lo_b != lo || hi_b != hi));
-    const bool mixed = __any_sync(0xffffffffu, differ);
+    // first key of key tile kt, and whether some row sees a key
+    auto key_of = [&](int kt) { return (X && kt >= first_tiles ? kt + skip : kt) * kKeys; };
+    auto in_sight = [&](int key) { return (key >= lo && key < hi) || (X && key < c); };
+    uint64_t drafts = 0;  // of the drafts from this one on, those that the lane's row sees
+    int drafts_from = -64;
 
     const int* table = a.b.pages + b * a.b.page_stride;
-    const int w0 = hi > 0 ? max(kt0, lo / kKeys) : kt1, w1 = min(kt1, (hi + kKeys - 1) / kKeys);
 
     // The page of this lane's key in tile kt (lane & 15), asked for a tile ahead of
     // the loads that need it; -1 if no row sees the key.
     auto lookup = [&](int kt) {
-      const int key = kt * kKeys + (lane & 15);
-      return kt < w1 && key >= lo && key < hi ? table[key / a.c.page_size] : -1;
+      const int key = key_of(kt) + (lane & 15);
+      return kt < w1 && in_sight(key) ? table[key / a.c.page_size] : -1;
     };
     auto issue = [&](int kt, int page) {
       const int st = kt % ST;
-      const int key = kt * kKeys + (lane & 15);
+      const int key = key_of(kt) + (lane & 15);
       const uint32_t dk = ring_a + st * 2 * C::kHalf, dv = dk + C::kHalf;
       const bool take = page >= 0 && page < a.c.pages;
-      if (!take && key >= lo && key < hi && a.b.status) atomicCAS(a.b.status, 0, (int)kDevBadPage);
+      if (!take && in_sight(key) && a.b.status) atomicCAS(a.b.status, 0, (int)kDevBadPage);
       long long ko = 0, vo = 0;
       if (take) {
         const int off = key % a.c.page_size;
@@ -324,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
       const uint32_t sk = ring_a + st * 2 * C::kHalf, sv = sk + C::kHalf;
       const uint32_t seen = s_seen[warp][st];
       if (seen) {
-        const int key0 = kt * kKeys;
+        const int key0 = key_of(kt);
         float sc[2][4] = {};
         const int kr = ((lane >> 4) << 3) + (lane & 7);
         const uint32_t krow = sk + kr * DP * 2;
@@ -344,17 +389,42 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
         }
         // mask: hidden keys to -inf
         bool part = seen != 0xffffu;  // some key hidden from every row
-        if (mixed) part = part || __any_sync(0xffffffffu, (r_a < cnt && (key0 < lo_a || key0 + kKeys > hi_a)) ||
-                                                              (r_b < cnt && (key0 < lo_b || key0 + kKeys > hi_b)));
+        uint32_t vis_a = seen, vis_b = seen;
+        if constexpr (X) {
+          if (!(key0 + kKeys <= c_all || (key0 >= lo_all && key0 + kKeys <= hi_all))) {
+            part = true;
+            uint32_t vis = sight_bits(mine, key0);
+            const int d0 = key0 - (s.len - s.n);
+            if (a.mask == kMaskTree && d0 + kKeys > 0) {
+              if (d0 + kKeys > drafts_from + 64) {
+                drafts_from = max(d0, 0);
+                drafts = ancestors(a, s, (row0 + min(lane, cnt - 1)) / a.group, drafts_from);
+              }
+              vis |= (uint32_t)(d0 >= drafts_from ? drafts >> (d0 - drafts_from) : drafts << (drafts_from - d0));
+            }
+            if (lane >= cnt) vis = 0;  // the tile has no such row; its place holds the lower parts of another's products
+            vis_a &= __shfl_sync(0xffffffffu, vis, r_a);
+            vis_b &= __shfl_sync(0xffffffffu, vis, r_b);
+          }
+        } else if (mixed) {
+          part = part || __any_sync(0xffffffffu, (r_a < cnt && (key0 < lo_a || key0 + kKeys > hi_a)) ||
+                                                     (r_b < cnt && (key0 < lo_b || key0 + kKeys > hi_b)));
+        }
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             sc[n][i] *= a.scale_log2;
             if (part) {
-              const int kk = n * 8 + (lane & 3) * 2 + (i & 1), key = key0 + kk;
-              const int f = i < 2 ? lo_a : lo_b, e = i < 2 ? hi_a : hi_b;
-              if (!((seen >> kk) & 1) || key < f || key >= e) sc[n][i] = -INFINITY;
+              const int kk = n * 8 + (lane & 3) * 2 + (i & 1);
+              bool hidden;
+              if constexpr (X) {
+                hidden = !(((i < 2 ? vis_a : vis_b) >> kk) & 1);
+              } else {
+                const int key = key0 + kk, f = i < 2 ? lo_a : lo_b, e = i < 2 ? hi_a : hi_b;
+                hidden = !((seen >> kk) & 1) || key < f || key >= e;
+              }
+              if (hidden) sc[n][i] = -INFINITY;
             }
           }
         float x_a = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
@@ -626,11 +696,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_c
   if (r == 0) put_empty<T>(a, blockIdx.x, gridDim.x);
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool X>
 cudaError_t go_split(const AttnArgs& a, int sms, cudaStream_t s) {
   using C = Cfg<DP>;
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem((const void*)kv_split_kernel<T, DP>, C::kSmem, &allowed);
+  cudaError_t e = allow_smem((const void*)kv_split_kernel<T, DP, X>, C::kSmem, &allowed);
   if (e != cudaSuccess) return e;
   const int G = sms * C::kCtas;
   // each may start as the kernel before it drains, and waits for its end
@@ -644,7 +714,7 @@ cudaError_t go_split(const AttnArgs& a, int sms, cudaStream_t s) {
   cfg.gridDim = dim3(G);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
-  e = cudaLaunchKernelEx(&cfg, kv_split_kernel<T, DP>, a);
+  e = cudaLaunchKernelEx(&cfg, kv_split_kernel<T, DP, X>, a);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(G, a.b.cu ? kRows : std::min(kRows, a.group));  // rows that a tile can have
   cfg.blockDim = dim3(32 * kJoinWarps);
@@ -654,13 +724,17 @@ cudaError_t go_split(const AttnArgs& a, int sms, cudaStream_t s) {
 
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
-template <typename T>
+template <typename T, bool X>
 cudaError_t by_dim(const AttnArgs& a, int sms, cudaStream_t s) {
   switch (padded(a.c.D)) {
-    case 64: return go_split<T, 64>(a, sms, s);
-    case 128: return go_split<T, 128>(a, sms, s);
-    default: return go_split<T, 256>(a, sms, s);
+    case 64: return go_split<T, 64, X>(a, sms, s);
+    case 128: return go_split<T, 128, X>(a, sms, s);
+    default: return go_split<T, 256, X>(a, sms, s);
   }
+}
+template <typename T>
+cudaError_t by_mask(const AttnArgs& a, int sms, cudaStream_t s) {
+  return a.mask == kMaskRanges ? by_dim<T, false>(a, sms, s) : by_dim<T, true>(a, sms, s);
 }
 
 }  // namespace
@@ -671,7 +745,7 @@ long long kv_attention_workspace(const AttnArgs& a, int sms) {
 }
 
 cudaError_t launch_kv_attention(const AttnArgs& a, int sms, cudaStream_t s) {
-  return a.c.elem == 1 ? by_dim<__nv_bfloat16>(a, sms, s) : by_dim<__half>(a, sms, s);
+  return a.c.elem == 1 ? by_mask<__nv_bfloat16>(a, sms, s) : by_mask<__half>(a, sms, s);
 }
 
 }  // namespace wan

@@ -51,7 +51,11 @@ struct Seq {
 __device__ __forceinline__ Seq sequence(const AttnArgs& a, int b, bool tell) {
   Seq s;
   const bool ok = kv_rows(a.b.cu, a.b.T, b, &s.r0, &s.n);
-  const bool okl = kv_length(a.b.lengths[b], a.b.max_pages, a.c.page_size, &s.len);
+  bool okl = kv_length(a.b.lengths[b], a.b.max_pages, a.c.page_size, &s.len);
+  if (a.mask != kMaskRanges && s.n > s.len) {  // its tokens have no places
+    okl = false;
+    s.len = 0;
+  }
   if (tell && !(ok && okl) && a.b.status) atomicCAS(a.b.status, 0, (int)kDevBadLength);
   return s;
 }
@@ -79,6 +83,45 @@ __device__ __forceinline__ void seen_range(const AttnArgs& a, int t, int len, in
     *last = min(len, a.ranges[2LL * t + 1]);
     if (*first >= *last) *first = *last = 0;
   }
+}
+// What the i-th token of a sequence sees by its place: [0, c) and [lo, hi), c <= lo, and in a tree the drafts of
+// ancestors() too.  (c = 0 where the two meet.)
+struct Sight {
+  int c, lo, hi;
+};
+__device__ __forceinline__ Sight sight(const AttnArgs& a, const Seq& s, int i) {
+  const int base = s.len - s.n;
+  if (a.mask == kMaskTree) return Sight{0, 0, base};
+  const uint32_t p = (uint32_t)(base + i);
+  const uint32_t e = a.frame == 1 ? p + 1 : (p / a.frame + 1) * a.frame;  // below 2^32: p and a frame are below 2^31
+  Sight v;
+  v.lo = e > a.span ? (int)(e - a.span) : 0;
+  v.hi = (int)min((uint32_t)s.len, e);
+  v.c = min(a.sinks, v.lo);
+  if (v.c == v.lo) v.c = v.lo = 0;
+  return v;
+}
+// The drafts [from, from + 64) that draft i of a sequence sees: bit j - from for its ancestor j, and itself.  A parent that
+// is none of the drafts before its child ends the walk, and is told.
+__device__ __forceinline__ uint64_t ancestors(const AttnArgs& a, const Seq& s, int i, int from) {
+  uint64_t bits = 0;
+  const int* up = a.parents + s.r0;
+  while (i >= from) {
+    if (i - from < 64) bits |= 1ull << (i - from);
+    const int p = __ldg(up + i);
+    if (p >= i || p < -1) {
+      if (a.b.status) atomicCAS(a.b.status, 0, (int)kDevBadParent);
+      break;
+    }
+    i = p;
+  }
+  return bits;
+}
+// The lowest n of 32 bits.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
+// Bit j: key k0 + j is in the row's two ranges.
+__device__ __forceinline__ uint32_t sight_bits(const Sight& v, int k0) {
+  return low_bits(v.c - k0) | (low_bits(v.hi - k0) & ~low_bits(v.lo - k0));
 }
 // Zeros for the rows of sequences without a key, and NaN for all others if `fault`:
 // block `me` of `G` takes every G-th sequence.

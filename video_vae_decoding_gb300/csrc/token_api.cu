@@ -87,6 +87,15 @@ wan_status check_batch(const wan_kv_batch* b, int page_size, KvBatch* o) {
   return WAN_OK;
 }
 
+// One row of the cache per (page, head, row).
+wan_status check_written(const KvCache& c) {
+  const int64_t need[6] = {c.pages, c.heads, c.page_size, c.pages, c.heads, c.page_size};
+  const int64_t have[6] = {c.k_page, c.k_head, c.k_row, c.v_page, c.v_head, c.v_row};
+  for (int i = 0; i < 6; ++i)
+    if (need[i] > 1 && have[i] == 0) return fail(WAN_ERR_INVALID_ARG, "a cache that is written to must not be broadcast");
+  return WAN_OK;
+}
+
 wan_status sm_count(int* n) {
   int dev;
   CUDA_TRY(cudaGetDevice(&dev));
@@ -103,7 +112,7 @@ constexpr int kChunkRows = 64;
 constexpr double kChunkWork = 6e5;
 
 bool chunk_rows(const AttnArgs& a, ChunkGeo* g) {
-  return (int64_t)a.b.T * a.group >= (int64_t)kChunkRows * a.b.B &&
+  return a.mask == kMaskRanges && (int64_t)a.b.T * a.group >= (int64_t)kChunkRows * a.b.B &&
          (double)a.b.T * a.q_heads * a.b.max_pages * a.c.page_size >= kChunkWork && kv_chunk_geometry(a, g);
 }
 int64_t workspace_of(const AttnArgs& a, bool chunk, int sms) {
@@ -250,6 +259,8 @@ wan_status wan_kv_status(int32_t* status, wan_cuda_stream stream) {
     if (code == 0) return WAN_OK;
     CUDA_TRY(cudaMemsetAsync(status, 0, sizeof(int), (cudaStream_t)stream));
     if (code == kDevBadPage) return fail(WAN_ERR_INTERNAL, "a page table named a page outside the cache (code %d)", code);
+    if (code == kDevBadParent)
+      return fail(WAN_ERR_INTERNAL, "a drafted token's parent is none of the drafts before it (code %d)", code);
     if (code == kDevBadLength)
       return fail(WAN_ERR_INTERNAL, "a sequence's length or token range does not fit its batch (code %d)", code);
     return fail(WAN_ERR_INTERNAL, "a token kernel reported error %d (a bounded wait expired)", code);
@@ -317,6 +328,44 @@ static wan_status attention_args(const wan_kv_cache* cache, const wan_kv_batch* 
   a->q_heads = q_heads;
   a->group = q_heads / a->c.heads;
   a->stall_at1 = 0;
+  a->mask = kMaskRanges;
+  a->ranges = a->parents = nullptr;
+  a->frame = a->span = 1;
+  a->sinks = 0;
+  return WAN_OK;
+}
+
+// An attention call whose sizes and mask are in `a`; its tensors and launch.
+static wan_status attend(AttnArgs& a, const void* q, int64_t q_token, int64_t q_head, double scale, void* out,
+                         int64_t out_token, int64_t out_head, float* lse, void* workspace, int64_t workspace_bytes,
+                         wan_cuda_stream stream) {
+  a.scale_log2 = (float)(scale * 1.4426950408889634);  // log2(e)
+  if (!std::isfinite(a.scale_log2)) return fail(WAN_ERR_INVALID_ARG, "the scale is not finite, or too large");
+  const int T = a.b.T;
+  if (q_token < 0 || q_head < 0) return fail(WAN_ERR_INVALID_ARG, "negative stride");
+  if ((T > 1 && out_token <= 0) || (a.q_heads > 1 && out_head <= 0))
+    return fail(WAN_ERR_INVALID_ARG, "out must not be broadcast");
+  if (T == 0) return WAN_OK;
+  if (!q || !out) return fail(WAN_ERR_INVALID_ARG, "null q or out");
+  if (a.mask == kMaskTree && !a.parents) return fail(WAN_ERR_INVALID_ARG, "null parents");
+  if (((uintptr_t)q | (uintptr_t)out) & 1 || ((uintptr_t)lse | (uintptr_t)a.ranges | (uintptr_t)a.parents) & 3)
+    return fail(WAN_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+  int sms = 0;
+  WAN_TRY(sm_count(&sms));
+  ChunkLaunch L;
+  bool chunk = chunk_rows(a, &L.geo);
+  const int64_t bytes = workspace_of(a, chunk, sms);
+  if (!workspace || ((uintptr_t)workspace & 15) || workspace_bytes < bytes)
+    return fail(WAN_ERR_INVALID_ARG, "workspace of %lld bytes, 16-byte aligned, needed (%lld given)", (long long)bytes,
+                (long long)workspace_bytes);
+  a.q = q, a.out = out, a.lse = lse;
+  a.q_t = q_token, a.q_h = q_head, a.o_t = out_token, a.o_h = out_head;
+  a.workspace = workspace;
+  if (chunk) {
+    chunk = chunk_maps(a, &L);  // without them the split kernel runs (there is room for either)
+    L.a = a;
+  }
+  CUDA_TRY(chunk ? launch_kv_chunk(L, sms, (cudaStream_t)stream) : launch_kv_attention(a, sms, (cudaStream_t)stream));
   return WAN_OK;
 }
 
@@ -327,32 +376,97 @@ wan_status wan_kv_attention(const wan_kv_cache* cache, const wan_kv_batch* batch
   API_GUARD({
     AttnArgs a;
     WAN_TRY(attention_args(cache, batch, q_heads, &a));
-    a.scale_log2 = (float)(scale * 1.4426950408889634);  // log2(e)
-    if (!std::isfinite(a.scale_log2)) return fail(WAN_ERR_INVALID_ARG, "the scale is not finite, or too large");
-    const int T = a.b.T;
-    if (q_token < 0 || q_head < 0) return fail(WAN_ERR_INVALID_ARG, "negative stride");
-    if ((T > 1 && out_token <= 0) || (q_heads > 1 && out_head <= 0))
-      return fail(WAN_ERR_INVALID_ARG, "out must not be broadcast");
-    if (T == 0) return WAN_OK;
-    if (!q || !out) return fail(WAN_ERR_INVALID_ARG, "null q or out");
-    if (((uintptr_t)q | (uintptr_t)out) & 1 || ((uintptr_t)lse | (uintptr_t)ranges) & 3)
+    a.ranges = ranges;
+    return attend(a, q, q_token, q_head, scale, out, out_token, out_head, lse, workspace, workspace_bytes, stream);
+  })
+}
+
+wan_status wan_kv_window_attention(const wan_kv_cache* cache, const wan_kv_batch* batch, const void* q, int32_t q_heads,
+                                   int64_t q_token, int64_t q_head, int32_t window, int32_t sinks, int32_t frame,
+                                   float scale, void* out, int64_t out_token, int64_t out_head, float* lse,
+                                   void* workspace, int64_t workspace_bytes, wan_cuda_stream stream) {
+  API_GUARD({
+    AttnArgs a;
+    WAN_TRY(attention_args(cache, batch, q_heads, &a));
+    if (window < 1 || frame < 1 || sinks < 0)
+      return fail(WAN_ERR_INVALID_ARG, "a window of %d frames of %d keys, and %d first keys", window, frame, sinks);
+    a.mask = kMaskWindow;
+    a.frame = (uint32_t)frame;
+    a.span = (uint32_t)std::min<int64_t>((int64_t)window * frame, 0x7fffffff);  // (more than any sequence holds)
+    a.sinks = sinks;
+    return attend(a, q, q_token, q_head, scale, out, out_token, out_head, lse, workspace, workspace_bytes, stream);
+  })
+}
+
+wan_status wan_kv_tree_attention(const wan_kv_cache* cache, const wan_kv_batch* batch, const void* q, int32_t q_heads,
+                                 int64_t q_token, int64_t q_head, const int32_t* parents, float scale, void* out,
+                                 int64_t out_token, int64_t out_head, float* lse, void* workspace,
+                                 int64_t workspace_bytes, wan_cuda_stream stream) {
+  API_GUARD({
+    AttnArgs a;
+    WAN_TRY(attention_args(cache, batch, q_heads, &a));
+    a.mask = kMaskTree;
+    a.parents = parents;
+    return attend(a, q, q_token, q_head, scale, out, out_token, out_head, lse, workspace, workspace_bytes, stream);
+  })
+}
+
+wan_status wan_kv_fork(const wan_kv_cache* cache, int32_t* pages, int64_t page_stride, int32_t max_pages,
+                       int32_t sequences, int32_t* lengths, const int32_t* sources, const int32_t* targets,
+                       const int32_t* fresh, int64_t fresh_stride, int32_t fresh_pages, int32_t forks, int32_t share,
+                       int32_t* status, wan_cuda_stream stream) {
+  API_GUARD({
+    ForkArgs a;
+    WAN_TRY(check_cache(cache, &a.c));
+    WAN_TRY(check_written(a.c));
+    const wan_kv_batch batch{pages, page_stride, max_pages, sequences, lengths, lengths, 0, status};
+    KvBatch b;
+    WAN_TRY(check_batch(&batch, a.c.page_size, &b));
+    if (sequences > 1 && page_stride < max_pages)
+      return fail(WAN_ERR_INVALID_ARG, "a page table that is written to must not be broadcast");
+    if (forks < 0 || fresh_pages < 0) return fail(WAN_ERR_INVALID_ARG, "%d forks with %d pages each", forks, fresh_pages);
+    if (forks > kMaxForks) return fail(WAN_ERR_UNSUPPORTED, "%d forks (at most %d a call)", forks, kMaxForks);
+    if (fresh_stride < 0 || (fresh_stride < fresh_pages && forks > 1))
+      return fail(WAN_ERR_INVALID_ARG, "fresh_stride %lld for rows of %d", (long long)fresh_stride, fresh_pages);
+    if (share != 0 && share != 1) return fail(WAN_ERR_INVALID_ARG, "share must be 0 or 1");
+    if (forks == 0) return WAN_OK;
+    if (!sources || !targets || (!fresh && fresh_pages > 0)) return fail(WAN_ERR_INVALID_ARG, "null argument");
+    if (((uintptr_t)pages | (uintptr_t)lengths | (uintptr_t)sources | (uintptr_t)targets | (uintptr_t)fresh |
+         (uintptr_t)status) & 3)
       return fail(WAN_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+    a.pages = pages, a.lengths = lengths;
+    a.page_stride = page_stride, a.max_pages = max_pages, a.B = sequences;
+    a.sources = sources, a.targets = targets, a.fresh = fresh;
+    a.fresh_stride = fresh_stride, a.fresh_pages = fresh_pages, a.N = forks;
+    a.share = share;
+    a.status = status;
     int sms = 0;
     WAN_TRY(sm_count(&sms));
-    ChunkLaunch L;
-    bool chunk = chunk_rows(a, &L.geo);
-    const int64_t bytes = workspace_of(a, chunk, sms);
-    if (!workspace || ((uintptr_t)workspace & 15) || workspace_bytes < bytes)
-      return fail(WAN_ERR_INVALID_ARG, "workspace of %lld bytes, 16-byte aligned, needed (%lld given)", (long long)bytes,
-                  (long long)workspace_bytes);
-    a.q = q, a.out = out, a.lse = lse, a.ranges = ranges;
-    a.q_t = q_token, a.q_h = q_head, a.o_t = out_token, a.o_h = out_head;
-    a.workspace = workspace;
-    if (chunk) {
-      chunk = chunk_maps(a, &L);  // without them the split kernel runs (there is room for either)
-      L.a = a;
-    }
-    CUDA_TRY(chunk ? launch_kv_chunk(L, sms, (cudaStream_t)stream) : launch_kv_attention(a, sms, (cudaStream_t)stream));
+    CUDA_TRY(launch_kv_fork(a, sms, (cudaStream_t)stream));
+    return WAN_OK;
+  })
+}
+
+wan_status wan_kv_compact(const wan_kv_cache* cache, const wan_kv_batch* batch, const int32_t* keep, int32_t* lengths,
+                          wan_cuda_stream stream) {
+  API_GUARD({
+    CompactArgs a;
+    WAN_TRY(check_cache(cache, &a.c));
+    WAN_TRY(check_written(a.c));
+    WAN_TRY(check_batch(batch, a.c.page_size, &a.b));
+    if (!a.b.cu || !lengths || (!keep && a.b.T > 0)) return fail(WAN_ERR_INVALID_ARG, "null ranges, keys or lengths");
+    if (((uintptr_t)a.b.pages | (uintptr_t)a.b.lengths | (uintptr_t)a.b.cu | (uintptr_t)keep | (uintptr_t)lengths |
+         (uintptr_t)a.b.status) & 3)
+      return fail(WAN_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+    const auto apart = [&](const int32_t* x, int64_t n) { return !x || lengths + a.b.B <= x || x + n <= lengths; };
+    if (!apart(a.b.lengths, a.b.B) || !apart(a.b.cu, a.b.B + 1LL) || !apart(keep, a.b.T))
+      return fail(WAN_ERR_INVALID_ARG, "lengths must not share memory with what the call reads");
+    if (a.c.heads > 1000) return fail(WAN_ERR_UNSUPPORTED, "%d heads (at most 1000)", a.c.heads);
+    a.keep = keep;
+    a.lengths = lengths;
+    int sms = 0;
+    WAN_TRY(sm_count(&sms));
+    CUDA_TRY(launch_kv_compact(a, sms, (cudaStream_t)stream));
     return WAN_OK;
   })
 }
@@ -362,6 +476,20 @@ int64_t wan_kv_attention_workspace(const wan_kv_cache* cache, const wan_kv_batch
     AttnArgs a;
     int sms = 0;
     if (attention_args(cache, batch, q_heads, &a) != WAN_OK || sm_count(&sms) != WAN_OK) return -1;
+    ChunkGeo g;
+    return workspace_of(a, chunk_rows(a, &g), sms);
+  } catch (...) {
+    fail(WAN_ERR_INTERNAL, "unexpected C++ exception");
+    return -1;
+  }
+}
+
+int64_t wan_kv_masked_attention_workspace(const wan_kv_cache* cache, const wan_kv_batch* batch, int32_t q_heads) {
+  try {
+    AttnArgs a;
+    int sms = 0;
+    if (attention_args(cache, batch, q_heads, &a) != WAN_OK || sm_count(&sms) != WAN_OK) return -1;
+    a.mask = kMaskTree;
     ChunkGeo g;
     return workspace_of(a, chunk_rows(a, &g), sms);
   } catch (...) {

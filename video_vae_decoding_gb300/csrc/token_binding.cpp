@@ -25,6 +25,11 @@ decltype(&wan_rotary) f_rotary;
 decltype(&wan_kv_append) f_append;
 decltype(&wan_kv_attention) f_attention;
 decltype(&wan_kv_attention_workspace) f_workspace;
+decltype(&wan_kv_window_attention) f_window;
+decltype(&wan_kv_tree_attention) f_tree;
+decltype(&wan_kv_masked_attention_workspace) f_masked_workspace;
+decltype(&wan_kv_fork) f_fork;
+decltype(&wan_kv_compact) f_compact;
 
 // A plain tensor (no subclass) that needs no gradient and carries no tangent; null for anything else.
 const at::Tensor* tensor(PyObject* o) {
@@ -204,54 +209,159 @@ PyObject* append(PyObject* const* a) {
   return give(a[11], std::move(out));
 }
 
-// attention(q, k_cache, v_cache, pages, lengths, cu, ranges, scale or None, out, return_lse, status): out, or (out, lse)
-PyObject* attention(PyObject* const* a) {
-  const at::Tensor *q = tensor(a[0]), *kc = tensor(a[1]), *vc = tensor(a[2]);
+// The arguments that the attention operators share: q, the caches and tables are a[0..5] (cu last), scale or None, out,
+// return_lse and status a[m..m + 3].
+struct Attention {
+  const at::Tensor* q;
   wan_kv_cache c;
   wan_kv_batch b;
-  if (!q || !kc || !vc || !cache_of(*kc, *vc, &c)) return nullptr;
-  const at::Device dev = kc->device();
-  if (q->scalar_type() != kc->scalar_type() || q->device() != dev || q->dim() != 3 || q->size(2) != c.head_dim ||
-      !fits(q->size(1)) || !rows(*q))
-    return nullptr;
-  const int64_t T = q->size(0), H = q->size(1);
-  if (T == 0 || !batch_of(dev, a[3], a[4], a[5], a[10], T, &b)) return nullptr;
-  const int32_t* ranges = nullptr;
-  if (a[6] != Py_None) {
-    const at::Tensor* r = tensor(a[6]);
-    if (!r || !ints(*r, dev, 2) || r->size(0) != T || r->size(1) != 2 || !r->is_contiguous()) return nullptr;
-    ranges = (const int32_t*)r->data_ptr();
-  }
-  const double scale = a[7] == Py_None ? 1.0 / sqrt((double)c.head_dim) : PyFloat_AsDouble(a[7]);
-  const int with_lse = PyObject_IsTrue(a[9]);
+  int64_t T, H;
+  float scale;
+  at::Tensor out, lse, ws;
+  int64_t bytes;
   wan_cuda_stream s;
-  if (PyErr_Occurred() || !stream_of(dev, &s)) return nullptr;
-  const int64_t bytes = f_workspace(&c, &b, (int32_t)H);
-  at::Tensor out, lse;
-  if (bytes < 0 || !result(a[8], *q, &out)) return nullptr;
-  // freed at the end of this call, so the caching allocator gives it to later work of this stream only
-  const at::Tensor ws = at::empty({bytes}, at::TensorOptions().dtype(at::kByte).device(dev));
-  if (with_lse) lse = at::empty({T, H}, at::TensorOptions().dtype(at::kFloat).device(dev));
-  if (f_attention(&c, &b, q->data_ptr(), (int32_t)H, q->stride(0), q->stride(1), ranges, (float)scale, out.data_ptr(),
-                  out.stride(0), out.stride(1), with_lse ? (float*)lse.data_ptr() : nullptr, ws.data_ptr(), bytes,
-                  s) != WAN_OK)
-    return nullptr;
-  PyObject* r = give(a[8], std::move(out));
-  if (!with_lse || !r) return r;
-  PyObject* l = THPVariable_Wrap(std::move(lse));
+  float* lse_ptr() const { return lse.defined() ? (float*)lse.data_ptr() : nullptr; }
+};
+bool attention_args(PyObject* const* a, int m, decltype(f_workspace) workspace, Attention* x) {
+  const at::Tensor *q = tensor(a[0]), *kc = tensor(a[1]), *vc = tensor(a[2]);
+  if (!q || !kc || !vc || !cache_of(*kc, *vc, &x->c)) return false;
+  const at::Device dev = kc->device();
+  if (q->scalar_type() != kc->scalar_type() || q->device() != dev || q->dim() != 3 || q->size(2) != x->c.head_dim ||
+      !fits(q->size(1)) || !rows(*q))
+    return false;
+  x->q = q, x->T = q->size(0), x->H = q->size(1);
+  if (x->T == 0 || !batch_of(dev, a[3], a[4], a[5], a[m + 3], x->T, &x->b)) return false;
+  x->scale = (float)(a[m] == Py_None ? 1.0 / sqrt((double)x->c.head_dim) : PyFloat_AsDouble(a[m]));
+  const int with_lse = PyObject_IsTrue(a[m + 2]);
+  if (PyErr_Occurred() || !stream_of(dev, &x->s)) return false;
+  x->bytes = workspace(&x->c, &x->b, (int32_t)x->H);
+  if (x->bytes < 0 || !result(a[m + 1], *q, &x->out)) return false;
+  // freed at the end of the call, so the caching allocator gives it to later work of this stream only
+  x->ws = at::empty({x->bytes}, at::TensorOptions().dtype(at::kByte).device(dev));
+  if (with_lse) x->lse = at::empty({x->T, x->H}, at::TensorOptions().dtype(at::kFloat).device(dev));
+  return true;
+}
+PyObject* give_both(PyObject* out, Attention& x) {
+  PyObject* r = give(out, std::move(x.out));
+  if (!x.lse.defined() || !r) return r;
+  PyObject* l = THPVariable_Wrap(std::move(x.lse));
   PyObject* both = l ? PyTuple_Pack(2, r, l) : nullptr;
   Py_DECREF(r);
   Py_XDECREF(l);
   return both;
 }
+// A contiguous int32 tensor of n values of the device.
+const int32_t* values(PyObject* o, at::Device dev, int64_t n) {
+  const at::Tensor* t = tensor(o);
+  return t && ints(*t, dev, 1) && t->size(0) == n && t->is_contiguous() ? (const int32_t*)t->data_ptr() : nullptr;
+}
 
-// init(addresses of the library's four functions)
+// attention(q, k_cache, v_cache, pages, lengths, cu, ranges, scale or None, out, return_lse, status): out, or (out, lse)
+PyObject* attention(PyObject* const* a) {
+  Attention x;
+  if (!attention_args(a, 7, f_workspace, &x)) return nullptr;
+  const int32_t* ranges = nullptr;
+  if (a[6] != Py_None) {
+    const at::Tensor* r = tensor(a[6]);
+    if (!r || !ints(*r, x.q->device(), 2) || r->size(0) != x.T || r->size(1) != 2 || !r->is_contiguous()) return nullptr;
+    ranges = (const int32_t*)r->data_ptr();
+  }
+  if (f_attention(&x.c, &x.b, x.q->data_ptr(), (int32_t)x.H, x.q->stride(0), x.q->stride(1), ranges, x.scale,
+                  x.out.data_ptr(), x.out.stride(0), x.out.stride(1), x.lse_ptr(), x.ws.data_ptr(), x.bytes, x.s) != WAN_OK)
+    return nullptr;
+  return give_both(a[8], x);
+}
+
+// window(q, k_cache, v_cache, pages, lengths, cu, window, sinks, frame, scale or None, out, return_lse, status)
+PyObject* window(PyObject* const* a) {
+  long n[3];
+  for (int i = 0; i < 3; ++i) {
+    if (!PyLong_CheckExact(a[6 + i])) return nullptr;
+    n[i] = PyLong_AsLong(a[6 + i]);
+    if (PyErr_Occurred() || n[i] < 0 || !fits(n[i])) return nullptr;
+  }
+  Attention x;
+  if (!attention_args(a, 9, f_masked_workspace, &x) ||
+      f_window(&x.c, &x.b, x.q->data_ptr(), (int32_t)x.H, x.q->stride(0), x.q->stride(1), (int32_t)n[0], (int32_t)n[1],
+               (int32_t)n[2], x.scale, x.out.data_ptr(), x.out.stride(0), x.out.stride(1), x.lse_ptr(), x.ws.data_ptr(),
+               x.bytes, x.s) != WAN_OK)
+    return nullptr;
+  return give_both(a[10], x);
+}
+
+// tree(q, k_cache, v_cache, pages, lengths, cu, parents, scale or None, out, return_lse, status)
+PyObject* tree(PyObject* const* a) {
+  Attention x;
+  if (!attention_args(a, 7, f_masked_workspace, &x)) return nullptr;
+  const int32_t* parents = values(a[6], x.q->device(), x.T);
+  if (!parents || f_tree(&x.c, &x.b, x.q->data_ptr(), (int32_t)x.H, x.q->stride(0), x.q->stride(1), parents, x.scale,
+                         x.out.data_ptr(), x.out.stride(0), x.out.stride(1), x.lse_ptr(), x.ws.data_ptr(), x.bytes,
+                         x.s) != WAN_OK)
+    return nullptr;
+  return give_both(a[8], x);
+}
+
+// fork(k_cache, v_cache, pages, lengths, sources, targets, fresh, share, status): True
+PyObject* fork(PyObject* const* a) {
+  const at::Tensor *kc = tensor(a[0]), *vc = tensor(a[1]), *fr = tensor(a[6]), *so = tensor(a[4]);
+  wan_kv_cache c;
+  wan_kv_batch b;
+  if (!kc || !vc || !fr || !so || !cache_of(*kc, *vc, &c)) return nullptr;
+  const at::Device dev = kc->device();
+  if (!batch_of(dev, a[2], a[3], Py_None, a[8], 0, &b) || so->dim() != 1) return nullptr;
+  const int64_t N = so->size(0);
+  const int32_t *sources = values(a[4], dev, N), *targets = values(a[5], dev, N);
+  const int share = PyObject_IsTrue(a[7]);
+  wan_cuda_stream s;
+  if (!sources || !targets || !ints(*fr, dev, 2) || fr->size(0) != N || (fr->size(1) > 1 && fr->stride(1) != 1) || !fits(N) ||
+      !fits(fr->size(1)) || PyErr_Occurred() || !stream_of(dev, &s))
+    return nullptr;
+  if (f_fork(&c, (int32_t*)b.pages, b.page_stride, b.max_pages, b.batch, (int32_t*)b.lengths, sources, targets,
+             (const int32_t*)fr->data_ptr(), fr->stride(0), (int32_t)fr->size(1), (int32_t)N, share, b.status, s) != WAN_OK)
+    return nullptr;
+  written(*kc);
+  written(*vc);
+  written(*tensor(a[2]));
+  written(*tensor(a[3]));
+  Py_RETURN_TRUE;
+}
+
+// compact(k_cache, v_cache, pages, first, keep, cu, lengths or None, status): the lengths
+PyObject* compact(PyObject* const* a) {
+  const at::Tensor *kc = tensor(a[0]), *vc = tensor(a[1]), *first = tensor(a[3]), *keep = tensor(a[4]);
+  wan_kv_cache c;
+  wan_kv_batch b;
+  if (!kc || !vc || !first || !keep || !cache_of(*kc, *vc, &c)) return nullptr;
+  const at::Device dev = kc->device();
+  wan_cuda_stream s;
+  if (!ints(*keep, dev, 1) || !keep->is_contiguous() || keep->size(0) == 0 || a[5] == Py_None ||
+      !batch_of(dev, a[2], a[3], a[5], a[7], keep->size(0), &b) || !stream_of(dev, &s))
+    return nullptr;
+  at::Tensor lengths;
+  if (a[6] == Py_None) {
+    lengths = at::empty({b.batch}, first->options());
+  } else {
+    if (!values(a[6], dev, b.batch)) return nullptr;
+    lengths = *tensor(a[6]);
+  }
+  if (f_compact(&c, &b, (const int32_t*)keep->data_ptr(), (int32_t*)lengths.data_ptr(), s) != WAN_OK) return nullptr;
+  written(*kc);
+  written(*vc);
+  return give(a[6], std::move(lengths));
+}
+
+// init(addresses of the library's functions)
 PyObject* init(PyObject*, PyObject* args) {
-  unsigned long long f[4];
-  if (!PyArg_ParseTuple(args, "KKKK", &f[0], &f[1], &f[2], &f[3])) return nullptr;
+  unsigned long long f[9];
+  if (!PyArg_ParseTuple(args, "KKKKKKKKK", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8])) return nullptr;
   f_append = (decltype(f_append))(uintptr_t)f[1];
   f_attention = (decltype(f_attention))(uintptr_t)f[2];
   f_workspace = (decltype(f_workspace))(uintptr_t)f[3];
+  f_window = (decltype(f_window))(uintptr_t)f[4];
+  f_tree = (decltype(f_tree))(uintptr_t)f[5];
+  f_masked_workspace = (decltype(f_masked_workspace))(uintptr_t)f[6];
+  f_fork = (decltype(f_fork))(uintptr_t)f[7];
+  f_compact = (decltype(f_compact))(uintptr_t)f[8];
   f_rotary = (decltype(f_rotary))(uintptr_t)f[0];
   Py_RETURN_NONE;
 }
@@ -261,6 +371,10 @@ PyMethodDef methods[] = {
     {"rotary", (PyCFunction)(void (*)(void))entry<rotary, 6>, METH_FASTCALL, nullptr},
     {"append", (PyCFunction)(void (*)(void))entry<append, 13>, METH_FASTCALL, nullptr},
     {"attention", (PyCFunction)(void (*)(void))entry<attention, 11>, METH_FASTCALL, nullptr},
+    {"window", (PyCFunction)(void (*)(void))entry<window, 13>, METH_FASTCALL, nullptr},
+    {"tree", (PyCFunction)(void (*)(void))entry<tree, 11>, METH_FASTCALL, nullptr},
+    {"fork", (PyCFunction)(void (*)(void))entry<fork, 9>, METH_FASTCALL, nullptr},
+    {"compact", (PyCFunction)(void (*)(void))entry<compact, 8>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tokens", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -19,6 +19,7 @@ constexpr int kMaxRotaryAxes = 4;
 enum TokenError : int {
   kDevBadPage = 4,    // a page number outside the cache
   kDevBadLength = 5,  // a length, token range or position outside what the batch describes
+  kDevBadParent = 6,  // a drafted token's parent is none of the drafts before it
 };
 
 // Pair j turns by position[axis[j]] * turn[j], in units of 2^-64 of a full
@@ -83,6 +84,14 @@ struct AppendArgs {
 };
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t s);
 
+// What a row sees.  Beside a range of its own (or every key), its place in the
+// sequence can tell: new tokens are then the sequence's last keys.
+enum AttnMask : int {
+  kMaskRanges = 0,
+  kMaskWindow = 1,  // the first `sinks` keys and a window of frames
+  kMaskTree = 2,    // what comes before the new tokens, its ancestors among them and itself
+};
+
 struct AttnArgs {
   KvCache c;
   KvBatch b;
@@ -95,10 +104,40 @@ struct AttnArgs {
   float scale_log2;  // scale * log2(e)
   void* workspace;
   int stall_at1;  // failure self test: 1-based block of keys that is never loaded (0: none)
+  int mask;       // AttnMask
+  // window: the token at place p sees [0, sinks) and the keys of [e - span, e), e the end of its frame
+  uint32_t frame, span;  // span: whole frames
+  int sinks;
+  const int* parents;    // tree: [T] place of each draft's parent among its sequence's, -1 for none
 };
 // Bytes of workspace of a call (a bound from host-side sizes alone).
 long long kv_attention_workspace(const AttnArgs& a, int sms);
 cudaError_t launch_kv_attention(const AttnArgs& a, int sms, cudaStream_t s);
+
+// Sequences targets[i] become copies of sources[i].
+constexpr int kMaxForks = 1024;
+struct ForkArgs {
+  KvCache c;
+  int *pages, *lengths;  // the call's tables, [B][max_pages] and [B]
+  long long page_stride;
+  int max_pages, B;
+  const int *sources, *targets;  // [N]
+  const int* fresh;              // [N][fresh_pages]: pages for what is copied
+  long long fresh_stride;
+  int fresh_pages, N;
+  int share;  // whole pages are shared, and only the last, partly filled one is copied
+  int* status;
+};
+cudaError_t launch_kv_fork(const ForkArgs& a, int sms, cudaStream_t s);
+
+// Key keep[cu[b] + j] of sequence b moves to place first + j (b.lengths: first; b.cu, b.T: ranges of keep).
+struct CompactArgs {
+  KvCache c;
+  KvBatch b;
+  const int* keep;
+  int* lengths;  // [B]: keys that are left
+};
+cudaError_t launch_kv_compact(const CompactArgs& a, int sms, cudaStream_t s);
 
 // Raises a kernel's dynamic shared memory limit once per device: `done` holds a
 // bit per device that has it (a call costs 0.5 us on the launch path).

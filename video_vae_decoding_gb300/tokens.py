@@ -8,6 +8,11 @@ turns into frames (wan_rotary, wan_kv_append, wan_kv_attention of
     q = kv_append(k, v, k_cache, v_cache, pages, lengths, cu_tokens=cu, positions=pos, sections=(22, 21, 21), q=q)
     out = kv_attention(q, k_cache, v_cache, pages, lengths, cu_tokens=cu)
 
+A stream that runs on attends by kv_window_attention, to its first keys and a
+window of the last ones; drafts of several continuations are attended as a tree
+(kv_tree_attention), and kv_compact keeps the accepted ones, or any keys;
+kv_fork makes sequences copies of others.
+
 Work goes to the current stream of the tensors' device, or to ``stream``
 (which has to wait for what makes the tensors; they may be dropped after the
 call); results and workspaces made here are allocated on that stream.  No call
@@ -21,6 +26,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import operator
 import struct
 import warnings
 
@@ -29,7 +35,8 @@ from torch.autograd import forward_ad
 
 from ._lib import WAN_BF16, WAN_F16, WAN_F32, WanRotation, check, load
 
-__all__ = ["Rotation", "rotary", "rotary_grad", "kv_append", "kv_attention", "kv_check", "kv_status"]
+__all__ = ["Rotation", "rotary", "rotary_grad", "kv_append", "kv_attention", "kv_window_attention",
+           "kv_tree_attention", "kv_fork", "kv_compact", "kv_check", "kv_status"]
 
 _CODES = {torch.float32: WAN_F32, torch.bfloat16: WAN_BF16, torch.float16: WAN_F16}
 _HALVES = (torch.bfloat16, torch.float16)
@@ -163,7 +170,7 @@ class _Absent:
     def _none(*args):
         return None
 
-    rotary = append = attention = _none
+    rotary = append = attention = window = tree = fork = compact = _none
 
 
 def _short_way():
@@ -179,7 +186,9 @@ def _short_way():
         from . import _tokens
 
         _tokens.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-            lib.wan_rotary, lib.wan_kv_append, lib.wan_kv_attention, lib.wan_kv_attention_workspace)))
+            lib.wan_rotary, lib.wan_kv_append, lib.wan_kv_attention, lib.wan_kv_attention_workspace,
+            lib.wan_kv_window_attention, lib.wan_kv_tree_attention, lib.wan_kv_masked_attention_workspace, lib.wan_kv_fork,
+            lib.wan_kv_compact)))
         _short = _tokens
     except ImportError as e:
         warnings.warn(f"the token operators are marshalled in Python, which takes three times the host's time: _tokens.so "
@@ -413,11 +422,12 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
 
 
 @functools.lru_cache(maxsize=1024)
-def _workspace(dtype, heads, size, D, columns, B, T, q_heads, device_index) -> int:
-    """Bytes of workspace of a call of these sizes (wan_kv_attention_workspace), whatever the addresses."""
+def _workspace(dtype, heads, size, D, columns, B, T, q_heads, device_index, masked=False) -> int:
+    """Bytes of workspace of a call of these sizes (wan_kv_attention_workspace, or masked's), whatever the addresses."""
     step = 8 * -(-D // 8)
     c = _pack_cache(16, 16, dtype, heads, size, D, 1, step, step, step, step, step, step)
-    n = load().wan_kv_attention_workspace(c, _pack_batch(16, columns, columns, B, 16, 16, T, 0), q_heads)
+    of = load().wan_kv_masked_attention_workspace if masked else load().wan_kv_attention_workspace
+    n = of(c, _pack_batch(16, columns, columns, B, 16, 16, T, 0), q_heads)
     if n < 0:
         msg = load().wan_vae_last_error()
         raise ValueError(msg.decode())
@@ -450,6 +460,13 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
         got = short.attention(q, k_cache, v_cache, pages, lengths, cu_tokens, ranges, scale, out, return_lse, status)
         if got is not None:
             return got
+    return _attend("wan_kv_attention", _ranges, ranges, q, k_cache, v_cache, pages, lengths, cu_tokens, scale, out, return_lse,
+                   status, stream)
+
+
+def _attend(name, mask_of, mask, q, k_cache, v_cache, pages, lengths, cu_tokens, scale, out, return_lse, status, stream):
+    """A call of one of the attention operators, marshalled here: `mask`, and what mask_of makes of it, is its own."""
+    of_mask = [m for m in (mask if isinstance(mask, tuple) else (mask,)) if isinstance(m, torch.Tensor)]
     _refuse_grad(q, k_cache, v_cache, out)
     dev = k_cache.device
     c, heads, size, D = _cache(k_cache, v_cache, dev)
@@ -464,15 +481,11 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     if qs[2] != 1:
         _rows_of(q, "q")
     b, B = _batch(dev, pages, lengths, cu_tokens, T, status)
-    rp = None
-    if ranges is not None:
-        _on(ranges, dev, "ranges", _INT32, 2)
-        if ranges.shape != (T, 2) or not ranges.is_contiguous():
-            raise ValueError(f"ranges must be contiguous [{T}, 2], not {tuple(ranges.shape)}")
-        rp = ranges.data_ptr()
+    args = mask_of(mask, dev, T)
     if _elsewhere(dev, stream):
-        with _Guard(dev, stream, q, k_cache, v_cache, pages, lengths, cu_tokens, ranges, out, status):
-            return kv_attention(q, k_cache, v_cache, pages, lengths, cu_tokens, ranges, scale, out, return_lse, status)
+        with _Guard(dev, stream, q, k_cache, v_cache, pages, lengths, cu_tokens, *of_mask, out, status):
+            return _attend(name, mask_of, mask, q, k_cache, v_cache, pages, lengths, cu_tokens, scale, out, return_lse, status,
+                           None)
     given = out is not None
     if not given:
         out = torch.empty(shape, dtype=dt, device=dev)
@@ -483,19 +496,161 @@ def kv_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
             raise ValueError(f"out is {tuple(out.shape)}, not {tuple(shape)}")
         _rows_of(out, "out")
         os = out.stride()
-    n = _workspace(_CODES[dt], heads, size, D, pages.shape[1], B, T, H, dev.index)
+    n = _workspace(_CODES[dt], heads, size, D, pages.shape[1], B, T, H, dev.index, name != "wan_kv_attention")
     ws = torch.empty(n, dtype=torch.uint8, device=dev)
     lse, lp = None, None
     if return_lse:
         lse = torch.empty((T, H), dtype=torch.float32, device=dev)
         lp = lse.data_ptr()
-    status = load().wan_kv_attention(c, b, q.data_ptr(), H, qs[0], qs[1], rp, D ** -0.5 if scale is None else scale,
-                                     out.data_ptr(), os[0], os[1], lp, ws.data_ptr(), n, _raw_stream(dev.index))
+    status = getattr(load(), name)(c, b, q.data_ptr(), H, qs[0], qs[1], *args, D ** -0.5 if scale is None else scale,
+                                   out.data_ptr(), os[0], os[1], lp, ws.data_ptr(), n, _raw_stream(dev.index))
     if status:
         check(status)
     if given:
         _written(out)
     return (out, lse) if return_lse else out
+
+
+def _ranges(ranges, dev, T):
+    if ranges is None:
+        return (None,)
+    _on(ranges, dev, "ranges", _INT32, 2)
+    if ranges.shape != (T, 2) or not ranges.is_contiguous():
+        raise ValueError(f"ranges must be contiguous [{T}, 2], not {tuple(ranges.shape)}")
+    return (ranges.data_ptr(),)
+
+
+def _window(mask, dev, T):
+    for n, what in zip(mask, ("frames as window", "first keys", "keys as frame")):
+        _int32(n, what)
+    return mask
+
+
+def _parents(parents, dev, T):
+    _on(parents, dev, "parents", _INT32, 1)
+    if parents.shape[0] != T or not parents.is_contiguous():
+        raise ValueError(f"parents must be {T} contiguous values, not {tuple(parents.shape)}")
+    return (parents.data_ptr(),)
+
+
+def kv_window_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor,
+                        lengths: torch.Tensor, window: int, sinks: int = 0, frame: int = 1,
+                        cu_tokens: torch.Tensor = None, scale: float = None, out: torch.Tensor = None,
+                        return_lse: bool = False, status: torch.Tensor = None, stream=None):
+    """kv_attention of tokens that are the last keys of their sequences, each
+    seeing the first `sinks` keys and a window: the token at place p, in frame f =
+    p // frame, sees the keys of frames f - window + 1 .. f (frame 1: the last
+    `window` keys up to its own; larger frames: its own frame's later keys too).
+
+    Pages that hold no key that any token sees are not read: their numbers in
+    `pages` may be anything, so the cache need not grow with the stream."""
+    short = _short or _short_way()
+    if stream is None:
+        got = short.window(q, k_cache, v_cache, pages, lengths, cu_tokens, window, sinks, frame, scale, out, return_lse, status)
+        if got is not None:
+            return got
+    mask = tuple(operator.index(n) for n in (window, sinks, frame))
+    return _attend("wan_kv_window_attention", _window, mask, q, k_cache, v_cache, pages, lengths, cu_tokens, scale, out,
+                   return_lse, status, stream)
+
+
+def kv_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor,
+                      lengths: torch.Tensor, parents: torch.Tensor, cu_tokens: torch.Tensor = None, scale: float = None,
+                      out: torch.Tensor = None, return_lse: bool = False, status: torch.Tensor = None, stream=None):
+    """kv_attention of a tree of drafted tokens, the last keys of their
+    sequences: each sees the keys ahead of the drafts, its ancestors and itself.
+
+    parents [tokens] int32: the place of a draft's parent among its sequence's
+    drafts (0: the first), which comes before it, or -1.  Others count as -1 and
+    leave a code in `status`.  Time goes with the tree's depth; a chain is better
+    a range of kv_attention."""
+    short = _short or _short_way()
+    if stream is None:
+        got = short.tree(q, k_cache, v_cache, pages, lengths, cu_tokens, parents, scale, out, return_lse, status)
+        if got is not None:
+            return got
+    return _attend("wan_kv_tree_attention", _parents, parents, q, k_cache, v_cache, pages, lengths, cu_tokens, scale, out,
+                   return_lse, status, stream)
+
+
+def kv_fork(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor, lengths: torch.Tensor,
+            sources: torch.Tensor, targets: torch.Tensor, fresh: torch.Tensor, share: bool = True,
+            status: torch.Tensor = None, stream=None) -> None:
+    """Makes sequences targets[i] copies of sequences sources[i], in place:
+    lengths, the rows of pages, and what has to be copied of the caches.
+
+    share: whole pages become common to both, and only the keys of a last, partly
+    filled page are copied, to page fresh[i, 0].  Otherwise all keys are copied,
+    to pages fresh[i, 0], fresh[i, 1], ...  sources, targets [forks] and fresh
+    [forks, n]: int32; fresh pages are the caller's to hand out.  A target must be
+    neither a source of the call nor the target of two forks: such forks, and
+    those whose numbers are none of the tables', are left out and leave a code in
+    `status`."""
+    short = _short or _short_way()
+    if stream is None and short.fork(k_cache, v_cache, pages, lengths, sources, targets, fresh, share, status) is not None:
+        return
+    _refuse_grad(k_cache, v_cache)
+    dev = k_cache.device
+    c, _, _, _ = _cache(k_cache, v_cache, dev)
+    _batch(dev, pages, lengths, None, 0, status)
+    for t, name, dim in (sources, "sources", 1), (targets, "targets", 1), (fresh, "fresh", 2):
+        _on(t, dev, name, _INT32, dim)
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name} must be contiguous")
+        if t.shape[0] != sources.shape[0]:
+            raise ValueError(f"{name} has {t.shape[0]} rows for {sources.shape[0]} forks")
+    _int32(sources.shape[0], "forks")
+    _int32(fresh.shape[1], "pages a fork")
+    if _elsewhere(dev, stream):
+        with _Guard(dev, stream, k_cache, v_cache, pages, lengths, sources, targets, fresh, status):
+            return kv_fork(k_cache, v_cache, pages, lengths, sources, targets, fresh, share, status)
+    check(load().wan_kv_fork(c, pages.data_ptr(), pages.stride(0), pages.shape[1], pages.shape[0], lengths.data_ptr(),
+                             sources.data_ptr(), targets.data_ptr(), fresh.data_ptr(), fresh.stride(0), fresh.shape[1],
+                             sources.shape[0], bool(share), 0 if status is None else status.data_ptr(),
+                             _raw_stream(dev.index)))
+    _written(k_cache, v_cache, pages, lengths)
+
+
+def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor, first: torch.Tensor,
+               keep: torch.Tensor, cu_keep: torch.Tensor, lengths: torch.Tensor = None, status: torch.Tensor = None,
+               stream=None) -> torch.Tensor:
+    """Moves the keys and values that are kept together, in place, and returns
+    the new lengths (int32, one a sequence; `lengths` if given).
+
+    The first first[b] keys of sequence b stay; the key at place keep[cu_keep[b] +
+    j] moves to place first[b] + j, all as if at once.  So the accepted drafts of a
+    tree are kept (first: the keys ahead of the drafts), a window rolls on, or a
+    choice of keys stays.  first [sequences], keep [n], cu_keep [sequences + 1]:
+    int32.  A key moves ahead or stays: others (keep < first + j, or without a
+    page) are left out and leave a code in `status`, as do sequences whose ranges
+    are none.  Pages behind the new lengths are the caller's again."""
+    short = _short or _short_way()
+    if stream is None:
+        got = short.compact(k_cache, v_cache, pages, first, keep, cu_keep, lengths, status)
+        if got is not None:
+            return got
+    _refuse_grad(k_cache, v_cache)
+    dev = k_cache.device
+    c, _, _, _ = _cache(k_cache, v_cache, dev)
+    _on(keep, dev, "keep", _INT32, 1)
+    _on(cu_keep, dev, "cu_keep", _INT32, 1)
+    _on(first, dev, "first", _INT32, 1)
+    if keep.shape[0] > 1 and keep.stride(0) != 1:
+        raise ValueError("keep must be contiguous")
+    b, B = _batch(dev, pages, first, cu_keep, keep.shape[0], status)
+    if lengths is not None:
+        _on(lengths, dev, "lengths", _INT32, 1)
+        if lengths.shape[0] != B or (B > 1 and lengths.stride(0) != 1):
+            raise ValueError(f"lengths must hold {B} contiguous values")
+    if _elsewhere(dev, stream):
+        with _Guard(dev, stream, k_cache, v_cache, pages, first, keep, cu_keep, lengths, status):
+            return kv_compact(k_cache, v_cache, pages, first, keep, cu_keep, lengths, status)
+    given = lengths is not None
+    if not given:
+        lengths = torch.empty(B, dtype=torch.int32, device=dev)
+    check(load().wan_kv_compact(c, b, keep.data_ptr() or None, lengths.data_ptr(), _raw_stream(dev.index)))
+    _written(k_cache, v_cache, *([lengths] if given else []))
+    return lengths
 
 
 def kv_check(pages: torch.Tensor, lengths: torch.Tensor, page_size: int, n_pages: int, cu_tokens: torch.Tensor = None,
