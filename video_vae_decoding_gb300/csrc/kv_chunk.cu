@@ -259,6 +259,13 @@ struct RowTile {
   int b, rt;  // b < 0: none
   int k0, k1;
 };
+// With X (rows see by their place): its rows see [0, c) and [lo, hi); k0 and k1 count the blocks of both without the
+// `skip` ones between them.
+struct SightTile : RowTile {
+  int c, lo, hi, skip;
+};
+template <bool X>
+using Tile = std::conditional_t<X, SightTile, RowTile>;
 // Room for the row tiles of T tokens in B sequences; those of a sequence that starts at row r0 stand from r0 * group /
 // tile_rows + b on, so that sequences never meet.
 __host__ __device__ inline long long row_tiles(const AttnArgs& a) {
@@ -275,18 +282,19 @@ __device__ __forceinline__ int tile_weight(const AttnArgs& a, const Seq& s, int 
 }
 
 constexpr int kFaultBytes = 16;
+template <bool X>
 struct Space {
   int* fault;  // a wait ran out: no row of the call is to be believed
-  RowTile* tiles;
+  Tile<X>* tiles;
   Open* open;
   float2* ml;  // [2 G][rows of a tile]
   float4* o;   // [2 G][DP / 4][rows of a tile]: the rows side by side
 };
-template <int DP>
-__host__ __device__ inline Space space(const AttnArgs& a, int G) {
-  Space s;
+template <int DP, bool X>
+__host__ __device__ inline Space<X> space(const AttnArgs& a, int G) {
+  Space<X> s;
   s.fault = (int*)a.workspace;
-  s.tiles = (RowTile*)((char*)a.workspace + kFaultBytes);
+  s.tiles = (Tile<X>*)((char*)a.workspace + kFaultBytes);
   s.open = (Open*)(s.tiles + row_tiles(a));
   s.ml = (float2*)(s.open + G);
   s.o = (float4*)(s.ml + (size_t)2 * G * Cfg<DP>::kRows);
@@ -295,6 +303,7 @@ __host__ __device__ inline Space space(const AttnArgs& a, int G) {
 
 // The row tiles of a call, a warp for each place.
 constexpr int kPlanWarps = 4;
+template <bool X>
 __global__ void __launch_bounds__(32 * kPlanWarps)
     kv_chunk_plan_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ ChunkGeo geo) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -302,7 +311,8 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
   const int lane = threadIdx.x & 31, tile = tile_rows(a.c.D);
   const long long place = (long long)blockIdx.x * kPlanWarps + (threadIdx.x >> 5);
   if (place >= row_tiles(a)) return;
-  RowTile t{-1, 0, 0, 0};
+  Tile<X> t{};
+  t.b = -1;
   for (int b0 = 0; b0 < a.b.B; b0 += 32) {
     Seq s{0, 0, 0};
     long long rt = 0;
@@ -319,7 +329,21 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
     s.n = __shfl_sync(0xffffffffu, s.n, from);
     s.len = __shfl_sync(0xffffffffu, s.len, from);
     t.k1 = blocks_of(geo, a.c.page_size, s.len);
-    if (a.ranges) {
+    if constexpr (X) {
+      // a window moves on with its tokens: the first one's begins, the last one's ends first keys and window of the tile
+      const int row0 = t.rt * tile;
+      const Sight from = sight(a, s, row0 / a.group), to = sight(a, s, (min(row0 + tile, s.n * a.group) - 1) / a.group);
+      t.c = to.c, t.lo = from.lo, t.hi = a.mask == kMaskTree ? s.len : to.hi;
+      if (t.lo <= t.c) t.c = t.lo = 0;
+      t.k0 = block_of_key(geo, a.c.page_size, t.lo);
+      t.k1 = block_of_key(geo, a.c.page_size, t.hi - 1) + 1;
+      if (t.c > 0) {
+        const int firsts = block_of_key(geo, a.c.page_size, t.c - 1) + 1;
+        t.skip = max(t.k0, firsts) - firsts;
+        t.k0 = 0;
+        t.k1 -= t.skip;
+      }
+    } else if (a.ranges) {
       int lo = 0x7fffffff, hi = 0;
       const int row0 = t.rt * tile, last = (min(row0 + tile, s.n * a.group) - 1) / a.group;
       for (int i = row0 / a.group + lane; i <= last; i += 32) {
@@ -334,8 +358,8 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
     }
     break;
   }
-  if (lane == 0) space<64>(a, 0).tiles[place] = t;
-  if (place == 0 && lane == 0) *space<64>(a, 0).fault = 0;
+  if (lane == 0) space<64, X>(a, 0).tiles[place] = t;
+  if (place == 0 && lane == 0) *space<64, X>(a, 0).fault = 0;
 }
 
 // A run: blocks [k0, k1) of one row tile and head.
@@ -347,6 +371,9 @@ struct alignas(16) Run {
   int blocks;                // k1 - k0; 0: the piece has no more runs
   int all_lo[2], all_hi[2];  // per half: keys that every row sees
   int odd_lo, odd_hi;        // blocks whose values were cleaned (below)
+  // With X the run's blocks are numbered as its tile's are: number o is block o, and from `firsts` on block o + skip;
+  // keys that some row sees are on pages [0, p_first) and [p_lo, p_hi), and all rows of a half see [0, all_c) too.
+  int firsts, skip, p_first, p_lo, p_hi, all_c[2];
 };
 
 // Where thread 0 stands on the line (in shared memory: the softmax has no register to spare).
@@ -393,7 +420,7 @@ __device__ __noinline__ bool clean_values(uint8_t* ring, uint64_t* full, int at,
   return true;
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool X>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                     const __grid_constant__ AttnArgs a, const __grid_constant__ ChunkGeo geo) {
@@ -415,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* done = o_done + 4;    // [2] all products issued by warp 1, and by warp 2, complete
   if (smem_u32(smem) & 1023) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (threadIdx.x == 0) *space<DP>(a, gridDim.x).fault = 1;
+    if (threadIdx.x == 0) *space<DP, X>(a, gridDim.x).fault = 1;
     if (a.b.status) atomicCAS(a.b.status, 0, (int)kDevTimeoutFull);
     return;
   }
@@ -428,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int G = gridDim.x, me = blockIdx.x;
-  const Space ws = space<DP>(a, G);
+  const Space<X> ws = space<DP, X>(a, G);
   const int page_size = a.c.page_size;
   int* const err = a.b.status;
 
@@ -465,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");  // for the plan
   auto units = [&](const RowTile& t, int w) { return (long long)(kRunUnits + w * (t.k1 - t.k0)); };
   const Piece cut = cut_line<kThreads / 32, 1>((int)row_tiles(a), kLeast, reinterpret_cast<long long*>(half_ml), [&](int i) {
-    const RowTile t = ws.tiles[i];
+    const Tile<X> t = ws.tiles[i];
     return t.b < 0 ? 0 : a.c.heads * units(t, tile_weight(a, sequence(a, t.b, false), t.rt));
   });
   tc_fence_before();
@@ -490,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int i = cursor->i;
     run->blocks = 0;
     while (line < pc.end && run->blocks == 0) {
-      RowTile t = ws.tiles[i];
+      Tile<X> t = ws.tiles[i];
       Seq s{0, 0, 0};
       long long n = 0;  // units of a head
       int w = 0;
@@ -523,6 +550,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       run->odd_lo = 0x7fffffff;
       run->odd_hi = -1;
+      if constexpr (X) {
+        run->all_c[0] = run->all_c[1] = 0x7fffffff;
+        run->firsts = t.c > 0 ? block_of_key(geo, page_size, t.c - 1) + 1 : 0;
+        run->skip = t.skip;
+        run->p_first = (t.c + page_size - 1) / page_size;
+        run->p_lo = t.lo / page_size;
+        run->p_hi = (t.hi - 1) / page_size + 1;
+      }
       if (run->k0 == t.k0 && run->k1 > t.k0 && run->k1 < t.k1)
         ws.open[me] = Open{pc.holder(line + n - u0 - 1) - me, h, run->row0, run->cnt, s, 0};
       at += u1 - u0;
@@ -553,9 +588,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (split ? 0 : half * kHalfRows) + hrow;
     const bool softmax = warp >= 4 && warp < kSoftEnd, real = softmax && row < cnt;
     int lo = 0, hi = 0x40000000;  // rows past the tile's see everything: they need no mask
+    int first_keys = 0;           // with X: [0, first_keys) too, and drafts
     if (softmax) {
       if (real) {
-        seen_range(a, s.r0 + (row0 + row) / a.group, s.len, &lo, &hi);
+        if constexpr (X) {
+          const Sight v = sight(a, s, (row0 + row) / a.group);
+          first_keys = v.c, lo = v.lo, hi = v.hi;
+          atomicMin(&run->all_c[half], first_keys);
+        } else {
+          seen_range(a, s.r0 + (row0 + row) / a.group, s.len, &lo, &hi);
+        }
         if (lo > 0) atomicMax(&run->all_lo[half], lo);
         atomicMin(&run->all_hi[half], hi);
       }
@@ -598,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // blocks [n0, n1) of a run whose first block is the it-th
     auto loads = [&](auto which, const Run* run, int it, int n0, int n1) {
       constexpr bool ofK = decltype(which)::value;
-      const int h = run->h, j0 = run->k0 + n0;
+      const int h = run->h, o0 = run->k0 + n0, j0 = X && o0 >= run->firsts ? o0 + run->skip : o0;
       const CUtensorMap* map = ofK ? &mapK : &mapV;
       const int* table = a.b.pages + run->b * a.b.page_stride;
       const int held = (run->s.len + page_size - 1) / page_size;  // pages of the sequence
@@ -611,13 +653,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       int idx = geo.parts == 1 ? j0 * geo.pages + lane : j0 / geo.parts, part = geo.parts == 1 ? 0 : j0 - idx * geo.parts;
       int idx2 = idx, part2 = part;
       const int wide = lane < geo.pages ? held : 0;
-      auto advance = [&](int& i, int& p) {
-        if (geo.parts == 1) i += geo.pages;
+      // with X: blocks to the one behind the first keys, and where that one is
+      int left = 0, left2 = 0, idx_to = 0, part_to = 0, p_first = 0, p_lo = 0, p_hi = 0;
+      if constexpr (X) {
+        p_first = run->p_first, p_lo = run->p_lo, p_hi = run->p_hi;
+        left = left2 = run->firsts - o0;
+        if (left > 0) {
+          const int to = run->firsts + run->skip;
+          idx_to = geo.parts == 1 ? to * geo.pages + lane : to / geo.parts;
+          part_to = geo.parts == 1 ? 0 : to - idx_to * geo.parts;
+        }
+      }
+      // whether some row sees a key of page i of the sequence: its number is looked at
+      auto wanted = [&](int i) { return !X || i < p_first || (i >= p_lo && i < p_hi); };
+      auto advance = [&](int& i, int& p, int& left) {
+        if (X && --left == 0) i = idx_to, p = part_to;
+        else if (geo.parts == 1) i += geo.pages;
         else if (++p == geo.parts) p = 0, ++i;
       };
       auto entry = [&](int n) {
-        const int e = n < n1 && idx2 < wide ? table[idx2] : (int)a.c.pages;  // past the cache, which reads as zeros
-        advance(idx2, part2);
+        // past the cache, which reads as zeros
+        const int e = n < n1 && idx2 < wide && wanted(idx2) ? table[idx2] : (int)a.c.pages;
+        advance(idx2, part2, left2);
         return e;
       };
       int page = entry(n0), next = entry(n0 + 1);
@@ -626,8 +683,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = n0; n < n1 && ok; ++n) {
         const int after = entry(n + 2);
         const int off = part * kBlock;
-        const bool none = idx < wide && (page < 0 || page >= a.c.pages);
-        advance(idx, part);
+        const bool none = idx < wide && wanted(idx) && (page < 0 || page >= a.c.pages);
+        advance(idx, part, left);
         if (none) {
           page = (int)a.c.pages;
           if (err) atomicCAS(err, 0, (int)kDevBadPage);
@@ -773,6 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // their columns, but for the last part of a long page: `behind` parts come
       // after the block in its page.
       int plain_lo = 0x7fffffff, plain_hi = 0, behind = 1;
+      int plain_first = 0;  // with X blocks [0, plain_first) do too
       const bool tails = geo.parts > 1 ? page_size % kBlock != 0 : geo.pages * page_size != kBlock;
       // Where both halves take every block, half 0, whose product comes first, cleans a block's values (below) for both:
       // its blocks are plain if all rows of the tile see them.
@@ -782,18 +840,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int p_hi = turns && cleans ? min(all_hi, run->all_hi[1]) : all_hi;
         plain_lo = p_lo > 0 ? block_of_key(geo, page_size, p_lo - 1) + 1 : 0;
         plain_hi = block_of_key(geo, page_size, min(p_hi, s.len));
+        if constexpr (X) {
+          const int c = turns && cleans ? min(run->all_c[0], run->all_c[1]) : run->all_c[half];
+          plain_first = block_of_key(geo, page_size, min(c, s.len));
+        }
       }
       if (tails) behind = geo.parts - 1 - (j0 + (split ? half : 0)) % geo.parts;
       uint32_t s_there = 0;  // S of block i is known to be there
       for (int i = 0; i < mine; ++i) {
-        const int j = j0 + (split ? 2 * i + half : i);
-        const bool inside = j >= plain_lo && j < plain_hi, plain = inside && behind != 0;
-        if (tails && geo.parts > 1) behind = behind >= step ? behind - step : behind - step + geo.parts;
+        const int o = j0 + (split ? 2 * i + half : i), j = X && o >= run->firsts ? o + run->skip : o;
+        if (X && tails && geo.parts > 1) behind = geo.parts - 1 - j % geo.parts;
+        const bool inside = (j >= plain_lo && j < plain_hi) || (X && j < plain_first), plain = inside && behind != 0;
+        if (!X && tails && geo.parts > 1) behind = behind >= step ? behind - step : behind - step + geo.parts;
         const int c = n0 + i;
+        // with X, in a block that is not plain: the columns that the row sees (found ahead of S, which fills the registers)
+        uint32_t vis[X ? 4 : 1];
+        bool hidden = false;  // some row does not see some key of the block, whose values this half cleans
+        if constexpr (X) {
+          if (__builtin_expect(!plain, 0)) {
+            int base = 0, rows = page_size - (geo.parts - 1) * kBlock;  // inside: the last part of a page that all see
+            if (!inside) {
+              block_keys(geo, page_size, j, &base, &rows);
+              const int c_all = min(run->all_c[0], run->all_c[1]), lo_all = max(run->all_lo[0], run->all_lo[1]),
+                        hi_all = min(run->all_hi[0], run->all_hi[1]);
+              hidden = cleans && base + rows > c_all && (base < lo_all || base + rows > hi_all);
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) vis[w] = inside ? ~0u : sight_bits(Sight{first_keys, lo, hi}, base + 32 * w);
+            const int d0 = base - (s.len - s.n);
+            if (a.mask == kMaskTree && !inside && real && d0 + kBlock > 0) {
+#pragma unroll 1
+              for (int v = 0; v < 2; ++v) {
+                const int from = d0 + 64 * v;
+                if (from <= -64) continue;
+                uint64_t bits = ancestors(a, s, (row0 + row) / a.group, max(from, 0));
+                if (from < 0) bits <<= -from;
+                if (v == 0) vis[0] |= (uint32_t)bits, vis[1] |= (uint32_t)(bits >> 32);
+                else vis[2] |= (uint32_t)bits, vis[3] |= (uint32_t)(bits >> 32);
+              }
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) vis[w] &= low_bits(rows - 32 * w);
+          }
+        }
         if (!__all_sync(0xffffffffu, s_there)) ok = wait_phase(&s_full[half], (n0 + i) & 1, err, kDevTimeoutAccum);
         __syncwarp();
         tc_fence_after();
-        const uint32_t nones = hole[(it + j - j0) & 31];
+        const uint32_t nones = hole[(it + o - j0) & 31];
         float x[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(myS + 32 * c, x[c]);
@@ -804,25 +897,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(smem_u32(&s_free[half]));
         if (__builtin_expect(!plain || nones != 0, 0)) {
-          // columns [d0, d1) are keys of this row, [u0, u1) of all rows of this half; in the last part of a page that all
-          // see, the page's rows (without block_keys' division)
-          int d0 = 0, d1 = plain ? kBlock : page_size - (geo.parts - 1) * kBlock, u0 = d0, u1 = d1;
-          bool hidden = false;  // some row does not see some key of the block, whose values this half cleans
-          if (!inside) {
-            int base, rows;
-            block_keys(geo, page_size, j, &base, &rows);
-            d0 = lo - base, d1 = min(rows, hi - base);
-            u0 = all_lo - base, u1 = min(rows, all_hi - base);
-            if (cleans) hidden = base < max(run->all_lo[0], run->all_lo[1]) || base + rows > min(run->all_hi[0], run->all_hi[1]);
-          }
-          // by groups of 16 columns, if some row does not see them all
+          if constexpr (X) {
+            if (!plain) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (u0 > 16 * q || u1 < 16 * q + 16) {
+              for (int w = 0; w < 4; ++w)
+                if (!__all_sync(0xffffffffu, vis[w] == ~0u)) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (16 * q + e < d0 || 16 * q + e >= d1) x[q >> 1][16 * (q & 1) + e] = -INFINITY;
+                  for (int e = 0; e < 32; ++e)
+                    if (!((vis[w] >> e) & 1)) x[w][e] = -INFINITY;
+                }
             }
+          } else {
+            // columns [d0, d1) are keys of this row, [u0, u1) of all rows of this half; in the last part of a page that all
+            // see, the page's rows (without block_keys' division)
+            int d0 = 0, d1 = plain ? kBlock : page_size - (geo.parts - 1) * kBlock, u0 = d0, u1 = d1;
+            if (!inside) {
+              int base, rows;
+              block_keys(geo, page_size, j, &base, &rows);
+              d0 = lo - base, d1 = min(rows, hi - base);
+              u0 = all_lo - base, u1 = min(rows, all_hi - base);
+              if (cleans) hidden = base < max(run->all_lo[0], run->all_lo[1]) || base + rows > min(run->all_hi[0], run->all_hi[1]);
+            }
+            // by groups of 16 columns, if some row does not see them all
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (u0 > 16 * q || u1 < 16 * q + 16) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  if (16 * q + e < d0 || 16 * q + e >= d1) x[q >> 1][16 * (q & 1) + e] = -INFINITY;
+              }
+          }
           const int per = geo.parts == 1 ? page_size : kBlock;
           for (uint32_t left = nones; left; left &= left - 1) {
             const int p0 = (__ffs(left) - 1) * per;
@@ -836,7 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The lap of the ring before this block's has to be known to be there: the P V before the last one of this
             // half is, which is enough where both halves take all blocks and a block one slot.
             if (ok && i > 0 && (split || kOne)) ok = wait_phase(&o_done[bar_of(half, c - 1)], phase_of(c - 1), err, kDevTimeoutAccum);
-            ok = ok && clean_values<T, DP>(sV, full + SK, (it + j - j0) * pv, pv, hrow, j, run, err);
+            ok = ok && clean_values<T, DP>(sV, full + SK, (it + o - j0) * pv, pv, hrow, j, run, err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
           }
@@ -946,7 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!split || half == 0) {
         const float rl = l == 0.f ? 0.f : 1.f / l;
-        const int odd_lo = max(run->odd_lo, j0), odd_hi = min(run->odd_hi, k1 - 1);
+        const int odd_lo = X ? run->odd_lo : max(run->odd_lo, j0), odd_hi = X ? run->odd_hi : min(run->odd_hi, k1 - 1);
         T* dst = real ? out_row<T>(a, s, h, row0 + row) : nullptr;
 #pragma unroll 1
         for (int c = 0; c < DP / 16; ++c) {
@@ -976,7 +1080,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             block_keys(geo, page_size, odd_lo, &k_lo, &kr);
             block_keys(geo, page_size, odd_hi, &k_hi, &kr);
             k_hi += kr;
-            for (int k = max(lo, k_lo); k < min(hi, k_hi); ++k) {
+            if (X && a.mask == kMaskTree) k_hi = min(k_hi, s.len);
+            for (int k = X ? k_lo : max(lo, k_lo); k < (X ? k_hi : min(hi, k_hi)); ++k) {
+              if constexpr (X) {
+                bool sees = k < first_keys || (k >= lo && k < hi);
+                const int d = k - (s.len - s.n);
+                if (!sees && a.mask == kMaskTree && d >= 0) sees = ancestors(a, s, (row0 + row) / a.group, d) & 1;
+                if (!sees) continue;
+              }
               const int page = kv_page(table, k, page_size, a.c.pages);
               if (page < 0) continue;
               const T* src = (const T*)a.c.v + page * a.c.v_page + h * a.c.v_head + (k % page_size) * a.c.v_row;
@@ -1046,12 +1157,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // order of the keys.  A warp takes 8 rows x 16 channels: 128-byte reads of the
 // parts, 32-byte writes of the rows.
 constexpr int kJoinThreads = 256;
-template <typename T, int DP>
+template <typename T, int DP, bool X>
 __global__ void __launch_bounds__(kJoinThreads) kv_chunk_join_kernel(const __grid_constant__ AttnArgs a, const int G) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int kRows = Cfg<DP>::kRows;
   const int me = blockIdx.x;
-  const Space ws = space<DP>(a, G);
+  const Space<X> ws = space<DP, X>(a, G);
   const Open op = ws.open[me];
   // Rows of sequences without a key get their zeros here.  Where a wait ran out the other rows, written or not, become
   // NaN: the call may have no status word to tell it.
@@ -1108,11 +1219,11 @@ __global__ void __launch_bounds__(kJoinThreads) kv_chunk_join_kernel(const __gri
   }
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool X>
 cudaError_t go(const ChunkLaunch& L, int sms, cudaStream_t s) {
   using C = Cfg<DP>;
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem((const void*)kv_chunk_kernel<T, DP>, C::kSmem, &allowed);
+  cudaError_t e = allow_smem((const void*)kv_chunk_kernel<T, DP, X>, C::kSmem, &allowed);
   if (e != cudaSuccess) return e;
   // each may start as the kernel before it drains, and waits for its end
   cudaLaunchConfig_t cfg = {};
@@ -1124,17 +1235,17 @@ cudaError_t go(const ChunkLaunch& L, int sms, cudaStream_t s) {
   cfg.stream = s;
   cfg.gridDim = dim3((unsigned)((row_tiles(L.a) + kPlanWarps - 1) / kPlanWarps));
   cfg.blockDim = dim3(32 * kPlanWarps);
-  e = cudaLaunchKernelEx(&cfg, kv_chunk_plan_kernel, L.a, L.geo);
+  e = cudaLaunchKernelEx(&cfg, kv_chunk_plan_kernel<X>, L.a, L.geo);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(sms);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
-  e = cudaLaunchKernelEx(&cfg, kv_chunk_kernel<T, DP>, L.k, L.v, L.a, L.geo);
+  e = cudaLaunchKernelEx(&cfg, kv_chunk_kernel<T, DP, X>, L.k, L.v, L.a, L.geo);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(sms, 16);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, kv_chunk_join_kernel<T, DP>, L.a, sms);
+  return cudaLaunchKernelEx(&cfg, kv_chunk_join_kernel<T, DP, X>, L.a, sms);
 }
 
 }  // namespace
@@ -1150,14 +1261,23 @@ bool kv_chunk_geometry(const AttnArgs& a, ChunkGeo* g) {
 
 long long kv_chunk_workspace(const AttnArgs& a, int sms) {
   const int DP = a.c.D <= 64 ? 64 : a.c.D <= 128 ? 128 : 256;
-  return kFaultBytes + row_tiles(a) * (long long)sizeof(RowTile) + (long long)sms * (sizeof(Open) + 2 * tile_rows(DP) * (sizeof(float2) + (size_t)DP * sizeof(float)));
+  return kFaultBytes + row_tiles(a) * (long long)(a.mask == kMaskRanges ? sizeof(Tile<false>) : sizeof(Tile<true>)) + (long long)sms * (sizeof(Open) + 2 * tile_rows(DP) * (sizeof(float2) + (size_t)DP * sizeof(float)));
 }
 
-cudaError_t launch_kv_chunk(const ChunkLaunch& L, int sms, cudaStream_t s) {
+namespace {
+
+template <bool X>
+cudaError_t by_kind(const ChunkLaunch& L, int sms, cudaStream_t s) {
   const bool bf16 = L.a.c.elem == 1;
-  if (L.a.c.D <= 64) return bf16 ? go<__nv_bfloat16, 64>(L, sms, s) : go<__half, 64>(L, sms, s);
-  if (L.a.c.D <= 128) return bf16 ? go<__nv_bfloat16, 128>(L, sms, s) : go<__half, 128>(L, sms, s);
-  return bf16 ? go<__nv_bfloat16, 256>(L, sms, s) : go<__half, 256>(L, sms, s);
+  if (L.a.c.D <= 64) return bf16 ? go<__nv_bfloat16, 64, X>(L, sms, s) : go<__half, 64, X>(L, sms, s);
+  if (L.a.c.D <= 128) return bf16 ? go<__nv_bfloat16, 128, X>(L, sms, s) : go<__half, 128, X>(L, sms, s);
+  return bf16 ? go<__nv_bfloat16, 256, X>(L, sms, s) : go<__half, 256, X>(L, sms, s);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_chunk(const ChunkLaunch& L, int sms, cudaStream_t s) {
+  return L.a.mask == kMaskRanges ? by_kind<false>(L, sms, s) : by_kind<true>(L, sms, s);
 }
 
 }  // namespace wan

@@ -112,7 +112,7 @@ constexpr int kChunkRows = 64;
 constexpr double kChunkWork = 6e5;
 
 bool chunk_rows(const AttnArgs& a, ChunkGeo* g) {
-  return a.mask == kMaskRanges && (int64_t)a.b.T * a.group >= (int64_t)kChunkRows * a.b.B &&
+  return (int64_t)a.b.T * a.group >= (int64_t)kChunkRows * a.b.B &&
          (double)a.b.T * a.q_heads * a.b.max_pages * a.c.page_size >= kChunkWork && kv_chunk_geometry(a, g);
 }
 int64_t workspace_of(const AttnArgs& a, bool chunk, int sms) {
