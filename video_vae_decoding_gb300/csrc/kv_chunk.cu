@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kSoftEnd = kOne ? 8 : 12;  // softmax warps are 4 up to this one
   // the only shared memory of the kernel, so it starts on a 1024-byte boundary, as the swizzled boxes must
   extern __shared__ __align__(1024) uint8_t smem[];
-  static_assert(2 * sizeof(Run) + sizeof(Cursor) + 8 * (2 * S + 14) + 8 + 128 + 16 <= 1024, "barriers and the run's description");
+  static_assert(2 * sizeof(Run) + sizeof(Cursor) + 8 * (2 * S + 15) + 8 + 128 + 16 <= 1024, "barriers and the run's description");
   uint8_t* sQ = smem;  // [half][64-channel box][128 rows]
   uint8_t *sK = sQ + C::kQ, *sV = sK + SK * C::kKeySlot;  // SK slots of K, SV of V; their barriers in this order
   uint64_t* full = reinterpret_cast<uint64_t*>(sV + SV * C::kValSlot);
@@ -440,13 +440,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_full = s_free + 2;  // [half][P buffer] 128 arrivals: P_t in TMEM (and O_t rescaled)
   uint64_t* o_done = p_full + 4;  // [half][P buffer] O_t += P_t V_j complete
   uint64_t* done = o_done + 4;    // [2] all products issued by warp 1, and by warp 2, complete
+  uint64_t* told = done + 2;      // the next run is described
   if (smem_u32(smem) & 1023) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x == 0) *space<DP, X>(a, gridDim.x).fault = 1;
     if (a.b.status) atomicCAS(a.b.status, 0, (int)kDevTimeoutFull);
     return;
   }
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 2);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(told + 1);
   volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* hole = tmem_slot + 2;  // [32]: bit i of hole[c % 32]: page i of the c-th block is none of the cache's
   Run* runs = reinterpret_cast<Run*>((reinterpret_cast<uintptr_t>(hole + 32) + 15) & ~uintptr_t(15));  // [2]
@@ -473,6 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&p_full[t]), 128);
       mbar_init(smem_u32(&o_done[t]), 1);
     }
+    mbar_init(smem_u32(told), 1);
     *stop = 0;
     fence_mbar_init();
     tma_prefetch_map(&mapK);
@@ -577,6 +579,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
 
+  // Q and the first V of the next run come while this one ends: q in its room from the last Q K on (by warp 1), where the
+  // halves do not need that for their sums and its rows can be copied as they are.  (64 drafts of 24 sequences, heads of
+  // 128, take 132 us so, 135 without; ragged causal chunks at heads of 64 take 104 and 91: too little time to fill.)
+  constexpr bool kAheadOfRun = DP > 64;
+  const bool q_plain = a.scale_log2 > 0.f && ((uintptr_t)a.q & 15) == 0 && (a.q_t & 7) == 0 && (a.q_h & 7) == 0;
+  bool q_came = false;
+  // where row `row` of a run has its q (-1: the tile has no such row)
+  constexpr int CH = DP / 8, RPI = 32 / CH;  // 16-byte pieces of a row, rows that a warp fetches in a step
+  auto q_of = [&](const Run* run, int row) {
+    if (row >= run->cnt) return -1LL;
+    const int t = (run->row0 + row) / a.group, g = run->row0 + row - t * a.group;
+    return (long long)(run->s.r0 + t) * a.q_t + (long long)(run->h * a.group + g) * a.q_h;
+  };
+
   for (int r = 0; runs[r & 1].blocks > 0; ++r) {
     Run* const run = &runs[r & 1];
     const int h = run->h, row0 = run->row0, cnt = run->cnt, k0 = run->k0, k1 = run->k1;
@@ -601,34 +617,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lo > 0) atomicMax(&run->all_lo[half], lo);
         atomicMin(&run->all_hi[half], hi);
       }
-      uint8_t* q = sQ + half * ND * kBoxBytes + hrow * 128;
+    }
+    if (softmax && !q_came) {
       // q is negated for a negative scale (the maximum is then that of q . k) and cleared for a scale of zero
-      // (whose product with a hidden key's -inf is none)
+      // (whose product with a hidden key's -inf is none).  A warp fetches its 32 rows whole, side by side, and stores
+      // them when all are on their way: lane i knows where row i is.
       const bool flip = a.scale_log2 < 0.f;
-      const T* src = nullptr;
-      if (real) {
-        const int t = (row0 + row) / a.group, g = row0 + row - t * a.group;
-        src = (const T*)a.q + (long long)(s.r0 + t) * a.q_t + (long long)(h * a.group + g) * a.q_h;
-      }
-#pragma unroll 4
-      for (int c = 0; c < DP / 8; ++c) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (real && c * 8 < a.c.D) {
-          if (((uintptr_t)src & 15) == 0) {
-            v = *reinterpret_cast<const uint4*>(src + c * 8);
-          } else {
-            const uint16_t* e = reinterpret_cast<const uint16_t*>(src + c * 8);
-            v = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16,
-                           e[6] | (uint32_t)e[7] << 16);
+      const long long at = q_of(run, row);
+      const int c = lane % CH;
+      uint8_t* const q = sQ + (half * ND + (c >> 3)) * kBoxBytes;
+      const bool whole16 = ((uintptr_t)a.q & 15) == 0 && (a.q_t & 7) == 0 && (a.q_h & 7) == 0;
+      constexpr int kBatch = CH < 16 ? CH : 16;  // steps whose loads are all on their way before the first is stored
+#pragma unroll 1
+      for (int i0 = 0; i0 < CH; i0 += kBatch) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const long long from = __shfl_sync(0xffffffffu, at, (i0 + i) * RPI + lane / CH);
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (from >= 0 && c * 8 < a.c.D && a.scale_log2 != 0.f) {
+            const T* src = (const T*)a.q + from + c * 8;
+            if (whole16) {
+              v[i] = *reinterpret_cast<const uint4*>(src);
+            } else {
+              const uint16_t* e = reinterpret_cast<const uint16_t*>(src);
+              v[i] = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16,
+                                e[6] | (uint32_t)e[7] << 16);
+            }
           }
-          if (a.scale_log2 == 0.f) v = make_uint4(0, 0, 0, 0);
-          if (flip) v = make_uint4(v.x ^ 0x80008000u, v.y ^ 0x80008000u, v.z ^ 0x80008000u, v.w ^ 0x80008000u);
         }
-        *reinterpret_cast<uint4*>(q + (c >> 3) * kBoxBytes + (((c & 7) ^ (hrow & 7)) << 4)) = v;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int to = 32 * (warp & 3) + (i0 + i) * RPI + lane / CH;
+          const uint32_t sign = flip ? 0x80008000u : 0u;
+          *reinterpret_cast<uint4*>(q + to * 128 + (((c & 7) ^ (to & 7)) << 4)) =
+              make_uint4(v[i].x ^ sign, v[i].y ^ sign, v[i].z ^ sign, v[i].w ^ sign);
+        }
       }
       fence_proxy_async_smem();
     }
+    if (warp == 1 && q_came) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+    }
     if (softmax || warp == 1) q_sync<kOne ? 160 : 288>();
+    q_came = kAheadOfRun && q_plain && !split;  // (of the next run)
     const int j0 = k0, nb = k1 - k0;
     // blocks of each half
     const int nh[2] = {split ? (nb + 1) / 2 : nb, kOne ? 0 : split ? nb / 2 : nb};
@@ -728,11 +761,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kAhead = SK / pk;
       loads(std::true_type(), run, it, r > 0 ? min(nb, kAhead) : 0, nb);
       Run* const next = &runs[(r + 1) & 1];
-      if (lane == 0) describe(next);
+      if (lane == 0) {
+        describe(next);
+        mbar_arrive(smem_u32(told));
+      }
       __syncwarp();
       if (ok && next->blocks > 0) loads(std::true_type(), next, it + nb, 0, min(next->blocks, kAhead));
     } else if (warp == 3) {
-      loads(std::false_type(), run, it, 0, nb);
+      // as with K: the slots that V of the next run's first blocks takes held blocks whose products need nothing of this warp
+      const int kAhead = kAheadOfRun ? SV / pv : 0;
+      loads(std::false_type(), run, it, r > 0 ? min(nb, kAhead) : 0, nb);
+      const Run* const next = &runs[(r + 1) & 1];
+      if (kAheadOfRun && ok && !__all_sync(0xffffffffu, wait_phase(told, r & 1, err, kDevTimeoutFull))) {
+        ok = false;
+        *stop = 1;
+      }
+      if (kAheadOfRun && ok && next->blocks > 0) loads(std::false_type(), next, it + nb, 0, min(next->blocks, kAhead));
     } else if (warp == 1 || warp == 2) {
       // ------------------------------------------------- products: Q K, and P V
       // A whole warp walks the steps (what it computes stays in uniform
@@ -782,6 +826,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
           if (ends) there = g + 1 < steps && ask_phase(&full[slot], phase);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (kAheadOfRun && ok && q_came) {
+          const int t = turns ? 1 : kOne ? 0 : (steps - 1) & 1;  // the last step's half
+          ok = wait_phase(told, r & 1, err, kDevTimeoutFull);
+          if (ok) ok = wait_phase(&s_full[t], (ns[t] + nh[t] - 1) & 1, err, kDevTimeoutAccum);
+          ok = __all_sync(0xffffffffu, ok);
+          const Run* const next = &runs[(r + 1) & 1];
+          if (ok && next->blocks > 0) {
+            // the products that read q are complete
+            const bool twice = !kOne && next->cnt <= kHalfRows;  // the same rows for both halves
+            const int c = lane % CH;
+#pragma unroll 1
+            for (int w = 0; w < kRows / 32; ++w) {
+              const long long at = q_of(next, 32 * (twice ? w & 3 : w) + lane);
+              const uint32_t q = smem_u32(sQ) + ((w >> 2) * ND + (c >> 3)) * kBoxBytes;
+#pragma unroll 4
+              for (int i = 0; i < CH; ++i) {
+                const int from_row = i * RPI + lane / CH, to = 32 * (w & 3) + from_row;
+                const long long from = __shfl_sync(0xffffffffu, at, from_row);
+                const bool take = from >= 0 && c * 8 < a.c.D;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(q + to * 128 + (((c & 7) ^ (to & 7)) << 4)),
+                             "l"((const T*)a.q + (take ? from + c * 8 : 0)), "r"(take ? 16 : 0)
+                             : "memory");
+              }
+            }
+          }
         }
       } else {
         const uint32_t vd0 = desc_v(smem_u32(sV)), id0 = idesc(Pack<T>::kFormat, true, 16 * min(4 * C::kValBoxes, dn));
@@ -845,13 +916,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           plain_first = block_of_key(geo, page_size, min(c, s.len));
         }
       }
-      if (tails) behind = geo.parts - 1 - (j0 + (split ? half : 0)) % geo.parts;
+      // with X, the block at hand: number j0 (+ 1) of the tile's, and the first number behind the gap if that is still ahead
+      int at = j0 + (split ? half : 0), gap = 0x7fffffff;
+      if constexpr (X) {
+        if (at >= run->firsts) at += run->skip;
+        else gap = run->firsts;
+      }
+      if (tails) behind = geo.parts - 1 - at % geo.parts;
       uint32_t s_there = 0;  // S of block i is known to be there
       for (int i = 0; i < mine; ++i) {
-        const int o = j0 + (split ? 2 * i + half : i), j = X && o >= run->firsts ? o + run->skip : o;
-        if (X && tails && geo.parts > 1) behind = geo.parts - 1 - j % geo.parts;
+        const int o = j0 + (split ? 2 * i + half : i), j = X ? at : o;
         const bool inside = (j >= plain_lo && j < plain_hi) || (X && j < plain_first), plain = inside && behind != 0;
-        if (!X && tails && geo.parts > 1) behind = behind >= step ? behind - step : behind - step + geo.parts;
+        if (tails && geo.parts > 1) behind = behind >= step ? behind - step : behind - step + geo.parts;
+        if constexpr (X) {
+          at += step;
+          if (at >= gap) {  // (once: the gap is behind it then)
+            at += run->skip;
+            gap = 0x7fffffff;
+            if (tails) behind = geo.parts - 1 - at % geo.parts;
+          }
+        }
         const int c = n0 + i;
         // with X, in a block that is not plain: the columns that the row sees (found ahead of S, which fills the registers)
         uint32_t vis[X ? 4 : 1];
@@ -1133,6 +1217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (*stop) break;
   }
 
+  if (warp == 1) asm volatile("cp.async.wait_all;" ::: "memory");
   // after a wait that ran out: the loads in flight arrive, and the MMAs complete, before the memory is given back
   if (*stop && warp == 0 && lane == 0) {
     for (int s = 0; s < S; ++s) {
