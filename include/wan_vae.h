@@ -573,11 +573,12 @@ wan_status wan_kv_fork(const wan_kv_cache* cache, int32_t* pages, int64_t page_s
  * lengths[b] = f counts the first keys of sequence b that stay where they are,
  * and cu_tokens (not NULL) its range of keep (`tokens` numbers, device int32):
  * the key at place keep[cu_tokens[b] + j] moves to place f + j, all as if at
- * once, and lengths[b], the call's result, becomes f plus their count.  A key
- * moves ahead or stays: one with keep[..] < f + j, or one that the table has no
- * page for, is left out (place f + j keeps what it had) with a code in the
- * batch's status word; so is a sequence whose f, range or result the table
- * cannot hold (none of its keys move, and its result is f, or 0 where f is none).
+ * once, and lengths[b], the call's result, becomes f plus their count.  A
+ * sequence's numbers ascend, from f or later on.  Where they do not, or the table
+ * has no page for one, some of its keys are left out (their new places keep what
+ * they had) and a code is left in the batch's status word; so is a sequence whose
+ * f, range or result the table cannot hold (none of its keys move, and its result
+ * is f, or 0 where f is none).
  * Several sequences of a call must not share a page that the call writes to or
  * that one of them reads from and another writes.  lengths: device int32, not in
  * the memory that the call reads.  heads: up to 1000.  Errors: as above. */

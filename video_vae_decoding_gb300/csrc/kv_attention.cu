@@ -276,6 +276,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
     auto in_sight = [&](int key) { return (key >= lo && key < hi) || (X && key < c); };
     uint64_t drafts = 0;  // of the drafts from this one on, those that the lane's row sees
     int drafts_from = -64;
+    Family kin = {};
+    if constexpr (X) {
+      if (a.mask == kMaskTree && key_of(w1) > s.len - s.n) kin = family(a, s);
+    }
 
     const int* table = a.b.pages + b * a.b.page_stride;
 
@@ -398,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
             if (a.mask == kMaskTree && d0 + kKeys > 0) {
               if (d0 + kKeys > drafts_from + 64) {
                 drafts_from = max(d0, 0);
-                drafts = ancestors(a, s, (row0 + min(lane, cnt - 1)) / a.group, drafts_from);
+                drafts = ancestors(a, s, kin, (row0 + min(lane, cnt - 1)) / a.group, drafts_from);
               }
               vis |= (uint32_t)(d0 >= drafts_from ? drafts >> (d0 - drafts_from) : drafts << (drafts_from - d0));
             }

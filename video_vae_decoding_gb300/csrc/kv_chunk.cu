@@ -952,12 +952,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int w = 0; w < 4; ++w) vis[w] = inside ? ~0u : sight_bits(Sight{first_keys, lo, hi}, base + 32 * w);
             const int d0 = base - (s.len - s.n);
-            if (a.mask == kMaskTree && !inside && real && d0 + kBlock > 0) {
+            if (a.mask == kMaskTree && !inside && d0 + kBlock > 0) {
+              const Family kin = family(a, s);
 #pragma unroll 1
               for (int v = 0; v < 2; ++v) {
                 const int from = d0 + 64 * v;
                 if (from <= -64) continue;
-                uint64_t bits = ancestors(a, s, (row0 + row) / a.group, max(from, 0));
+                uint64_t bits = ancestors(a, s, kin, real ? (row0 + row) / a.group : -1, max(from, 0));
                 if (from < 0) bits <<= -from;
                 if (v == 0) vis[0] |= (uint32_t)bits, vis[1] |= (uint32_t)(bits >> 32);
                 else vis[2] |= (uint32_t)bits, vis[3] |= (uint32_t)(bits >> 32);
@@ -1158,19 +1159,26 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (__builtin_expect(odd_lo <= odd_hi && real, 0)) {
+          if (__builtin_expect(odd_lo <= odd_hi && (real || X), 0)) {
             const int* table = a.b.pages + run->b * a.b.page_stride;
             int k_lo, k_hi, kr;
             block_keys(geo, page_size, odd_lo, &k_lo, &kr);
             block_keys(geo, page_size, odd_hi, &k_hi, &kr);
             k_hi += kr;
-            if (X && a.mask == kMaskTree) k_hi = min(k_hi, s.len);
+            Family kin = {};
+            if (X && a.mask == kMaskTree) {
+              k_hi = min(k_hi, s.len);
+              kin = family(a, s);
+            }
             for (int k = X ? k_lo : max(lo, k_lo); k < (X ? k_hi : min(hi, k_hi)); ++k) {
               if constexpr (X) {
                 bool sees = k < first_keys || (k >= lo && k < hi);
                 const int d = k - (s.len - s.n);
-                if (!sees && a.mask == kMaskTree && d >= 0) sees = ancestors(a, s, (row0 + row) / a.group, d) & 1;
-                if (!sees) continue;
+                if (a.mask == kMaskTree && d >= 0) {  // (the warp's lanes walk together)
+                  const uint64_t up = ancestors(a, s, kin, real ? (row0 + row) / a.group : -1, d);
+                  sees = sees || (up & 1);
+                }
+                if (!sees || !real) continue;
               }
               const int page = kv_page(table, k, page_size, a.c.pages);
               if (page < 0) continue;

@@ -13,6 +13,9 @@ namespace wan {
 
 namespace {
 
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((unsigned long long)a | (unsigned long long)b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
 __device__ __forceinline__ void tell(int* status, int code) {
   if (status) atomicCAS(status, 0, code);
 }
@@ -22,11 +25,11 @@ __device__ __forceinline__ void tell(int* status, int code) {
 // each copy (three copies of a cache of 223 MB: 894 MB instead of 1341).
 //
 // The work of a call is one line of row groups (source, page, K or V, head,
-// rows) that is cut into equal pieces, one per warp, from the lengths on the
-// device: one long sequence is spread over the whole card, and a captured
-// graph follows its lengths.
-constexpr int kForkWarps = 8, kForkCtas = 4;
+// rows), laid out from the lengths on the device: one long sequence is spread over
+// the whole card, and a captured graph follows its lengths.
+constexpr int kForkWarps = 8, kForkCtas = 3;
 constexpr int kAhead = 4;  // row groups that a warp has in flight
+constexpr int kTurn = 8;  // and that it takes at a time, if there are as many for each
 
 struct ForkPlan {  // per fork, in shared memory
   int source, target;
@@ -38,7 +41,7 @@ struct ForkPlan {  // per fork, in shared memory
 __global__ void __launch_bounds__(32 * kForkWarps, kForkCtas) kv_fork_kernel(const __grid_constant__ ForkArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   ForkPlan* plan = reinterpret_cast<ForkPlan*>(smem);
-  __shared__ long long s_warp[kForkWarps + 1];
+  __shared__ long long s_warp[kForkWarps];
   constexpr int kThreads = 32 * kForkWarps;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int CH = a.c.D / 8, RPW = 32 / CH;  // 16-byte pieces of a row, rows of a group
@@ -47,71 +50,74 @@ __global__ void __launch_bounds__(32 * kForkWarps, kForkCtas) kv_fork_kernel(con
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int i = threadIdx.x; i < a.N; i += kThreads) {
-    plan[i].source = a.sources[i];
-    plan[i].target = a.targets[i];
+    const int p = a.sources[i], t = a.targets[i];
+    plan[i].source = p;
+    plan[i].target = t;
+    int len = -1;
+    if (p >= 0 && p < a.B && t >= 0 && t < a.B && kv_length(a.lengths[p], a.max_pages, size, &len)) {
+      const int copied = a.share ? (len % size ? 1 : 0) : (len + size - 1) / size;
+      if (copied > a.fresh_pages) len = -1;
+    } else {
+      len = -1;
+    }
+    plan[i].len = len;
   }
   __syncthreads();
   // A fork whose target is a source, or the target of an earlier one, would race with it.
   for (int i = threadIdx.x; i < a.N; i += kThreads) {
-    const int p = plan[i].source, t = plan[i].target;
-    int len = 0, code = 0;
-    if (p < 0 || p >= a.B || t < 0 || t >= a.B) {
-      code = kDevBadLength;
-    } else {
-      for (int k = 0; k < a.N; ++k)
-        if (plan[k].source == t || (k < i && plan[k].target == t)) code = kDevBadLength;
-      if (!kv_length(a.lengths[p], a.max_pages, size, &len)) code = kDevBadLength;
-      const int copied = a.share ? (len % size ? 1 : 0) : (len + size - 1) / size;
-      if (copied > a.fresh_pages) code = kDevBadLength;
-    }
-    if (code) tell(a.status, code);
-    plan[i].len = code ? -1 : len;
+    const int t = plan[i].target;
+    bool left_out = plan[i].len < 0;
+#pragma unroll 8
+    for (int k = 0; k < a.N; ++k) left_out = left_out || plan[k].source == t || (k < i && plan[k].target == t);
+    if (left_out) tell(a.status, kDevBadLength);
+    plan[i].next = left_out;
   }
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.N; i += kThreads)
+    if (plan[i].next) plan[i].len = -1;
   __syncthreads();
   // chains of forks of one source, and the groups of each chain's first
-  constexpr int kEach = kMaxForks / kThreads;  // forks of a thread, side by side
-  long long groups[kEach], mine = 0;
-#pragma unroll
-  for (int e = 0; e < kEach; ++e) {
-    const int i = threadIdx.x * kEach + e;
-    groups[e] = 0;
-    if (i >= a.N) continue;
-    int next = -1;
-    const int len = plan[i].len;
-    if (len > 0) {
-      bool first = true;
-      for (int k = 0; k < i; ++k) first = first && !(plan[k].len >= 0 && plan[k].source == plan[i].source);
-      for (int k = a.N - 1; k > i; --k)
-        if (plan[k].len >= 0 && plan[k].source == plan[i].source) next = k;
-      if (first) {
-        const long long whole = a.share ? 0 : len / size;
-        groups[e] = 2LL * a.c.heads * (whole * ((size + RPW - 1) / RPW) + (len % size + RPW - 1) / RPW);
-      }
+  for (int i = threadIdx.x; i < a.N; i += kThreads) {
+    const int len = plan[i].len, p = plan[i].source;
+    int next = a.N;
+    bool first = len > 0;
+#pragma unroll 8
+    for (int k = 0; k < a.N; ++k) {
+      const bool same = plan[k].len >= 0 && plan[k].source == p;
+      first = first && !(same && k < i);
+      if (same && k > i) next = min(next, k);
     }
-    plan[i].next = next;
-    mine += groups[e];
+    long long groups = 0;
+    if (first) {
+      const long long whole = a.share ? 0 : len / size;
+      groups = 2LL * a.c.heads * (whole * ((size + RPW - 1) / RPW) + (len % size + RPW - 1) / RPW);
+    }
+    plan[i].next = len > 0 && next < a.N ? next : -1;
+    plan[i].begin = groups;
   }
-  long long incl = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += o;
-  }
-  if (lane == 31) s_warp[warp] = incl;
   __syncthreads();
-  long long before = incl - mine, total = 0;
+  // where each begins: forks side by side in a thread, in rounds
+  long long total = 0;
+  for (int i0 = 0; i0 < a.N; i0 += kThreads) {
+    const int i = i0 + threadIdx.x;
+    const long long mine = i < a.N ? plan[i].begin : 0;
+    long long incl = mine;
 #pragma unroll
-  for (int w = 0; w < kForkWarps; ++w) {
-    if (w < warp) before += s_warp[w];
-    total += s_warp[w];
-  }
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    long long before = total + incl - mine;
 #pragma unroll
-  for (int e = 0; e < kEach; ++e) {
-    const int i = threadIdx.x * kEach + e;
+    for (int w = 0; w < kForkWarps; ++w) {
+      if (w < warp) before += s_warp[w];
+      total += s_warp[w];
+    }
     if (i < a.N) plan[i].begin = before;
-    before += groups[e];
+    __syncthreads();
   }
-  __syncthreads();
 
   // the tables: rows that are written are read by no fork
   for (int i = blockIdx.x; i < a.N; i += gridDim.x) {
@@ -124,92 +130,47 @@ __global__ void __launch_bounds__(32 * kForkWarps, kForkCtas) kv_fork_kernel(con
     if (threadIdx.x == 0) a.lengths[f.target] = f.len;
   }
 
-  // this warp's piece of the line
-  const long long W = (long long)gridDim.x * kForkWarps, me = (long long)blockIdx.x * kForkWarps + warp;
-  const long long each = total / W, more = total - each * W;
-  long long at = me * each + min(me, more);
-  const long long end = at + each + (me < more ? 1 : 0);
-  if (at >= end) return;
-  int i = 0;  // the last fork that begins at or before `at` (forks without groups begin with the next one)
-  {
-    int lo = 0, hi = a.N;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (plan[mid].begin <= at) lo = mid; else hi = mid;
-    }
-    i = lo;
-  }
-  // place in fork i's groups: page j of those that are copied, plane (K or V, head), group g
-  int len, whole, j, plane, g, rows, per;
-  auto enter = [&](long long off) {
-    len = plan[i].len;
-    whole = len / size;  // full pages
-    const int full = (size + RPW - 1) / RPW;
-    const long long page_groups = 2LL * a.c.heads * full, in_full = a.share ? 0 : whole * page_groups;
-    j = a.share ? whole : (int)(off < in_full ? off / page_groups : whole);
-    const long long r = off < in_full ? off - j * page_groups : off - in_full;
-    rows = j < whole ? size : len - whole * size;
-    per = (rows + RPW - 1) / RPW;
-    plane = (int)(r / per);
-    g = (int)(r - (long long)plane * per);
-  };
-  enter(at - plan[i].begin);
-  const int sub = lane / CH, ch = lane - sub * CH;
-  const bool busy = sub < RPW;
-  while (at < end) {
-    // up to kAhead groups of fork i's chain
-    uint4 v[kAhead];
-    int jj[kAhead], hd[kAhead], row[kAhead];
-    bool ofv[kAhead], live[kAhead];
-    const int chain = i;
-    int n = 0;
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      live[u] = false;
-      if (at >= end || i != chain) continue;
-      n = u + 1;
-      jj[u] = j;
-      ofv[u] = plane >= a.c.heads;
-      hd[u] = ofv[u] ? plane - a.c.heads : plane;
-      row[u] = g * RPW + sub;
-      const int page = a.pages[plan[i].source * a.page_stride + j];
-      const bool there = page >= 0 && page < a.c.pages;
-      if (!there) tell(a.status, kDevBadPage);
-      live[u] = there && busy && row[u] < rows;
-      if (live[u]) {
-        const long long o = ofv[u] ? page * a.c.v_page + hd[u] * a.c.v_head + row[u] * a.c.v_row
-                                   : page * a.c.k_page + hd[u] * a.c.k_head + row[u] * a.c.k_row;
-        v[u] = *reinterpret_cast<const uint4*>((const uint16_t*)(ofv[u] ? a.c.v : a.c.k) + o + ch * 8);
+  // The line goes round the warps, a few groups at a time: what is copied at one time lies together in memory.
+  const long long W = (long long)gridDim.x * kForkWarps, each = min((long long)kTurn, quotient(total + W - 1, W));
+  const int sub = lane / CH, ch = lane - sub * CH, full = (size + RPW - 1) / RPW;
+  int i = 0;  // the last fork that begins at or before the turn (forks without groups begin with the next one)
+  for (long long turn = (long long)blockIdx.x * kForkWarps + warp; turn * each < total; turn += W) {
+    long long at = turn * each;
+    const long long end = min(total, at + each);
+    while (at < end) {
+      // group g of a plane (page j of fork i's, K or V, head), and how many of the plane's there are from it on
+      while (i + 1 < a.N && plan[i + 1].begin <= at) ++i;
+      const int len = plan[i].len, whole = len / size;  // full pages
+      const long long off = at - plan[i].begin, page_groups = 2LL * a.c.heads * full, in_full = a.share ? 0 : whole * page_groups;
+      const int j = a.share ? whole : (int)(off < in_full ? quotient(off, page_groups) : whole);
+      const long long r = off < in_full ? off - j * page_groups : off - in_full;
+      const int rows = j < whole ? size : len - whole * size, per = (rows + RPW - 1) / RPW;
+      const int plane = (int)quotient(r, per), g = (int)(r - (long long)plane * per);
+      const int n = (int)min((long long)(per - g), end - at);
+      at += n;
+      const bool ofv = plane >= a.c.heads;
+      const long long s_page = ofv ? a.c.v_page : a.c.k_page, s_row = ofv ? a.c.v_row : a.c.k_row;
+      const long long first = (ofv ? (plane - a.c.heads) * a.c.v_head : plane * a.c.k_head) + (g * RPW + sub) * s_row + ch * 8;
+      uint16_t* const base = (uint16_t*)(ofv ? a.c.v : a.c.k) + first;
+      const int page = a.pages[plan[i].source * a.page_stride + j], left = sub < RPW ? rows - g * RPW - sub : 0;
+      if (page < 0 || page >= a.c.pages) {
+        tell(a.status, kDevBadPage);
+        continue;
       }
-      // the next group
-      ++at;
-      if (++g == per) {
-        g = 0;
-        if (++plane == 2 * a.c.heads) {
-          plane = 0;
-          ++j;
-          if (j == whole && len > whole * size) {
-            rows = len - whole * size;
-            per = (rows + RPW - 1) / RPW;
-          } else if (j >= whole && at < end) {  // the next fork with groups
-            do ++i; while (i + 1 < a.N && plan[i + 1].begin <= at);
-            enter(at - plan[i].begin);
+      for (int b = 0; b < n; b += kAhead) {
+        uint4 v[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          if (b + u < n && (b + u) * RPW < left) v[u] = *reinterpret_cast<const uint4*>(base + page * s_page + (b + u) * RPW * s_row);
+        for (int m = i; m >= 0; m = plan[m].next) {
+          const int to = a.fresh[m * a.fresh_stride + (a.share ? 0 : j)];
+          if (to < 0 || to >= a.c.pages) {
+            tell(a.status, kDevBadPage);
+            continue;
           }
-        }
-      }
-    }
-    for (int m = chain; m >= 0; m = plan[m].next) {
-      const int skip = a.share ? plan[m].len / size : 0;
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (u >= n) continue;
-        const int page = a.fresh[m * a.fresh_stride + jj[u] - skip];
-        const bool there = page >= 0 && page < a.c.pages;
-        if (!there) tell(a.status, kDevBadPage);
-        if (there && live[u]) {
-          const long long o = ofv[u] ? page * a.c.v_page + hd[u] * a.c.v_head + row[u] * a.c.v_row
-                                     : page * a.c.k_page + hd[u] * a.c.k_head + row[u] * a.c.k_row;
-          *reinterpret_cast<uint4*>((uint16_t*)(ofv[u] ? a.c.v : a.c.k) + o + ch * 8) = v[u];
+          for (int u = 0; u < kAhead; ++u)
+            if (b + u < n && (b + u) * RPW < left) *reinterpret_cast<uint4*>(base + to * s_page + (b + u) * RPW * s_row) = v[u];
         }
       }
     }
@@ -217,29 +178,35 @@ __global__ void __launch_bounds__(32 * kForkWarps, kForkCtas) kv_fork_kernel(con
 }
 
 // -------------------------------------------------------------- compaction
-// Key keep[j] of a sequence moves to place first + j, in place: since keep[j] >=
-// first + j, a row is read before, or in the same step as, any row whose place
-// it is.  A block moves a slice of channels of one sequence, head and K or V, in
-// steps of many rows: the rows of step c + 1 are asked for, a barrier says that
-// those of step c are all in registers, and they are stored.  What a later step
-// reads lies behind all places that earlier ones write.
-constexpr int kMoveWarps = 16;
+// Key keep[j] of a sequence moves to place first + j, in place; keep ascends.
+// Blocks share a sequence, head and K or V in one of two ways:
+//  - where no key's old place is a new one (keep[0] >= first + n, as when a window
+//    rolls on by more than its length), each takes its part of the keys, in any
+//    order;
+//  - otherwise each takes a slice of channels of all keys and goes through them in
+//    steps of many rows.  Since keep[j] >= first + j, what a later step reads lies
+//    behind all places that earlier ones write: the rows of step c + 1 are asked
+//    for, a barrier says that those of step c are all read, and they are stored.
+constexpr int kMoveWarps = 4, kMoveCtas = 8;
 constexpr int kMoveAhead = 4;  // row groups of a warp in a step
 
-struct Move {  // of the row that this lane looks up
+// Of the row that this lane looks up:
+struct Ask {
+  int from, to, pf, pt;  // places (to < 0: nothing moves) and the numbers of their pages
+};
+struct Move {
   long long from, to;  // in elements; from < 0: none
 };
 
-__global__ void __launch_bounds__(32 * kMoveWarps) kv_compact_kernel(const __grid_constant__ CompactArgs a, const int slice) {
+__global__ void __launch_bounds__(32 * kMoveWarps, kMoveCtas)
+    kv_compact_kernel(const __grid_constant__ CompactArgs a, const int blocks, const int ordered) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int CH = a.c.D / 8, slices = (CH + slice - 1) / slice;
-  const int part = blockIdx.y % slices, plane = blockIdx.y / slices;
+  const int part = blockIdx.y % blocks, plane = blockIdx.y / blocks;
   const bool ofv = plane >= a.c.heads;
   const int h = ofv ? plane - a.c.heads : plane, size = a.c.page_size;
   const long long s_page = ofv ? a.c.v_page : a.c.k_page, s_row = ofv ? a.c.v_row : a.c.k_row;
-  uint16_t* const base = (uint16_t*)(ofv ? a.c.v : a.c.k) + h * (ofv ? a.c.v_head : a.c.k_head) + part * slice * 8;
 
   int k0, n, first;
   const long long room = (long long)a.b.max_pages * size;
@@ -255,26 +222,49 @@ __global__ void __launch_bounds__(32 * kMoveWarps) kv_compact_kernel(const __gri
   const int* table = a.b.pages + b * a.b.page_stride;
   const int* keep = a.keep + k0;
 
+  const bool apart = blocks > 1 && keep[0] >= first && keep[0] - first >= n;
+  if (!apart && part >= ordered) return;
+  const int CH = a.c.D / 8;                                              // 16-byte pieces of a row
+  const int slice = apart ? CH : (CH + ordered - 1) / ordered, c0 = apart ? 0 : part * slice;  // this block's
+  if (c0 >= CH) return;
+  uint16_t* const base = (uint16_t*)(ofv ? a.c.v : a.c.k) + h * (ofv ? a.c.v_head : a.c.k_head) + c0 * 8;
   const int RPW = min(8, 32 / slice);        // rows of a group
   const int look = kMoveAhead * RPW;         // rows that a warp looks up for a step, one a lane
   const int step = kMoveWarps * look;
   const int sub = lane / slice, ch = lane - sub * slice;
-  const bool busy = sub < RPW && part * slice + ch < CH;
-  auto lookup = [&](int c) {
+  const bool busy = sub < RPW && c0 + ch < CH;
+  // What a step needs is asked for ahead of it: which keys three steps, their pages two, the keys themselves one.
+  auto key = [&](int c) {  // of the lane's row, -1 for one that is left out
     const uint32_t j = (uint32_t)c * step + warp * look + lane;
-    Move m{-1, 0};
+    if (lane >= look || j >= (uint32_t)n) return -1;
+    const int from = keep[j], before = j > 0 ? keep[j - 1] : -1;
+    return from > before && from >= first + (apart ? n : (int)j) && from < room ? from : -1;
+  };
+  auto pages = [&](int c, int from) {
+    const uint32_t j = (uint32_t)c * step + warp * look + lane;
+    Ask q{from, -1, 0, 0};
     if (lane < look && j < (uint32_t)n) {
-      const int from = keep[j], to = first + (int)j;
-      if (from < to || from >= room) {
+      q.to = first + (int)j;
+      if (from < 0) {
         tell(a.b.status, kDevBadLength);
-      } else if (from != to) {
-        const int pf = kv_page(table, from, size, a.c.pages), pt = kv_page(table, to, size, a.c.pages);
-        if (pf < 0 || pt < 0) {
-          tell(a.b.status, kDevBadPage);
-        } else {
-          m.from = pf * s_page + from % size * s_row;
-          m.to = pt * s_page + to % size * s_row;
-        }
+        q.to = -1;
+      } else if (from == q.to) {
+        q.to = -1;
+      } else {
+        q.pf = table[from / size];
+        q.pt = table[q.to / size];
+      }
+    }
+    return q;
+  };
+  auto rows = [&](const Ask& q) {
+    Move m{-1, 0};
+    if (q.to >= 0) {
+      if (q.pf < 0 || q.pf >= a.c.pages || q.pt < 0 || q.pt >= a.c.pages) {
+        tell(a.b.status, kDevBadPage);
+      } else {
+        m.from = q.pf * s_page + q.from % size * s_row;
+        m.to = q.pt * s_page + q.to % size * s_row;
       }
     }
     return m;
@@ -295,19 +285,27 @@ __global__ void __launch_bounds__(32 * kMoveWarps) kv_compact_kernel(const __gri
     }
   };
   const int steps = (n + step - 1) / step;
+  // this block's: every `blocks`-th, or all
+  const int beg = apart ? part : 0, by = apart ? blocks : 1;
+  if (beg >= steps) return;
   uint4 v0[kMoveAhead], v1[kMoveAhead];
-  Move m0 = lookup(0), m1;
+  Move m0 = rows(pages(beg, key(beg))), m1;
   load(m0, v0);
-  for (int c = 0; c < steps; c += 2) {
-    m1 = lookup(c + 1);
-    load(m1, v1);
-    __syncthreads();
-    store(m0, v0);
-    if (c + 1 >= steps) break;
-    m0 = lookup(c + 2);
-    load(m0, v0);
-    __syncthreads();
-    store(m1, v1);
+  Ask next = pages(beg + by, key(beg + by));
+  int then = key(beg + 2 * by);
+  // stores step c, whose rows are on their way, and asks for those of step c + by
+  auto turn = [&](int c, const Move& mine, const uint4 (&v)[kMoveAhead], Move& other, uint4 (&w)[kMoveAhead]) {
+    other = rows(next);
+    load(other, w);
+    next = pages(c + 2 * by, then);
+    then = key(c + 3 * by);
+    if (!apart) __syncthreads();
+    store(mine, v);
+  };
+  for (int c = beg; c < steps; c += 2 * by) {
+    turn(c, m0, v0, m1, v1);
+    if (c + by >= steps) break;
+    turn(c + by, m1, v1, m0, v0);
   }
 }
 
@@ -329,10 +327,13 @@ cudaError_t launch_kv_fork(const ForkArgs& a, int sms, cudaStream_t s) {
 }
 
 cudaError_t launch_kv_compact(const CompactArgs& a, int sms, cudaStream_t s) {
-  // Slices of 64 bytes or more, two blocks for each SM if there are as many.
+  // Three times as many blocks as are resident, so that ragged sequences even out (13 of 500 to 1900 kept keys take 24.6 us,
+  // 27.8 with one time), fewer for a call of few keys; slices of 64 bytes or more.
   const int CH = a.c.D / 8;
-  int slice = CH;
-  while (slice > 4 && (long long)a.b.B * 2 * a.c.heads * ((CH + slice - 1) / slice) < 2 * sms) slice = (slice + 1) / 2;
+  const long long planes = 2LL * a.c.heads * a.b.B, step = kMoveWarps * kMoveAhead * std::max(1, 32 / CH);
+  const long long most = std::max(1LL, a.b.T / (a.b.B * step));  // steps of a sequence on average
+  const int blocks = (int)std::max(1LL, std::min(most, (3LL * kMoveCtas * sms + planes - 1) / planes));
+  const int ordered = std::min(blocks, std::max(1, CH / 4));
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -340,9 +341,9 @@ cudaError_t launch_kv_compact(const CompactArgs& a, int sms, cudaStream_t s) {
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   cfg.stream = s;
-  cfg.gridDim = dim3(a.b.B, 2 * a.c.heads * ((CH + slice - 1) / slice));
+  cfg.gridDim = dim3(a.b.B, 2 * a.c.heads * blocks);
   cfg.blockDim = dim3(32 * kMoveWarps);
-  return cudaLaunchKernelEx(&cfg, kv_compact_kernel, a, slice);
+  return cudaLaunchKernelEx(&cfg, kv_compact_kernel, a, blocks, ordered);
 }
 
 }  // namespace wan

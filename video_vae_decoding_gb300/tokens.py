@@ -621,9 +621,10 @@ def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor
     j] moves to place first[b] + j, all as if at once.  So the accepted drafts of a
     tree are kept (first: the keys ahead of the drafts), a window rolls on, or a
     choice of keys stays.  first [sequences], keep [n], cu_keep [sequences + 1]:
-    int32.  A key moves ahead or stays: others (keep < first + j, or without a
-    page) are left out and leave a code in `status`, as do sequences whose ranges
-    are none.  Pages behind the new lengths are the caller's again."""
+    int32.  A sequence's numbers ascend, from first[b] or later on.  Where they do
+    not, or a page is none, some of its keys are left out and a code is left in
+    `status`, as for sequences whose ranges are none.  Pages behind the new lengths
+    are the caller's again."""
     short = _short or _short_way()
     if stream is None:
         got = short.compact(k_cache, v_cache, pages, first, keep, cu_keep, lengths, status)
