@@ -387,7 +387,7 @@ struct alignas(16) Cursor {
 // values must not meet a weight of zero.  Such values leave the block here (V in
 // `count` slots from the ring's number `at` on, read by a half's 128 threads), and
 // the rows that see them get them at the end.  Where both halves' products read the
-// slot, half 0 does this for both, ahead of its weights and so of either product: no
+// slot, half 0 does this for both, ahead of its arrival and so of either product: no
 // product reads a value while it changes.  Not inline: the softmax's loop needs
 // the registers (two chunks of 1300 causal tokens of 48 heads 159 us, 162 inline).
 template <typename T, int DP>
@@ -1021,14 +1021,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 32; ++e)
                 if (32 * c + e >= p0 && 32 * c + e < p0 + per) x[c][e] = -INFINITY;
           }
-          if (hidden) {
-            // The lap of the ring before this block's has to be known to be there: the P V before the last one of this
-            // half is, which is enough where both halves take all blocks and a block one slot.
-            if (ok && i > 0 && (split || kOne)) ok = wait_phase(&o_done[bar_of(half, c - 1)], phase_of(c - 1), err, kDevTimeoutAccum);
-            ok = ok && clean_values<T, DP>(sV, full + SK, (it + o - j0) * pv, pv, hrow, j, run, err);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-          }
         }
         float mx[4];
 #pragma unroll
@@ -1083,6 +1075,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st16(myP + 16 * q, p);
         }
         tmem_st_wait();
+        if (__builtin_expect(hidden, 0)) {
+          // Behind the weights, when S has left the registers, and ahead of the barrier that the products wait for.  The lap of
+          // the ring before this block's has to be known to be there: the P V before the last one of this half is, which is
+          // enough where both halves take all blocks and a block one slot.
+          if (ok && i > 0 && (split || kOne)) ok = wait_phase(&o_done[bar_of(half, c - 1)], phase_of(c - 1), err, kDevTimeoutAccum);
+          ok = ok && clean_values<T, DP>(sV, full + SK, (it + o - j0) * pv, pv, hrow, j, run, err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
         tc_fence_before();
         mbar_arrive(smem_u32(&p_full[bar_of(half, c)]));
         s_there = ask_phase(&s_full[half], (n0 + i + 1) & 1);
