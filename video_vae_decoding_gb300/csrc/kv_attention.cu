@@ -141,7 +141,7 @@ struct Weights<__half> {
 // Tiles of a sequence on the line: row tiles x heads x key tiles.
 struct Tiles {
   int key_tiles;
-  long long all;
+  long long runs, all;  // row tiles of all heads, their key tiles
 };
 // With X (rows see by their place) a row tile's key tiles are those that some row of it sees, numbered without the
 // gap between the first keys and the window; as many as the widest row tile can have stand on the line, the others
@@ -157,8 +157,67 @@ __device__ __forceinline__ Tiles tiles_of(const AttnArgs& a, const Seq& s) {
     const uint32_t most = (a.span + reach) / kKeys + 2 + ((uint32_t)a.sinks + kKeys - 1) / kKeys;
     t.key_tiles = (int)min((uint32_t)t.key_tiles, most);
   }
-  t.all = ((long long)s.n * a.group + kRows - 1) / kRows * a.c.heads * t.key_tiles;
+  t.runs = ((long long)s.n * a.group + kRows - 1) / kRows * a.c.heads;
+  t.all = t.runs * t.key_tiles;
   return t;
+}
+
+// A call of few tiles, cut so that no warp has more than one run: one that ends a row tile and starts another takes 5 us
+// longer than the others, and the call with it (26 drafts of 16 heads against 2000 keys 23.9 us by the line, 21.3 so; 8
+// drafts 18.3 and 14.8; 32 single tokens with windows of 300 keys 23.2 and 21.1; 4 of 500 keys 11.7 and 12.3).  Each row
+// tile is cut into equal parts of at most `size` tiles, the least size for which there are warps enough; false if there are
+// more than kSmall tiles a warp, where a run's start counts less, or more than 32 sequences.  All warps find the same.
+constexpr int kSmall = 12;
+__device__ __forceinline__ float inverse(int d) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"((float)d));
+  return r;
+}
+// x / d by d's inverse, of results below 2^20 (which the product is off by less than one from)
+__device__ __forceinline__ int part_of(int x, int d, float inv) {
+  int q = (int)((float)x * inv);
+  if (q * d > x) --q;
+  if ((q + 1) * d <= x) ++q;
+  return q;
+}
+__device__ __forceinline__ bool cut_tiles(const AttnArgs& a, int me, int G, Piece* p, int* parts) {
+  if (a.b.B > 32) return false;
+  const int lane = threadIdx.x & 31;
+  const long long most = (kSmall + 1) * G;  // (a sequence's numbers are cut to it: sums of 32 then fit 32 bits)
+  Tiles t{0, 0, 0};
+  if (lane < a.b.B) t = tiles_of<true>(a, sequence(a, lane, false));
+  const int total = (int)__reduce_add_sync(0xffffffffu, (uint32_t)min(t.all, most));
+  if (total > kSmall * G) return false;
+  const int runs = t.key_tiles > 0 ? (int)t.runs : 0;
+  int size = max(1, (int)((float)total * inverse(G))), mine = 0, all;  // (one too few is one more round)
+  for (;; ++size) {
+    mine = runs * part_of(t.key_tiles + size - 1, size, inverse(size));
+    all = (int)__reduce_add_sync(0xffffffffu, (uint32_t)mine);
+    if (all <= G) break;
+    if (size > 2 * kSmall) return false;  // (more row tiles than warps)
+  }
+  int incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  p->beg = p->end = 0;
+  p->live = all;
+  p->size = size;
+  p->longer = 0;
+  p->b = 0;
+  p->at = 0;
+  if (me >= all) return true;
+  p->b = __ffs(__ballot_sync(0xffffffffu, me >= incl - mine && me < incl)) - 1;
+  const int q = me - __shfl_sync(0xffffffffu, incl - mine, p->b);
+  const int n = __shfl_sync(0xffffffffu, t.key_tiles, p->b), of = part_of(n + size - 1, size, inverse(size));
+  const float inv = inverse(of);
+  const int tile = part_of(q, of, inv), part = q - tile * of, t0 = part_of(n * part, of, inv), t1 = part_of(n * (part + 1), of, inv);
+  *parts = of;
+  p->at = (long long)tile * n + t0;
+  p->end = t1 - t0;
+  return true;
 }
 
 struct Space {  // the workspace: per piece an Open and two parts (0: a row tile's later keys, 1: its first ones)
@@ -200,8 +259,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // for what came before on the stream
 
-  const Piece pc = cut_line<kWarps, kWarps>(a.b.B, kLeast, s_line,
-                                            [&](int b) { return tiles_of<X>(a, sequence(a, b, false)).all; });
+  // The line is cut as it comes, or (with X) each of few row tiles for itself: parts of it, else 0.
+  int parts = 0;
+  Piece pc;
+  if (!X || !cut_tiles(a, me, gridDim.x * kWarps, &pc, &parts))
+    pc = cut_line<kWarps, kWarps>(a.b.B, kLeast, s_line, [&](int b) { return tiles_of<X>(a, sequence(a, b, false)).all; });
   if (lane == 0) ws.open[me].parts = 0;
   int b = pc.b;
   long long at = pc.at;
@@ -587,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
     }
     if (!whole && kt0 == 0 && lane == 0) {
       const long long last = line + tl.key_tiles - 1;  // the row tile's last tile: its piece is the last part's
-      ws.open[me] = Open{pc.holder(last) - me, h, row0, cnt, s, 0};
+      ws.open[me] = Open{parts ? parts - 1 : pc.holder(last) - me, h, row0, cnt, s, 0};
     }
     __syncwarp();
     at += kt1 - kt0;

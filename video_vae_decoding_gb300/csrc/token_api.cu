@@ -111,16 +111,18 @@ wan_status sm_count(int* n) {
 constexpr int kChunkRows = 64;
 constexpr double kChunkWork = 6e5;
 
-// Rows that see by their place: from 24 rows on, by the keys that a window leaves.  us with split / many tokens: a tree of 8
-// drafts of 4 heads a key head against 2000 keys of 8 heads 22 / 23, of 32 sequences and 3000 keys 151 / 101; 16 drafts of
-// one head 94 / 100, 32 152 / 101; 100 tokens of 4 sequences with a window of 100 keys 25 / 28, of 1000 46 / 29.
-constexpr int kMaskedRows = 24;
+// Rows that see by their place: from 20 rows on, and by the keys that a window leaves.  us with split / many tokens: a tree of
+// 5 drafts of 4 heads a key head against 4000 keys, 8 sequences of 8 heads, 62 / 51; of 16 drafts of one head against 3000
+// keys, 32 sequences, 94 / 100, of 32 drafts 152 / 101; one of 26 drafts of 16 heads against 2000 keys 21 / 24, of 48
+// 25 / 25, of 64 30 / 25; 100 tokens of 4 sequences with a window of 1000 keys 46 / 29.
+constexpr int kMaskedRows = 20;
+constexpr double kMaskedWork = 1.3e6;
 
 bool chunk_rows(const AttnArgs& a, ChunkGeo* g) {
   double keys = (double)a.b.max_pages * a.c.page_size;
   if (a.mask == kMaskWindow) keys = std::min(keys, (double)a.span + a.sinks);
   return (int64_t)a.b.T * a.group >= (int64_t)(a.mask == kMaskRanges ? kChunkRows : kMaskedRows) * a.b.B &&
-         (double)a.b.T * a.q_heads * keys >= kChunkWork && kv_chunk_geometry(a, g);
+         (double)a.b.T * a.q_heads * keys >= (a.mask == kMaskRanges ? kChunkWork : kMaskedWork) && kv_chunk_geometry(a, g);
 }
 int64_t workspace_of(const AttnArgs& a, bool chunk, int sms) {
   const int64_t split = kv_attention_workspace(a, sms);
