@@ -89,6 +89,8 @@ WINDOW = [
     ([3000, 20], [2, 20], 4, 2, 128, 256, 10, 700, 100), ([2600], [300], 2, 1, 64, 390, 90, 200, 1),
     ([4000, 700], [200, 150], 1, 1, 256, 256, 500, 300, 1), ([1513], [400], 1, 2, 192, 24, 64, 1000, 7),
     ([900], [300], 1, 16, 144, 8, 40, 5, 1), ([1290], [400], 2, 2, 128, 16, 2, 130, 129),
+    ([600], [200], 1, 2, 64, 8, 100, 37, 1), ([600, 250], [100, 200], 2, 2, 128, 128, 50, 130, 1), ([3000], [300], 1, 1, 128, 16, 1000, 16, 1),
+    ([900], [250], 1, 4, 256, 32, 5, 70, 33), ([700], [260], 1, 1, 64, 40, 90, 41, 1),
 ]
 
 

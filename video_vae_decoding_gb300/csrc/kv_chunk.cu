@@ -259,10 +259,12 @@ struct RowTile {
   int b, rt;  // b < 0: none
   int k0, k1;
 };
-// With X (rows see by their place): its rows see [0, c) and [lo, hi); k0 and k1 count the blocks of both without the
-// `skip` ones between them.
+// With X (rows see by their place) its rows see the first keys and a window.  What holds them is taken together: units (pages,
+// or the blocks of a longer page) 0 .. firsts - 1, and `skip` units further on the rest of `units`; a block takes as many
+// units as it has pages.  (Blocks of the window alone and of the first keys alone took 103 us for ragged prompts with windows of
+// 1000 keys and pages of 32.)
 struct SightTile : RowTile {
-  int c, lo, hi, skip;
+  int firsts, skip, units, pad;
 };
 template <bool X>
 using Tile = std::conditional_t<X, SightTile, RowTile>;
@@ -277,8 +279,11 @@ __host__ __device__ inline long long row_tiles(const AttnArgs& a) {
 // causal tokens of 48 heads take 184 us with 30 for a run, 173 with 45, 162 with 60, 164 with 80.  (A smaller tile does
 // half the arithmetic, but asks for K and V as fast as a larger one would at twice the speed.)
 constexpr int kPairUnits = 5, kSingleUnits = 4, kRunUnits = 60;
+constexpr int kSightSingleUnits = 3;  // with X (trees of up to 47 drafts 40 us with 4, 38 with 3)
+template <bool X>
 __device__ __forceinline__ int tile_weight(const AttnArgs& a, const Seq& s, int rt) {
-  return a.c.D <= 128 && s.n * a.group - rt * tile_rows(a.c.D) <= kHalfRows ? kSingleUnits : kPairUnits;
+  const bool single = a.c.D <= 128 && s.n * a.group - rt * tile_rows(a.c.D) <= kHalfRows;
+  return !single ? kPairUnits : X ? kSightSingleUnits : kSingleUnits;
 }
 
 constexpr int kFaultBytes = 16;
@@ -333,16 +338,16 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
       // a window moves on with its tokens: the first one's begins, the last one's ends first keys and window of the tile
       const int row0 = t.rt * tile;
       const Sight from = sight(a, s, row0 / a.group), to = sight(a, s, (min(row0 + tile, s.n * a.group) - 1) / a.group);
-      t.c = to.c, t.lo = from.lo, t.hi = a.mask == kMaskTree ? s.len : to.hi;
-      if (t.lo <= t.c) t.c = t.lo = 0;
-      t.k0 = block_of_key(geo, a.c.page_size, t.lo);
-      t.k1 = block_of_key(geo, a.c.page_size, t.hi - 1) + 1;
-      if (t.c > 0) {
-        const int firsts = block_of_key(geo, a.c.page_size, t.c - 1) + 1;
-        t.skip = max(t.k0, firsts) - firsts;
-        t.k0 = 0;
-        t.k1 -= t.skip;
-      }
+      int c = to.c, lo = from.lo;
+      const int hi = a.mask == kMaskTree ? s.len : to.hi;
+      if (lo <= c) c = lo = 0;
+      const bool pages = geo.parts == 1;
+      auto unit = [&](int key) { return pages ? key / a.c.page_size : block_of_key(geo, a.c.page_size, key); };
+      t.firsts = c > 0 ? unit(c - 1) + 1 : 0;
+      t.skip = max(unit(lo), t.firsts) - t.firsts;
+      t.units = unit(hi - 1) + 1 - t.skip;
+      t.k0 = 0;
+      t.k1 = pages ? (t.units + geo.pages - 1) / geo.pages : t.units;
     } else if (a.ranges) {
       int lo = 0x7fffffff, hi = 0;
       const int row0 = t.rt * tile, last = (min(row0 + tile, s.n * a.group) - 1) / a.group;
@@ -371,9 +376,8 @@ struct alignas(16) Run {
   int blocks;                // k1 - k0; 0: the piece has no more runs
   int all_lo[2], all_hi[2];  // per half: keys that every row sees
   int odd_lo, odd_hi;        // blocks whose values were cleaned (below)
-  // With X the run's blocks are numbered as its tile's are: number o is block o, and from `firsts` on block o + skip;
-  // keys that some row sees are on pages [0, p_first) and [p_lo, p_hi), and all rows of a half see [0, all_c) too.
-  int firsts, skip, p_first, p_lo, p_hi, all_c[2];
+  int firsts, skip, units;   // with X: the tile's
+  int all_c[2];              // and all rows of a half see [0, all_c) too
 };
 
 // Where thread 0 stands on the line (in shared memory: the softmax has no register to spare).
@@ -388,10 +392,11 @@ struct alignas(16) Cursor {
 // `count` slots from the ring's number `at` on, read by a half's 128 threads), and
 // the rows that see them get them at the end.  Where both halves' products read the
 // slot, half 0 does this for both, ahead of its arrival and so of either product: no
-// product reads a value while it changes.  Not inline: the softmax's loop needs
-// the registers (two chunks of 1300 causal tokens of 48 heads 159 us, 162 inline).
+// product reads a value while it changes.  Not inline but for windows and trees at
+// heads of 64: the softmax's loop needs the registers (two chunks of 1300 causal
+// tokens of 48 heads 159 us, 162 inline; ragged windows at heads of 64 90 and 85).
 template <typename T, int DP>
-__device__ __noinline__ bool clean_values(uint8_t* ring, uint64_t* full, int at, int count, int thread, int block, Run* run,
+__device__ __forceinline__ bool clean_values(uint8_t* ring, uint64_t* full, int at, int count, int thread, int block, Run* run,
                                           int* err) {
   using C = Cfg<DP>;
   constexpr int SV = C::kValSlots;
@@ -418,6 +423,11 @@ __device__ __noinline__ bool clean_values(uint8_t* ring, uint64_t* full, int at,
   }
   fence_proxy_async_smem();
   return true;
+}
+template <typename T, int DP>
+__device__ __noinline__ bool clean_values_apart(uint8_t* ring, uint64_t* full, int at, int count, int thread, int block, Run* run,
+                                                int* err) {
+  return clean_values<T, DP>(ring, full, at, count, thread, block, run, err);
 }
 
 template <typename T, int DP, bool X>
@@ -495,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto units = [&](const RowTile& t, int w) { return (long long)(kRunUnits + w * (t.k1 - t.k0)); };
   const Piece cut = cut_line<kThreads / 32, 1>((int)row_tiles(a), kLeast, reinterpret_cast<long long*>(half_ml), [&](int i) {
     const Tile<X> t = ws.tiles[i];
-    return t.b < 0 ? 0 : a.c.heads * units(t, tile_weight(a, sequence(a, t.b, false), t.rt));
+    return t.b < 0 ? 0 : a.c.heads * units(t, tile_weight<X>(a, sequence(a, t.b, false), t.rt));
   });
   tc_fence_before();
   __syncthreads();
@@ -526,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (;;) {
         if (t.b >= 0) {
           s = sequence(a, t.b, false);
-          w = tile_weight(a, s, t.rt);
+          w = tile_weight<X>(a, s, t.rt);
           n = units(t, w);
           if (at < a.c.heads * n) break;
           at -= a.c.heads * n;
@@ -554,11 +564,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       run->odd_hi = -1;
       if constexpr (X) {
         run->all_c[0] = run->all_c[1] = 0x7fffffff;
-        run->firsts = t.c > 0 ? block_of_key(geo, page_size, t.c - 1) + 1 : 0;
+        run->firsts = t.firsts;
         run->skip = t.skip;
-        run->p_first = (t.c + page_size - 1) / page_size;
-        run->p_lo = t.lo / page_size;
-        run->p_hi = (t.hi - 1) / page_size + 1;
+        run->units = t.units;
       }
       if (run->k0 == t.k0 && run->k1 > t.k0 && run->k1 < t.k1)
         ws.open[me] = Open{pc.holder(line + n - u0 - 1) - me, h, run->row0, run->cnt, s, 0};
@@ -579,10 +587,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
 
-  // Q and the first V of the next run come while this one ends: q in its room from the last Q K on (by warp 1), where the
-  // halves do not need that for their sums and its rows can be copied as they are.  (64 drafts of 24 sequences, heads of
-  // 128, take 132 us so, 135 without; ragged causal chunks at heads of 64 take 104 and 91: too little time to fill.)
-  constexpr bool kAheadOfRun = DP > 64;
+  // The first V of the next run, and q, come while this one ends: q in its room from the last Q K on (by warp 1), where the
+  // halves do not need that for their sums and its rows can be copied as they are.  880 tokens against 27,280 keys take 176 us
+  // with q ahead, 190 without; with X a window of 9 latent frames 102 and 89; at heads of 64 ragged causal chunks 104 and 91
+  // (too little time to fill).
+  constexpr bool kValuesAhead = DP > 64, kAheadOfRun = DP > 64 && !X;
   const bool q_plain = a.scale_log2 > 0.f && ((uintptr_t)a.q & 15) == 0 && (a.q_t & 7) == 0 && (a.q_h & 7) == 0;
   bool q_came = false;
   // where row `row` of a run has its q (-1: the tile has no such row)
@@ -673,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // blocks [n0, n1) of a run whose first block is the it-th
     auto loads = [&](auto which, const Run* run, int it, int n0, int n1) {
       constexpr bool ofK = decltype(which)::value;
-      const int h = run->h, o0 = run->k0 + n0, j0 = X && o0 >= run->firsts ? o0 + run->skip : o0;
+      const int h = run->h, o0 = run->k0 + n0, j0 = X && geo.parts > 1 && o0 >= run->firsts ? o0 + run->skip : o0;
       const CUtensorMap* map = ofK ? &mapK : &mapV;
       const int* table = a.b.pages + run->b * a.b.page_stride;
       const int held = (run->s.len + page_size - 1) / page_size;  // pages of the sequence
@@ -686,27 +695,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       int idx = geo.parts == 1 ? j0 * geo.pages + lane : j0 / geo.parts, part = geo.parts == 1 ? 0 : j0 - idx * geo.parts;
       int idx2 = idx, part2 = part;
       const int wide = lane < geo.pages ? held : 0;
-      // with X: blocks to the one behind the first keys, and where that one is
-      int left = 0, left2 = 0, idx_to = 0, part_to = 0, p_first = 0, p_lo = 0, p_hi = 0;
+      // With X the lane's page is a unit: its place in the table comes from it.  Of a longer page: blocks to the one behind
+      // the first keys, and where that one is.
+      int left = 0, left2 = 0, idx_to = 0, part_to = 0;
+      const int firsts = X ? run->firsts : 0, skip = X ? run->skip : 0, limit = X && geo.parts == 1 ? (wide ? run->units : 0) : wide;
       if constexpr (X) {
-        p_first = run->p_first, p_lo = run->p_lo, p_hi = run->p_hi;
-        left = left2 = run->firsts - o0;
-        if (left > 0) {
-          const int to = run->firsts + run->skip;
-          idx_to = geo.parts == 1 ? to * geo.pages + lane : to / geo.parts;
-          part_to = geo.parts == 1 ? 0 : to - idx_to * geo.parts;
+        left = left2 = firsts - o0;
+        if (geo.parts > 1 && left > 0) {
+          idx_to = (firsts + skip) / geo.parts;
+          part_to = firsts + skip - idx_to * geo.parts;
         }
       }
-      // whether some row sees a key of page i of the sequence: its number is looked at
-      auto wanted = [&](int i) { return !X || i < p_first || (i >= p_lo && i < p_hi); };
       auto advance = [&](int& i, int& p, int& left) {
-        if (X && --left == 0) i = idx_to, p = part_to;
-        else if (geo.parts == 1) i += geo.pages;
+        if (geo.parts == 1) i += geo.pages;
+        else if (X && --left == 0) i = idx_to, p = part_to;
         else if (++p == geo.parts) p = 0, ++i;
       };
+      auto place = [&](int i) { return X && geo.parts == 1 && i >= firsts ? i + skip : i; };
       auto entry = [&](int n) {
-        // past the cache, which reads as zeros
-        const int e = n < n1 && idx2 < wide && wanted(idx2) ? table[idx2] : (int)a.c.pages;
+        const int e = n < n1 && idx2 < limit ? table[place(idx2)] : (int)a.c.pages;  // past the cache, which reads as zeros
         advance(idx2, part2, left2);
         return e;
       };
@@ -716,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = n0; n < n1 && ok; ++n) {
         const int after = entry(n + 2);
         const int off = part * kBlock;
-        const bool none = idx < wide && wanted(idx) && (page < 0 || page >= a.c.pages);
+        const bool none = idx < limit && (page < 0 || page >= a.c.pages);
         advance(idx, part, left);
         if (none) {
           page = (int)a.c.pages;
@@ -769,14 +776,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && next->blocks > 0) loads(std::true_type(), next, it + nb, 0, min(next->blocks, kAhead));
     } else if (warp == 3) {
       // as with K: the slots that V of the next run's first blocks takes held blocks whose products need nothing of this warp
-      const int kAhead = kAheadOfRun ? SV / pv : 0;
+      const int kAhead = kValuesAhead ? SV / pv : 0;
       loads(std::false_type(), run, it, r > 0 ? min(nb, kAhead) : 0, nb);
       const Run* const next = &runs[(r + 1) & 1];
-      if (kAheadOfRun && ok && !__all_sync(0xffffffffu, wait_phase(told, r & 1, err, kDevTimeoutFull))) {
+      if (kValuesAhead && ok && !__all_sync(0xffffffffu, wait_phase(told, r & 1, err, kDevTimeoutFull))) {
         ok = false;
         *stop = 1;
       }
-      if (kAheadOfRun && ok && next->blocks > 0) loads(std::false_type(), next, it + nb, 0, min(next->blocks, kAhead));
+      if (kValuesAhead && ok && next->blocks > 0) loads(std::false_type(), next, it + nb, 0, min(next->blocks, kAhead));
     } else if (warp == 1 || warp == 2) {
       // ------------------------------------------------- products: Q K, and P V
       // A whole warp walks the steps (what it computes stays in uniform
@@ -909,16 +916,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (mine > 0 && !(geo.parts == 1 && tails)) {
         const int p_lo = turns && cleans ? max(all_lo, run->all_lo[1]) : all_lo;
         const int p_hi = turns && cleans ? min(all_hi, run->all_hi[1]) : all_hi;
-        plain_lo = p_lo > 0 ? block_of_key(geo, page_size, p_lo - 1) + 1 : 0;
-        plain_hi = block_of_key(geo, page_size, min(p_hi, s.len));
-        if constexpr (X) {
-          const int c = turns && cleans ? min(run->all_c[0], run->all_c[1]) : run->all_c[half];
-          plain_first = block_of_key(geo, page_size, min(c, s.len));
+        if (X && geo.parts == 1) {
+          const int c = min(turns && cleans ? min(run->all_c[0], run->all_c[1]) : run->all_c[half], s.len);
+          plain_lo = max((p_lo + page_size - 1) / page_size - run->skip, run->firsts);
+          plain_lo = (plain_lo + geo.pages - 1) / geo.pages;
+          plain_hi = max(min(p_hi, s.len) / page_size - run->skip, 0) / geo.pages;
+          plain_first = c / page_size / geo.pages;
+        } else {
+          plain_lo = p_lo > 0 ? block_of_key(geo, page_size, p_lo - 1) + 1 : 0;
+          plain_hi = block_of_key(geo, page_size, min(p_hi, s.len));
+          if constexpr (X) {
+            const int c = turns && cleans ? min(run->all_c[0], run->all_c[1]) : run->all_c[half];
+            plain_first = block_of_key(geo, page_size, min(c, s.len));
+          }
         }
       }
-      // with X, the block at hand: number j0 (+ 1) of the tile's, and the first number behind the gap if that is still ahead
+      // with X, the block at hand: the tile's number j0 (+ 1) of it, in a longer page its own, and the first number behind the gap
+      // if that is still ahead
       int at = j0 + (split ? half : 0), gap = 0x7fffffff;
-      if constexpr (X) {
+      if (X && geo.parts > 1) {
         if (at >= run->firsts) at += run->skip;
         else gap = run->firsts;
       }
@@ -942,15 +958,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool hidden = false;  // some row does not see some key of the block, whose values this half cleans
         if constexpr (X) {
           if (__builtin_expect(!plain, 0)) {
-            int base = 0, rows = page_size - (geo.parts - 1) * kBlock;  // inside: the last part of a page that all see
+            // columns [0, at_c) are keys from base_c on, those behind them from base on (both less the column)
+            int base_c = 0, base = 0, at_c = 0, rows = page_size - (geo.parts - 1) * kBlock;  // inside: the last part of a page
             if (!inside) {
-              block_keys(geo, page_size, j, &base, &rows);
+              if (geo.parts == 1) {
+                rows = geo.pages * page_size;
+                base_c = j * rows;
+                base = base_c + run->skip * page_size;
+                at_c = min(max((run->firsts - j * geo.pages) * page_size, 0), rows);
+              } else {
+                block_keys(geo, page_size, j, &base, &rows);
+              }
               const int c_all = min(run->all_c[0], run->all_c[1]), lo_all = max(run->all_lo[0], run->all_lo[1]),
                         hi_all = min(run->all_hi[0], run->all_hi[1]);
-              hidden = cleans && base + rows > c_all && (base < lo_all || base + rows > hi_all);
+              auto all_see = [&](int k0, int k1) { return k0 >= k1 || k1 <= c_all || (k0 >= lo_all && k1 <= hi_all); };
+              hidden = cleans && !(all_see(base_c, base_c + at_c) && all_see(base + at_c, base + rows));
             }
 #pragma unroll
-            for (int w = 0; w < 4; ++w) vis[w] = inside ? ~0u : sight_bits(Sight{first_keys, lo, hi}, base + 32 * w);
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t firsts = low_bits(at_c - 32 * w);
+              const Sight v{first_keys, lo, hi};
+              vis[w] = inside ? ~0u : (sight_bits(v, base_c + 32 * w) & firsts) | (sight_bits(v, base + 32 * w) & ~firsts);
+            }
             const int d0 = base - (s.len - s.n);
             if (a.mask == kMaskTree && !inside && d0 + kBlock > 0) {
               const Family kin = family(a, s);
@@ -983,15 +1012,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(smem_u32(&s_free[half]));
         if (__builtin_expect(!plain || nones != 0, 0)) {
           if constexpr (X) {
-            if (!plain) {
+            if (plain) vis[0] = vis[1] = vis[2] = vis[3] = ~0u;
+            const int per = geo.parts == 1 ? page_size : kBlock;
+            for (uint32_t left = nones; left; left &= left - 1) {  // pages that the cache does not have
+              const int p0 = (__ffs(left) - 1) * per;
 #pragma unroll
-              for (int w = 0; w < 4; ++w)
-                if (!__all_sync(0xffffffffu, vis[w] == ~0u)) {
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    if (!((vis[w] >> e) & 1)) x[w][e] = -INFINITY;
-                }
+              for (int w = 0; w < 4; ++w) vis[w] &= ~(low_bits(p0 + per - 32 * w) & ~low_bits(p0 - 32 * w));
             }
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              if (!__all_sync(0xffffffffu, vis[w] == ~0u)) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!((vis[w] >> e) & 1)) x[w][e] = -INFINITY;
+              }
           } else {
             // columns [d0, d1) are keys of this row, [u0, u1) of all rows of this half; in the last part of a page that all
             // see, the page's rows (without block_keys' division)
@@ -1011,15 +1045,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = 0; e < 16; ++e)
                   if (16 * q + e < d0 || 16 * q + e >= d1) x[q >> 1][16 * (q & 1) + e] = -INFINITY;
               }
-          }
-          const int per = geo.parts == 1 ? page_size : kBlock;
-          for (uint32_t left = nones; left; left &= left - 1) {
-            const int p0 = (__ffs(left) - 1) * per;
+            const int per = geo.parts == 1 ? page_size : kBlock;
+            for (uint32_t left = nones; left; left &= left - 1) {
+              const int p0 = (__ffs(left) - 1) * per;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+              for (int c = 0; c < 4; ++c)
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (32 * c + e >= p0 && 32 * c + e < p0 + per) x[c][e] = -INFINITY;
+                for (int e = 0; e < 32; ++e)
+                  if (32 * c + e >= p0 && 32 * c + e < p0 + per) x[c][e] = -INFINITY;
+            }
           }
         }
         float mx[4];
@@ -1080,7 +1114,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the ring before this block's has to be known to be there: the P V before the last one of this half is, which is
           // enough where both halves take all blocks and a block one slot.
           if (ok && i > 0 && (split || kOne)) ok = wait_phase(&o_done[bar_of(half, c - 1)], phase_of(c - 1), err, kDevTimeoutAccum);
-          ok = ok && clean_values<T, DP>(sV, full + SK, (it + o - j0) * pv, pv, hrow, j, run, err);
+          if constexpr (X && DP == 64) ok = ok && clean_values<T, DP>(sV, full + SK, (it + o - j0) * pv, pv, hrow, j, run, err);
+          else ok = ok && clean_values_apart<T, DP>(sV, full + SK, (it + o - j0) * pv, pv, hrow, j, run, err);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
         }
@@ -1162,20 +1197,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (__builtin_expect(odd_lo <= odd_hi && (real || X), 0)) {
             const int* table = a.b.pages + run->b * a.b.page_stride;
-            int k_lo, k_hi, kr;
-            block_keys(geo, page_size, odd_lo, &k_lo, &kr);
-            block_keys(geo, page_size, odd_hi, &k_hi, &kr);
-            k_hi += kr;
+            int k_lo, k_hi, kr, n_pages = 0;
             Family kin = {};
-            if (X && a.mask == kMaskTree) {
-              k_hi = min(k_hi, s.len);
-              kin = family(a, s);
+            if (X && geo.parts == 1) {  // all units' keys, of which the row's are taken
+              n_pages = geo.pages;
+              k_lo = odd_lo * n_pages * page_size, k_hi = min((odd_hi + 1) * n_pages, run->units) * page_size;
+            } else {
+              block_keys(geo, page_size, odd_lo, &k_lo, &kr);
+              block_keys(geo, page_size, odd_hi, &k_hi, &kr);
+              k_hi += kr;
             }
-            for (int k = X ? k_lo : max(lo, k_lo); k < (X ? k_hi : min(hi, k_hi)); ++k) {
+            if (X && a.mask == kMaskTree) kin = family(a, s);
+            for (int at = X ? k_lo : max(lo, k_lo); at < (X ? k_hi : min(hi, k_hi)); ++at) {
+              const int k = X && geo.parts == 1 && at >= run->firsts * page_size ? at + run->skip * page_size : at;
               if constexpr (X) {
                 bool sees = k < first_keys || (k >= lo && k < hi);
                 const int d = k - (s.len - s.n);
-                if (a.mask == kMaskTree && d >= 0) {  // (the warp's lanes walk together)
+                if (a.mask == kMaskTree && d >= 0 && d < s.n) {  // (the warp's lanes walk together)
                   const uint64_t up = ancestors(a, s, kin, real ? (row0 + row) / a.group : -1, d);
                   sees = sees || (up & 1);
                 }
