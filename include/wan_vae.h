@@ -526,10 +526,10 @@ int64_t wan_kv_attention_workspace(const wan_kv_cache* cache, const wan_kv_batch
  * it, or -1 for none.  One that does not come before its child counts as none
  * and leaves a code in the batch's status word.  A row's mask is found by a walk
  * up the tree, so a call takes time by its depth; what is a chain throughout is
- * better a range.
+ * better a range.  At most 1024 new tokens a sequence.
  *
- * A sequence with more new tokens than keys gets zeros and leaves a code in the
- * status word.  Pages that hold no key that any token sees (between the first
+ * A sequence with more new tokens than keys (or than a tree may have) gets zeros
+ * and leaves a code in the status word.  Pages that hold no key that any token sees (between the first
  * keys and the windows) are not read, and their numbers in the table may be
  * anything.  Precision, kernels, errors and the other arguments are those of
  * wan_kv_attention; workspace: wan_kv_masked_attention_workspace bytes. */
@@ -562,7 +562,8 @@ int64_t wan_kv_masked_attention_workspace(const wan_kv_cache* cache, const wan_k
  * length are none of the table's, if fresh_pages are too few, or if its target
  * is a source of the call, or the target of an earlier fork.  A page number
  * outside the cache: what it would hold is not copied, and a code is left.
- * forks: up to 1024.  Errors: WAN_ERR_INVALID_ARG, WAN_ERR_DTYPE,
+ * What the call reads (sources, targets, fresh) shares no memory with the tables
+ * (other columns of the page table's rows are fine).  forks: up to 1024.  Errors: WAN_ERR_INVALID_ARG, WAN_ERR_DTYPE,
  * WAN_ERR_UNSUPPORTED, WAN_ERR_CUDA. */
 wan_status wan_kv_fork(const wan_kv_cache* cache, int32_t* pages, int64_t page_stride, int32_t max_pages,
                        int32_t sequences, int32_t* lengths, const int32_t* sources, const int32_t* targets,

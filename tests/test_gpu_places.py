@@ -139,7 +139,7 @@ TREE = [
     ([500, 64, 65], [64, 64, 64], 2, 4, 128, 64, "random"), ([1000, 129], [64, 64], 1, 8, 64, 16, "comb"),
     ([400, 1300], [129, 200], 1, 2, 128, 128, "random"), ([300], [300], 1, 1, 128, 24, "chain"), ([900], [257], 2, 1, 64, 390, "random"),
     ([1000], [64], 1, 16, 256, 64, "random"), ([500, 300], [33, 1], 1, 40, 80, 8, "star"), ([2000], [280], 1, 1, 256, 256, "comb"),
-    ([130] * 20, [64] * 20, 2, 2, 128, 16, "random"), ([1100], [1100], 1, 1, 64, 64, "random"),
+    ([130] * 20, [64] * 20, 2, 2, 128, 16, "random"), ([1100], [1024], 1, 1, 64, 64, "random"),
 ]
 
 
@@ -282,6 +282,51 @@ def test_what_is_not_there_is_left_out(wv, new, kind):
         assert not got[rows].any() and bool(torch.isinf(lse[rows]).all())
         ref.assert_rounded(got[keep], good[0][keep], good[1][keep])
     lengths[1] = lens[1]
+
+
+@pytest.mark.parametrize("drafts", [1024, 1025])
+def test_most_drafts_of_a_tree(wv, drafts):
+    """One more than a tree may have: zeros and a code; the other sequence as ever."""
+    lens, new = [1300, 90], [drafts, 70]
+    q, kc, vc, pages, lengths, cu = _case(lens, new, 1, 1, 64, 64, torch.bfloat16)
+    trees = [_tree(m, "chain") for m in new]
+    status = _status()
+    got, lse = wv.kv_tree_attention(q, kc, vc, pages, lengths, _i32(sum(trees, [])), cu, status=status, return_lse=True)
+    want = place.attention(q, kc, vc, pages, lengths, cu, [place.tree_sees(n, t) for n, t in zip(lens, trees)])
+    if drafts > 1024:
+        with pytest.raises(wv.WanError, match="length or token range"):
+            wv.kv_status(status)
+        assert not got[:drafts].any() and bool(torch.isinf(lse[:drafts]).all())
+        ref.check_attention(got[drafts:], lse[drafts:], tuple(t[drafts:] for t in want))
+    else:
+        wv.kv_status(status)
+        ref.check_attention(got, lse, want)
+
+
+@pytest.mark.parametrize("new", [[2, 5], [150, 90]], ids=["few", "many"])
+def test_places_past_32_bits(wv, new):
+    """Pages more than 2^31 elements apart: attention, forks and compaction reach them all."""
+    lens, size, D, hk = [200, 90], 64, 64, 1
+    far = 2 ** 31 + 64                                        # elements from page to page
+    base = torch.zeros(6 * far + hk * size * D, dtype=torch.bfloat16, device="cuda")
+    kc, vc = (base[i * hk * size * D:].as_strided((6, hk, size, D), (far, size * D, D, 1)) for i in (0, 1))
+    pages = _i32([[5, 0, 3, 1] + [-1] * 700, [4, 2, 0, 0] + [-1] * 700])   # room for more: many rows go by their own kernel
+    lengths = _i32(lens)
+    fill = [(_randn(6, hk, size, D, dtype=torch.bfloat16, seed=i)) for i in (1, 2)]
+    kc.copy_(fill[0]), vc.copy_(fill[1])
+    cu = _i32([0, new[0], sum(new)])
+    q = _randn(sum(new), 2, D, dtype=torch.bfloat16, seed=3)
+    for kind in "window", "tree":
+        call, sees = _calls(wv, kind, kc, vc, pages, lengths, cu, lens, [min(a, b) for a, b in zip(new, lens)])
+        ref.check_attention(call(q), None, place.attention(q, *fill, pages, lengths, cu, sees))
+    tables = _i32([[5, 0, 3, 1], [-1] * 4]), _i32([120, 0])
+    want = place.fork(*fill, *tables, [0], [1], _i32([[2, 4]]), False)
+    wv.kv_fork(kc, vc, *tables, _i32([0]), _i32([1]), _i32([[2, 4]]), False)
+    assert torch.equal(kc, want[0]) and torch.equal(vc, want[1]) and torch.equal(tables[0], want[2])
+    keep = list(range(10, 200, 3))
+    want = place.compact(want[0], want[1], pages, [5], [keep])
+    assert wv.kv_compact(kc, vc, pages[:1], _i32([5]), _i32(keep), _i32([0, len(keep)])).tolist() == want[2]
+    assert torch.equal(kc, want[0]) and torch.equal(vc, want[1])
 
 
 def test_window_and_ranges_agree(wv):

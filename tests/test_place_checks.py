@@ -79,6 +79,13 @@ def test_fork_refusals(lib):
     assert _fork(lib, c=_cache(k_head=0)) == 1
     assert b"broadcast" in lib.wan_vae_last_error()
     assert _fork(lib, n=1025) == 5
+    # memory in common: fresh in the table's columns, in the lengths; sources in either; but not other columns of the same rows
+    at = dict(pages=4096, stride=8, columns=4, B=3, lengths=8192, sources=12288, targets=16384, n=3, fp=2)
+    for kw in (dict(fresh=4096, fs=8), dict(fresh=4096 + 32 + 12, fs=8), dict(fresh=4096 + 16, fs=7), dict(fresh=4096 + 28, fs=8),
+               dict(fresh=8192, fs=2), dict(fresh=1 << 20, fs=2, sources=4096), dict(fresh=1 << 20, fs=2, targets=8200),
+               dict(fresh=1 << 20, fs=2, lengths=4100)):
+        assert _fork(lib, **{**at, **kw}) == 1, kw
+        assert b"share" in lib.wan_vae_last_error(), kw
     assert _fork(lib, n=0, sources=None, targets=None, fresh=None) == 0
 
 
@@ -88,7 +95,7 @@ def test_compact_refusals(lib):
     assert _compact(lib, keep=4098) == 1 and _compact(lib, lengths=8193) == 1
     assert _compact(lib, c=_cache(v_row=0)) == 1
     assert b"broadcast" in lib.wan_vae_last_error()
-    for over in 64, 60, 72, 128, 4100:                       # in the memory of lengths, of the ranges, of keep
+    for over in 64, 60, 72, 128, 4100:                       # in the memory of lengths and the table, of the ranges, of keep
         assert _compact(lib, lengths=over) == 1, over
         assert b"share" in lib.wan_vae_last_error()
     assert _compact(lib, c=_cache(heads=1001, k_page=2 ** 20, v_page=2 ** 20)) == 5

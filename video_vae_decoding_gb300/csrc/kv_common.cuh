@@ -52,7 +52,8 @@ __device__ __forceinline__ Seq sequence(const AttnArgs& a, int b, bool tell) {
   Seq s;
   const bool ok = kv_rows(a.b.cu, a.b.T, b, &s.r0, &s.n);
   bool okl = kv_length(a.b.lengths[b], a.b.max_pages, a.c.page_size, &s.len);
-  if (a.mask != kMaskRanges && s.n > s.len) {  // its tokens have no places
+  // its tokens have no places, or are more than a tree's may be
+  if (a.mask != kMaskRanges && (s.n > s.len || (a.mask == kMaskTree && s.n > kMaxDrafts))) {
     okl = false;
     s.len = 0;
   }

@@ -96,6 +96,22 @@ wan_status check_written(const KvCache& c) {
   return WAN_OK;
 }
 
+// Whether two arrays of numbers have memory in common.
+bool meet(const int32_t* x, int64_t n, const int32_t* y, int64_t m) {
+  const uintptr_t a = (uintptr_t)x, b = (uintptr_t)y;
+  return n > 0 && m > 0 && a < b + 4 * (uintptr_t)m && b < a + 4 * (uintptr_t)n;
+}
+// Whether two tables whose ranges meet are different columns of one: rows as far apart, and none of one's columns the other's.
+bool columns_apart(const int32_t* x, int64_t x_stride, int64_t x_columns, int64_t x_rows, const int32_t* y, int64_t y_stride,
+                   int64_t y_columns, int64_t y_rows) {
+  if (x_rows > 1 && y_rows > 1 && x_stride != y_stride) return false;
+  const int64_t stride = x_rows > 1 ? x_stride : y_stride;  // (two single rows that meet are not apart)
+  if (stride <= 0 || (x_rows <= 1 && y_rows <= 1)) return false;
+  int64_t col = (((intptr_t)x - (intptr_t)y) / 4) % stride;  // of x's first column among y's
+  if (col < 0) col += stride;
+  return col >= y_columns && col + x_columns <= stride;
+}
+
 wan_status sm_count(int* n) {
   int dev;
   CUDA_TRY(cudaGetDevice(&dev));
@@ -443,6 +459,12 @@ wan_status wan_kv_fork(const wan_kv_cache* cache, int32_t* pages, int64_t page_s
     if (((uintptr_t)pages | (uintptr_t)lengths | (uintptr_t)sources | (uintptr_t)targets | (uintptr_t)fresh |
          (uintptr_t)status) & 3)
       return fail(WAN_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+    const int64_t table = (int64_t)(sequences - 1) * page_stride + max_pages, rest = (int64_t)(forks - 1) * fresh_stride + fresh_pages;
+    const bool beside = fresh_pages > 0 && meet(fresh, rest, pages, table) && !columns_apart(fresh, fresh_stride, fresh_pages, forks, pages, page_stride, max_pages, sequences);
+    if (beside || (fresh_pages > 0 && meet(fresh, rest, lengths, sequences)) || meet(sources, forks, pages, table) ||
+        meet(targets, forks, pages, table) || meet(sources, forks, lengths, sequences) || meet(targets, forks, lengths, sequences) ||
+        meet(lengths, sequences, pages, table))
+      return fail(WAN_ERR_INVALID_ARG, "sources, targets, fresh, lengths and the page table must not share memory");
     a.pages = pages, a.lengths = lengths;
     a.page_stride = page_stride, a.max_pages = max_pages, a.B = sequences;
     a.sources = sources, a.targets = targets, a.fresh = fresh;
@@ -467,8 +489,8 @@ wan_status wan_kv_compact(const wan_kv_cache* cache, const wan_kv_batch* batch, 
     if (((uintptr_t)a.b.pages | (uintptr_t)a.b.lengths | (uintptr_t)a.b.cu | (uintptr_t)keep | (uintptr_t)lengths |
          (uintptr_t)a.b.status) & 3)
       return fail(WAN_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
-    const auto apart = [&](const int32_t* x, int64_t n) { return !x || lengths + a.b.B <= x || x + n <= lengths; };
-    if (!apart(a.b.lengths, a.b.B) || !apart(a.b.cu, a.b.B + 1LL) || !apart(keep, a.b.T))
+    if (meet(lengths, a.b.B, a.b.lengths, a.b.B) || meet(lengths, a.b.B, a.b.cu, a.b.B + 1LL) || meet(lengths, a.b.B, keep, a.b.T) ||
+        meet(lengths, a.b.B, a.b.pages, (a.b.B - 1) * a.b.page_stride + a.b.max_pages))
       return fail(WAN_ERR_INVALID_ARG, "lengths must not share memory with what the call reads");
     if (a.c.heads > 1000) return fail(WAN_ERR_UNSUPPORTED, "%d heads (at most 1000)", a.c.heads);
     a.keep = keep;

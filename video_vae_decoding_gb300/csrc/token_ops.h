@@ -91,6 +91,8 @@ enum AttnMask : int {
   kMaskWindow = 1,  // the first `sinks` keys and a window of frames
   kMaskTree = 2,    // what comes before the new tokens, its ancestors among them and itself
 };
+// New tokens that a sequence of a tree call may have: a row finds its ancestors by a walk, whose length this bounds.
+constexpr int kMaxDrafts = 1024;
 
 struct AttnArgs {
   KvCache c;

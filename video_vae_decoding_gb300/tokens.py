@@ -563,7 +563,8 @@ def kv_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     parents [tokens] int32: the place of a draft's parent among its sequence's
     drafts (0: the first), which comes before it, or -1.  Others count as -1 and
     leave a code in `status`.  Time goes with the tree's depth; a chain is better
-    a range of kv_attention."""
+    a range of kv_attention.  At most 1024 drafts a sequence (others get zeros and
+    leave a code)."""
     short = _short or _short_way()
     if stream is None:
         got = short.tree(q, k_cache, v_cache, pages, lengths, cu_tokens, parents, scale, out, return_lse, status)
