@@ -27,6 +27,11 @@
 // first two took 11 and 2 us more.)
 // Sums, maxima and outputs are held in 32 bits; how the weights are rounded is
 // told at Weights.
+//
+// The kernel's second form (X) is for rows that see by their place: a window with
+// first keys, or a tree of drafts.  Its line holds only the tiles that a row tile's
+// rows see: 48 ragged sequences of up to 20,000 keys, windows of 4096 and 128 first
+// keys, 32 heads of 128 on 8 (0.78 GB), take 130 us, 6.0 TB/s.
 #include <algorithm>
 
 #include "kv_common.cuh"

@@ -44,6 +44,13 @@
 // The line of (sequence, row tile, head, key block) is cut into equal pieces,
 // one per SM, as in the split kernel (weighed by what a block costs in a larger
 // and in a smaller tile); the join adds up what a cut divides.
+//
+// The second form (X) is for rows that see by their place (a window with first keys,
+// a tree of drafts): blocks are made of the pages that some row of the tile sees.
+// A window of 9 latent frames and the first one, 880 tokens of 16 heads of 128, takes
+// 87 us (0.73 PFLOP/s: runs of 30 blocks, of which start and end are a quarter), 64
+// drafts of 24 sequences of up to 9000 keys, 32 heads on 8, 134 us, ragged windows of
+// 1000 keys at heads of 64 85 us.
 #include <type_traits>
 
 #include "kv_common.cuh"
@@ -261,8 +268,8 @@ struct RowTile {
 };
 // With X (rows see by their place) its rows see the first keys and a window.  What holds them is taken together: units (pages,
 // or the blocks of a longer page) 0 .. firsts - 1, and `skip` units further on the rest of `units`; a block takes as many
-// units as it has pages.  (Blocks of the window alone and of the first keys alone took 103 us for ragged prompts with windows of
-// 1000 keys and pages of 32.)
+// units as it has pages.  (With blocks of the window alone and of the first keys alone, ragged prompts with windows of 1000 keys
+// and pages of 32 took 103 us instead of 92.)
 struct SightTile : RowTile {
   int firsts, skip, units, pad;
 };
