@@ -527,6 +527,7 @@ def _keeps(kind, lens, seed=0):
 COMPACT = [
     ([5], 1, 8, 16), ([40, 0, 17, 1], 2, 128, 16), ([900, 333], 3, 80, 24), ([5000], 2, 128, 64), ([2000, 30], 1, 256, 390),
     ([700] * 9, 1, 72, 7), ([130], 12, 64, 1), ([2640], 4, 96, 880), ([60] * 200, 1, 64, 16), ([4000], 1, 136, 128),
+    ([300] * 12, 4, 128, 16), ([300, 500] * 3, 4, 128, 32),
 ]
 
 

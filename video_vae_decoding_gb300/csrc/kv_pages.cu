@@ -189,10 +189,11 @@ __global__ void __launch_bounds__(32 * kForkWarps, kForkCtas) kv_fork_kernel(con
 //    steps of many rows.  Since keep[j] >= first + j, what a later step reads lies
 //    behind all places that earlier ones write: the rows of step c + 1 are asked
 //    for, a barrier says that those of step c are all read, and they are stored.
-// 11,440 keys of 16 heads of 128 in the first way (187 MB read and written) take 32
-// us, 5.8 TB/s (in the second 44); 13 sequences of up to 1900 scattered keys, 8 heads
-// of 96, 24 us.  (Blocks of 8 warps, three an SM, 42 and 28 us.)
-constexpr int kMoveWarps = 4, kMoveCtas = 8;
+// 11,440 keys of 16 heads of 128 in the first way (187 MB read and written) take 34
+// us, 5.4 TB/s; 13 sequences of up to 1900 scattered keys, 8 heads of 96, 24 us.  For
+// the second way's steps a call of few planes has blocks of up to 32 warps: 16,368
+// scattered keys of 27,280, 16 heads of 128 (268 MB), 59 us.
+constexpr int kMoveLanes = 32;  // warps of the blocks that share an SM
 constexpr int kMoveAhead = 4;  // row groups of a warp in a step
 
 // Of the row that this lane looks up:
@@ -203,7 +204,8 @@ struct Move {
   long long from, to;  // in elements; from < 0: none
 };
 
-__global__ void __launch_bounds__(32 * kMoveWarps, kMoveCtas)
+template <int kMoveWarps>
+__global__ void __launch_bounds__(32 * kMoveWarps, kMoveLanes / kMoveWarps)
     kv_compact_kernel(const __grid_constant__ CompactArgs a, const int blocks, const int ordered) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -331,14 +333,15 @@ cudaError_t launch_kv_fork(const ForkArgs& a, int sms, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kv_fork_kernel, a);
 }
 
-cudaError_t launch_kv_compact(const CompactArgs& a, int sms, cudaStream_t s) {
-  // Three times as many blocks as are resident, so that ragged sequences even out (13 of 500 to 1900 kept keys take 24.6 us,
-  // 27.8 with one time), fewer for a call of few keys; slices of 64 bytes or more.
-  const int CH = a.c.D / 8;
-  const long long planes = 2LL * a.c.heads * a.b.B, step = kMoveWarps * kMoveAhead * std::max(1, 32 / CH);
-  const long long most = std::max(1LL, a.b.T / (a.b.B * step));  // steps of a sequence on average
-  const int blocks = (int)std::max(1LL, std::min(most, (3LL * kMoveCtas * sms + planes - 1) / planes));
-  const int ordered = std::min(blocks, std::max(1, CH / 4));
+template <int W>
+static cudaError_t go_compact(const CompactArgs& a, long long planes, int slices, int sms, cudaStream_t s) {
+  // Three times as many small blocks as are resident, so that ragged sequences even out (13 of 500 to 1900 kept keys take 24.6
+  // us, 27.8 with one time); of large ones as many, whose starts would come one after the other (a clip's roll 39 us with
+  // three times); fewer for a call of few keys.
+  const long long step = W * kMoveAhead * std::max(1, 32 / (a.c.D / 8)), steps = std::max(1LL, a.b.T / (a.b.B * step));
+  const long long resident = (long long)(kMoveLanes / W) * sms;
+  const long long want = W <= 8 ? (3 * resident + planes - 1) / planes : std::max((long long)slices, resident / planes);
+  const int blocks = (int)std::max(1LL, std::min(steps, want));
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -347,8 +350,20 @@ cudaError_t launch_kv_compact(const CompactArgs& a, int sms, cudaStream_t s) {
   cfg.numAttrs = 1;
   cfg.stream = s;
   cfg.gridDim = dim3(a.b.B, 2 * a.c.heads * blocks);
-  cfg.blockDim = dim3(32 * kMoveWarps);
-  return cudaLaunchKernelEx(&cfg, kv_compact_kernel, a, blocks, ordered);
+  cfg.blockDim = dim3(32 * W);
+  return cudaLaunchKernelEx(&cfg, kv_compact_kernel<W>, a, blocks, std::min(blocks, slices));
+}
+
+cudaError_t launch_kv_compact(const CompactArgs& a, int sms, cudaStream_t s) {
+  // In steps, planes in slices of 64 bytes or more have to keep the card busy: the fewer, the more warps each.  us for
+  // 16,368 of 27,280 keys of 16 heads of 128 (32 planes, 268 MB) in blocks of 4, 8, 16, 32 warps: 166, 106, 77, 59; for 8
+  // sequences of 8000 and 8 heads (128 planes, 367 MB) 86, 66, 71, 80; for the first way's 11,440 keys 32, 32, 33, 34.
+  const int slices = std::max(1, a.c.D / 32);
+  const long long planes = 2LL * a.c.heads * a.b.B, most = (long long)kMoveLanes * sms / (planes * slices);
+  if (a.b.T < 64LL * a.b.B || most < 8) return go_compact<4>(a, planes, slices, sms, s);
+  if (most < 16) return go_compact<8>(a, planes, slices, sms, s);
+  if (most < 32) return go_compact<16>(a, planes, slices, sms, s);
+  return go_compact<32>(a, planes, slices, sms, s);
 }
 
 }  // namespace wan
