@@ -658,7 +658,9 @@ def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor
 def kv_check(pages: torch.Tensor, lengths: torch.Tensor, page_size: int, n_pages: int, cu_tokens: torch.Tensor = None,
              tokens: int = None, append: bool = False):
     """Checks host (CPU int32) tables as kv_append (append=True) and kv_attention
-    would read them; raises WanError naming the sequence at fault."""
+    would read them; raises WanError naming the sequence at fault.
+    kv_window_attention and kv_tree_attention ask for no more new tokens than keys,
+    as kv_append does, and look only at pages that some token sees."""
     cpu = torch.device("cpu")
     if tokens is None:
         tokens = int(cu_tokens[-1]) if cu_tokens is not None else lengths.shape[0]
