@@ -382,7 +382,10 @@ struct alignas(16) Run {
   int first, last;           // of the tile's blocks [first, last)
   int blocks;                // k1 - k0; 0: the piece has no more runs
   int all_lo[2], all_hi[2];  // per half: keys that every row sees
-  int odd_lo, odd_hi;        // blocks whose values were cleaned (below)
+  int odd_lo, odd_hi;        // first and last block with odd values (below) of keys that the sequence has
+  uint32_t odd_some;         // bit j % 32: block j may be one
+  ChunkGeo geo;              // the call's, for what has no registers for them
+  int page_size;
   int firsts, skip, units;   // with X: the tile's
   int all_c[2];              // and all rows of a half see [0, all_c) too
 };
@@ -394,17 +397,74 @@ struct alignas(16) Cursor {
   int i;
 };
 
-// Keys that some row of a tile does not see: an infinity or a NaN among their
-// values must not meet a weight of zero.  Such values leave the block here (V in
+// The keys of block j's columns: columns [0, at_c) hold those from base_c on, [at_c, rows) those from base on (both less the
+// column).
+struct Columns {
+  int base_c, base, at_c, rows;
+  __device__ __forceinline__ int key(int column) const { return (column < at_c ? base_c : base) + column; }
+};
+template <bool X>
+__device__ __forceinline__ Columns columns_of(const ChunkGeo& geo, int page_size, const Run* run, int j) {
+  Columns k{0, 0, 0, 0};
+  if (X && geo.parts == 1) {
+    k.rows = geo.pages * page_size;
+    k.base_c = j * k.rows;
+    k.base = k.base_c + run->skip * page_size;
+    k.at_c = min(max((run->firsts - j * geo.pages) * page_size, 0), k.rows);
+  } else {
+    block_keys(geo, page_size, j, &k.base, &k.rows);
+  }
+  return k;
+}
+
+// Keys that some row of a tile does not see: an infinity or a NaN (an odd value) among
+// their values must not meet a weight of zero.  Such values leave the block here (V in
 // `count` slots from the ring's number `at` on, read by a half's 128 threads), and
-// the rows that see them get them at the end.  Where both halves' products read the
+// the rows that see them get them at the end (what stands behind the end of the sequence
+// is nobody's).  Where both halves' products read the
 // slot, half 0 does this for both, ahead of its arrival and so of either product: no
 // product reads a value while it changes.  Not inline but for windows and trees at
 // heads of 64: the softmax's loop needs the registers (two chunks of 1300 causal
 // tokens of 48 heads 159 us, 162 inline; ragged windows at heads of 64 90 and 85).
-template <typename T, int DP>
+template <int DP, bool X>
+constexpr bool kCleanInline = X && DP == 64;
+template <typename T>
+__device__ __forceinline__ uint32_t even32(uint32_t v) {
+  return (odd16<T>(v) ? 0u : v & 0xffffu) | (odd16<T>(v >> 16) ? 0u : v & 0xffff0000u);
+}
+template <typename T>
+__device__ __forceinline__ bool odd128(const uint4& v) {
+  return odd32<T>(v.x) || odd32<T>(v.y) || odd32<T>(v.z) || odd32<T>(v.w);
+}
+// The rest of clean_values, where there are such values: they leave the block, and the run learns of those of the sequence.
+template <typename T, int DP, bool X>
+__device__ __forceinline__ void drop_values(uint8_t* ring, int at, int count, int thread, int block, Run* run) {
+  using C = Cfg<DP>;
+  const Columns k = columns_of<X>(run->geo, run->page_size, run, block);
+  bool held = false;
+  for (int u = at; u < at + count; ++u) {
+    uint4* v = reinterpret_cast<uint4*>(ring + u % C::kValSlots * C::kValSlot);
+    for (int e = thread; e < C::kValSlot / 16; e += kHalfRows) {
+      const uint4 w = v[e];
+      if (!odd128<T>(w)) continue;
+      const int column = (e >> 3) & (kBlock - 1);  // 128 bytes a row of a box
+      held |= column < k.rows && k.key(column) < run->s.len;
+      v[e] = make_uint4(even32<T>(w.x), even32<T>(w.y), even32<T>(w.z), even32<T>(w.w));
+    }
+  }
+  if (!held) return;
+  atomicMin(&run->odd_lo, block);
+  atomicMax(&run->odd_hi, block);
+  atomicOr(&run->odd_some, 1u << (block & 31));
+  __threadfence_block();
+}
+template <typename T, int DP, bool X>
+__device__ __noinline__ void drop_values_apart(uint8_t* ring, int at, int count, int thread, int block, Run* run) {
+  drop_values<T, DP, X>(ring, at, count, thread, block, run);
+}
+template <typename T, int DP, bool X>
 __device__ __forceinline__ bool clean_values(uint8_t* ring, uint64_t* full, int at, int count, int thread, int block, Run* run,
-                                          int* err) {
+                                             int* err) {
   using C = Cfg<DP>;
   constexpr int SV = C::kValSlots;
   bool odd = false;
@@ -412,29 +472,106 @@ __device__ __forceinline__ bool clean_values(uint8_t* ring, uint64_t* full, int 
     if (!wait_phase(&full[u % SV], (u / SV) & 1, err, kDevTimeoutFull)) return false;
     const uint4* v = reinterpret_cast<const uint4*>(ring + u % SV * C::kValSlot);
 #pragma unroll 8
-    for (int e = thread; e < C::kValSlot / 16; e += kHalfRows) {
-      const uint4 w = v[e];
-      odd |= odd32<T>(w.x) || odd32<T>(w.y) || odd32<T>(w.z) || odd32<T>(w.w);
-    }
+    for (int e = thread; e < C::kValSlot / 16; e += kHalfRows) odd |= odd128<T>(v[e]);
   }
   if (odd) {
-    atomicMin(&run->odd_lo, block);
-    atomicMax(&run->odd_hi, block);
-    __threadfence_block();
-    for (int u = at; u < at + count; ++u) {
-      uint16_t* v = reinterpret_cast<uint16_t*>(ring + u % SV * C::kValSlot);
-      for (int e = thread; e < C::kValSlot / 16; e += kHalfRows)
-        for (int k = 0; k < 8; ++k)
-          if (odd16<T>(v[8 * e + k])) v[8 * e + k] = 0;
-    }
+    if constexpr (kCleanInline<DP, X>) drop_values_apart<T, DP, X>(ring, at, count, thread, block, run);
+    else drop_values<T, DP, X>(ring, at, count, thread, block, run);
   }
   fence_proxy_async_smem();
   return true;
 }
-template <typename T, int DP>
+template <typename T, int DP, bool X>
 __device__ __noinline__ bool clean_values_apart(uint8_t* ring, uint64_t* full, int at, int count, int thread, int block, Run* run,
                                                 int* err) {
-  return clean_values<T, DP>(ring, full, at, count, thread, block, run, err);
+  return clean_values<T, DP, X>(ring, full, at, count, thread, block, run, err);
+}
+
+// Windows and trees: adds the odd values of a run's blocks to the rows that see them, to row `row` of the tile, which the
+// thread has written as output, or as a part in `o`.  Called where the run is over: the softmax's loop needs the registers.
+// What a row sees of 64 columns is found once for all channels, and a lane looks whether one of 32 keys has such a value (a
+// chain of 1024 drafts with an infinity in the first and in the last takes 218 us, as without; with a walk up the tree for each
+// key and 16 channels it took 5800.  24 trees of 64 drafts with NaN behind the sequences' ends 137, where those were walked for
+// too 3100).  With ranges the softmax's threads do it, key by key, as they put out 16 channels: a range is soon looked up,
+// and that loop loses 10 to 27% by how it is then compiled if they do not.
+template <typename T, int DP>
+__device__ __noinline__ void give_back(const AttnArgs& a, const Run* run, int row, float4* o, int me) {
+  const Seq s = run->s;
+  const ChunkGeo& geo = run->geo;
+  const bool real = row < run->cnt;
+  const int lane = threadIdx.x & 31, page_size = a.c.page_size, mine = real ? (run->row0 + row) / a.group : -1;
+  const bool whole = run->k0 == run->first && run->k1 == run->last;
+  T* const dst = real ? out_row<T>(a, s, run->h, run->row0 + row) : nullptr;
+  float4* const part = o + ((2LL * me + (run->k0 == run->first ? 1 : 0)) * (DP / 4)) * Cfg<DP>::kRows + row;
+  Sight v{0, 0, 0};
+  if (real) v = sight(a, s, mine);
+  const int* table = a.b.pages + run->b * a.b.page_stride;
+  __syncwarp();
+  Family kin = {};
+  if (a.mask == kMaskTree) kin = family(a, s);
+  const int odd_lo = run->odd_lo, odd_hi = run->odd_hi;
+  for (int j = odd_lo; j <= odd_hi; ++j) {
+    if (geo.parts > 1 && j == run->firsts) j += run->skip;  // (what lies between first keys and window is in no block)
+    if (j > odd_hi || !((run->odd_some >> (j & 31)) & 1)) continue;
+    const Columns k = columns_of<true>(geo, page_size, run, j);
+    for (int c0 = 0; c0 < k.rows; c0 += 64) {
+      uint32_t sees[2];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int col = c0 + 32 * w;
+        const uint32_t firsts = low_bits(k.at_c - col);
+        sees[w] = (sight_bits(v, k.base_c + col) & firsts) | (sight_bits(v, k.base + col) & ~firsts);
+      }
+      const int d0 = k.base + c0 - (s.len - s.n);
+      if (a.mask == kMaskTree && d0 > -64) {
+        uint64_t up = ancestors(a, s, kin, mine, max(d0, 0));
+        if (d0 < 0) up <<= -d0;
+        sees[0] |= (uint32_t)up, sees[1] |= (uint32_t)(up >> 32);
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int col = c0 + 32 * w;
+        if (!real) sees[w] = 0;
+        sees[w] &= low_bits(k.rows - col);
+        const uint32_t any = __reduce_or_sync(0xffffffffu, sees[w]);
+        unsigned long long src = 0;
+        bool odd = false;
+        if ((any >> lane) & 1) {
+          const int key = k.key(col + lane), page = kv_page(table, key, page_size, a.c.pages);
+          if (page >= 0) {
+            const T* p = (const T*)a.c.v + page * a.c.v_page + run->h * a.c.v_head + (key % page_size) * a.c.v_row;
+            src = (unsigned long long)p;
+            for (int c = 0; c < a.c.D; c += 8) odd |= odd128<T>(*reinterpret_cast<const uint4*>(p + c));
+          }
+        }
+        const uint32_t odds = __ballot_sync(0xffffffffu, odd);
+        for (int c = 0; c < a.c.D && odds; c += 8) {
+          float sum[8] = {};
+          bool some = false;
+          for (uint32_t left = odds; left; left &= left - 1) {
+            const int l = __ffs(left) - 1;
+            const uint4 x = *reinterpret_cast<const uint4*>((const T*)__shfl_sync(0xffffffffu, src, l) + c);
+            if (!((sees[w] >> l) & 1) || !odd128<T>(x)) continue;
+            some = true;
+            const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint16_t bits = (uint16_t)(words[e / 2] >> (16 * (e & 1)));
+              if (odd16<T>(bits)) sum[e] += val<T>(*reinterpret_cast<const T*>(&bits));
+            }
+          }
+          if (some) {
+            for (int e = 0; e < 8; ++e) {
+              if (sum[e] == 0.f) continue;
+              if (!whole) (&part[(size_t)((c + e) / 4) * Cfg<DP>::kRows].x)[(c + e) & 3] += sum[e];
+              else dst[c + e] = round_to<T>(val<T>(dst[c + e]) + sum[e]);
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+  }
 }
 
 template <typename T, int DP, bool X>
@@ -569,6 +706,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       run->odd_lo = 0x7fffffff;
       run->odd_hi = -1;
+      run->odd_some = 0;
+      run->geo = geo;
+      run->page_size = page_size;
       if constexpr (X) {
         run->all_c[0] = run->all_c[1] = 0x7fffffff;
         run->firsts = t.firsts;
@@ -1011,8 +1151,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // one of this half is, which is enough where both halves take all blocks and a block one slot.
         auto clean = [&] {
           if (ok && i > 0 && (split || kOne)) ok = wait_phase(&o_done[bar_of(half, c - 1)], phase_of(c - 1), err, kDevTimeoutAccum);
-          if constexpr (X && DP == 64) ok = ok && clean_values<T, DP>(sV, full + SK, (it + o - j0) * pv, pv, hrow, j, run, err);
-          else ok = ok && clean_values_apart<T, DP>(sV, full + SK, (it + o - j0) * pv, pv, hrow, j, run, err);
+          if constexpr (kCleanInline<DP, X>) ok = ok && clean_values<T, DP, X>(sV, full + SK, (it + o - j0) * pv, pv, hrow, j, run, err);
+          else ok = ok && clean_values_apart<T, DP, X>(sV, full + SK, (it + o - j0) * pv, pv, hrow, j, run, err);
           return ok = __all_sync(0xffffffffu, ok);
         };
         if (!__all_sync(0xffffffffu, s_there)) ok = wait_phase(&s_full[half], (n0 + i) & 1, err, kDevTimeoutAccum);
@@ -1181,7 +1321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!split || half == 0) {
         const float rl = l == 0.f ? 0.f : 1.f / l;
-        const int odd_lo = X ? run->odd_lo : max(run->odd_lo, j0), odd_hi = X ? run->odd_hi : min(run->odd_hi, k1 - 1);
+        const int odd_lo = max(run->odd_lo, j0), odd_hi = min(run->odd_hi, k1 - 1);
         T* dst = real ? out_row<T>(a, s, h, row0 + row) : nullptr;
 #pragma unroll 1
         for (int c = 0; c < DP / 16; ++c) {
@@ -1205,30 +1345,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (__builtin_expect(odd_lo <= odd_hi && (real || X), 0)) {
+          if (!X && __builtin_expect(odd_lo <= odd_hi && real, 0)) {
             const int* table = a.b.pages + run->b * a.b.page_stride;
-            int k_lo, k_hi, kr, n_pages = 0;
-            Family kin = {};
-            if (X && geo.parts == 1) {  // all units' keys, of which the row's are taken
-              n_pages = geo.pages;
-              k_lo = odd_lo * n_pages * page_size, k_hi = min((odd_hi + 1) * n_pages, run->units) * page_size;
-            } else {
-              block_keys(geo, page_size, odd_lo, &k_lo, &kr);
-              block_keys(geo, page_size, odd_hi, &k_hi, &kr);
-              k_hi += kr;
-            }
-            if (X && a.mask == kMaskTree) kin = family(a, s);
-            for (int at = X ? k_lo : max(lo, k_lo); at < (X ? k_hi : min(hi, k_hi)); ++at) {
-              const int k = X && geo.parts == 1 && at >= run->firsts * page_size ? at + run->skip * page_size : at;
-              if constexpr (X) {
-                bool sees = k < first_keys || (k >= lo && k < hi);
-                const int d = k - (s.len - s.n);
-                if (a.mask == kMaskTree && d >= 0 && d < s.n) {  // (the warp's lanes walk together)
-                  const uint64_t up = ancestors(a, s, kin, real ? (row0 + row) / a.group : -1, d);
-                  sees = sees || (up & 1);
-                }
-                if (!sees || !real) continue;
-              }
+            int k_lo, k_hi, kr;
+            block_keys(geo, page_size, odd_lo, &k_lo, &kr);
+            block_keys(geo, page_size, odd_hi, &k_hi, &kr);
+            k_hi += kr;
+            for (int k = max(lo, k_lo); k < min(hi, k_hi); ++k) {
               const int page = kv_page(table, k, page_size, a.c.pages);
               if (page < 0) continue;
               const T* src = (const T*)a.c.v + page * a.c.v_page + h * a.c.v_head + (k % page_size) * a.c.v_row;
@@ -1272,6 +1395,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (*stop) break;
+    if constexpr (X) {
+      if (__builtin_expect(run->odd_lo <= run->odd_hi, 0)) {
+        if (warp >= 4 && warp < kSoftEnd) give_back<T, DP>(a, run, threadIdx.x - 128, ws.o, me);
+        __syncthreads();  // before the run's room is another's
+      }
+    }
   }
 
   if (warp == 1) asm volatile("cp.async.wait_all;" ::: "memory");
