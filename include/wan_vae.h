@@ -584,7 +584,9 @@ wan_status wan_kv_fork(const wan_kv_cache* cache, int32_t* pages, int64_t page_s
  * is f, or 0 where f is none).
  * Several sequences of a call must not share a page that the call writes to or
  * that one of them reads from and another writes.  lengths: device int32, not in
- * the memory that the call reads.  heads: up to 1000.  Errors: as above. */
+ * the memory that the call reads.  k and v may be one tensor, whose rows then move
+ * once; otherwise they have no memory in common (rows may interleave).  heads: up
+ * to 1000.  Errors: as above. */
 wan_status wan_kv_compact(const wan_kv_cache* cache, const wan_kv_batch* batch, const int32_t* keep, int32_t* lengths,
                           wan_cuda_stream stream);
 

@@ -349,7 +349,7 @@ static cudaError_t go_compact(const CompactArgs& a, long long planes, int slices
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   cfg.stream = s;
-  cfg.gridDim = dim3(a.b.B, 2 * a.c.heads * blocks);
+  cfg.gridDim = dim3(a.b.B, a.planes * blocks);
   cfg.blockDim = dim3(32 * W);
   return cudaLaunchKernelEx(&cfg, kv_compact_kernel<W>, a, blocks, std::min(blocks, slices));
 }
@@ -359,7 +359,7 @@ cudaError_t launch_kv_compact(const CompactArgs& a, int sms, cudaStream_t s) {
   // 16,368 of 27,280 keys of 16 heads of 128 (32 planes, 268 MB) in blocks of 4, 8, 16, 32 warps: 166, 106, 77, 59; for 8
   // sequences of 8000 and 8 heads (128 planes, 367 MB) 86, 66, 71, 80; for the first way's 11,440 keys 32, 32, 33, 34.
   const int slices = std::max(1, a.c.D / 32);
-  const long long planes = 2LL * a.c.heads * a.b.B, most = (long long)kMoveLanes * sms / (planes * slices);
+  const long long planes = (long long)a.planes * a.b.B, most = (long long)kMoveLanes * sms / (planes * slices);
   if (a.b.T < 64LL * a.b.B || most < 8) return go_compact<4>(a, planes, slices, sms, s);
   if (most < 16) return go_compact<8>(a, planes, slices, sms, s);
   if (most < 32) return go_compact<16>(a, planes, slices, sms, s);

@@ -96,6 +96,51 @@ wan_status check_written(const KvCache& c) {
   return WAN_OK;
 }
 
+// Whether k and v are one tensor, and whether a row of k has memory in common with one of v.
+bool same_rows(const KvCache& c) {
+  return c.k == c.v && (c.pages == 1 || c.k_page == c.v_page) && (c.heads == 1 || c.k_head == c.v_head) &&
+         (c.page_size == 1 || c.k_row == c.v_row);
+}
+// Rows meet if some sum of steps along the pages, heads and rows of k and of v makes up for their distance, but for less than
+// a row.  Steps are taken from the longest stride on, those alone from which the shorter ones can still reach; where
+// strides are so entangled that there are more than 4096 of them to look at, they count as meeting.
+bool rows_meet(const KvCache& c) {
+  using wide = __int128;  // a stride times a count may pass 64 bits
+  struct Step {
+    wide stride, lo, hi;  // times that it can be taken
+  };
+  Step steps[6];
+  int count = 0;
+  const int64_t n[3] = {c.pages, c.heads, c.page_size}, ks[3] = {c.k_page, c.k_head, c.k_row}, vs[3] = {c.v_page, c.v_head, c.v_row};
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] == 1) continue;
+    if (ks[i] == vs[i]) {
+      steps[count++] = {ks[i], 1 - n[i], n[i] - 1};
+    } else {
+      steps[count++] = {ks[i], 0, n[i] - 1};
+      steps[count++] = {vs[i], 1 - n[i], 0};
+    }
+  }
+  std::sort(steps, steps + count, [](const Step& x, const Step& y) { return x.stride > y.stride; });
+  wide least[7] = {}, most[7] = {};  // what the steps from one on can add
+  for (int i = count; i-- > 0;) {
+    least[i] = least[i + 1] + steps[i].lo * steps[i].stride;
+    most[i] = most[i + 1] + steps[i].hi * steps[i].stride;
+  }
+  const auto floor_div = [](wide x, wide y) { return x / y - (x % y < 0); };  // y > 0
+  int budget = 4096;
+  const auto found = [&](const auto& self, int i, wide at) -> bool {
+    if (i == count) return at > -c.D && at < c.D;
+    const Step& s = steps[i];  // -D < at + times * stride + (what the rest adds) < D
+    const wide lo = std::max(s.lo, floor_div(-c.D - most[i + 1] - at, s.stride) + 1);
+    const wide hi = std::min(s.hi, -floor_div(-(c.D - least[i + 1] - at), s.stride) - 1);
+    for (wide t = lo; t <= hi; ++t)
+      if (--budget < 0 || self(self, i + 1, at + t * s.stride)) return true;
+    return false;
+  };
+  return found(found, 0, ((wide)(intptr_t)c.k - (wide)(intptr_t)c.v) / 2);
+}
+
 // Whether two arrays of numbers have memory in common.
 bool meet(const int32_t* x, int64_t n, const int32_t* y, int64_t m) {
   const uintptr_t a = (uintptr_t)x, b = (uintptr_t)y;
@@ -493,6 +538,10 @@ wan_status wan_kv_compact(const wan_kv_cache* cache, const wan_kv_batch* batch, 
         meet(lengths, a.b.B, a.b.pages, (a.b.B - 1) * a.b.page_stride + a.b.max_pages))
       return fail(WAN_ERR_INVALID_ARG, "lengths must not share memory with what the call reads");
     if (a.c.heads > 1000) return fail(WAN_ERR_UNSUPPORTED, "%d heads (at most 1000)", a.c.heads);
+    const bool one = same_rows(a.c);
+    if (!one && rows_meet(a.c))
+      return fail(WAN_ERR_INVALID_ARG, "k and v must be one tensor or have no memory in common: their rows move in place");
+    a.planes = (one ? 1 : 2) * a.c.heads;
     a.keep = keep;
     a.lengths = lengths;
     int sms = 0;

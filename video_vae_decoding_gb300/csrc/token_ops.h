@@ -138,6 +138,7 @@ struct CompactArgs {
   KvBatch b;
   const int* keep;
   int* lengths;  // [B]: keys that are left
+  int planes;    // heads of K and of V, or of K alone (k and v are one tensor, whose rows move once)
 };
 cudaError_t launch_kv_compact(const CompactArgs& a, int sms, cudaStream_t s);
 

@@ -625,7 +625,8 @@ def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor
     int32.  A sequence's numbers ascend, from first[b] or later on.  Where they do
     not, or a page is none, some of its keys are left out and a code is left in
     `status`, as for sequences whose ranges are none.  Pages behind the new lengths
-    are the caller's again."""
+    are the caller's again.  The caches may be one tensor (its rows move once);
+    otherwise no row of one has memory in common with the other."""
     short = _short or _short_way()
     if stream is None:
         got = short.compact(k_cache, v_cache, pages, first, keep, cu_keep, lengths, status)
