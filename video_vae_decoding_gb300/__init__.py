@@ -31,7 +31,8 @@ from .tokens import (Rotation, kv_append, kv_attention, kv_check, kv_compact, kv
                      kv_window_attention, rotary, rotary_grad)
 
 __all__ = ["Model", "DecodeStream", "decode", "attention_block", "causal_conv3d", "out_frames", "WanError",
-           "Rotation", "rotary", "rotary_grad", "kv_append", "kv_attention", "kv_check", "kv_status"]
+           "Rotation", "rotary", "rotary_grad", "kv_append", "kv_attention", "kv_window_attention", "kv_tree_attention", "kv_fork",
+           "kv_compact", "kv_check", "kv_status"]
 
 
 def _code(dtype: torch.dtype) -> int:
