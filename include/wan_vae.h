@@ -457,6 +457,14 @@ typedef struct {
  * keys, and two new tokens of the call in one row of the cache.  Host only. */
 wan_status wan_kv_check(const wan_kv_batch* batch, int32_t page_size, int64_t pages, int32_t append);
 
+/* The same for wan_kv_compact: batch and keep in host memory, as that call would
+ * read them, and held: the keys of each sequence before it.  Refuses what it would
+ * leave out, and a key that would land in a row that stands for another one: of
+ * the same sequence, or of any other in the table (so of one that shares a page
+ * after wan_kv_fork, if the table has its row, with an empty range).  Host only. */
+wan_status wan_kv_check_compact(const wan_kv_batch* batch, const int32_t* held, const int32_t* keep, int32_t page_size,
+                                int64_t pages);
+
 /* Waits for `stream`, then reports what a batch's status word holds
  * (WAN_ERR_INTERNAL with a message; the word is cleared), or WAN_OK. */
 wan_status wan_kv_status(int32_t* status, wan_cuda_stream stream);
@@ -552,7 +560,8 @@ int64_t wan_kv_masked_attention_workspace(const wan_kv_cache* cache, const wan_k
  * device memory, and are written.  For i = 0 .. forks - 1, with n the keys of
  * sequence sources[i] (as lengths has them before the call): the first numbers of
  * row targets[i], one for each page of the n keys, become
- *   share 1: those of row sources[i] for whole pages, and fresh[i * fresh_stride]
+ *   share 1: those of row sources[i] for whole pages (common to both from then on:
+ *            wan_kv_compact must not move keys inside them), and fresh[i * fresh_stride]
  *            for the last page if it is partly filled, whose keys are copied
  *            there (later tokens then go to pages of each sequence's own);
  *   share 0: fresh[i * fresh_stride ..], and all keys are copied;
@@ -582,8 +591,11 @@ wan_status wan_kv_fork(const wan_kv_cache* cache, int32_t* pages, int64_t page_s
  * they had) and a code is left in the batch's status word; so is a sequence whose
  * f, range or result the table cannot hold (none of its keys move, and its result
  * is f, or 0 where f is none).
- * Several sequences of a call must not share a page that the call writes to or
- * that one of them reads from and another writes.  lengths: device int32, not in
+ * The rows that keys move to must be the sequence's alone: whole pages that it
+ * shares with others after wan_kv_fork (share 1) stand ahead of f + the first key
+ * that moves, or the others' keys are overwritten, whether they are in the call
+ * or not, and nothing tells of it (wan_kv_check_compact does, of host tables).
+ * A sequence that is to roll on inside them is forked with share 0.  lengths: device int32, not in
  * the memory that the call reads.  k and v may be one tensor, whose rows then move
  * once; otherwise they have no memory in common (rows may interleave).  heads: up
  * to 1000.  Errors: as above. */

@@ -144,6 +144,7 @@ SIGNATURES = {
                                      ctypes.c_float, _vp, _i64, _i64, _vp, _vp, _i64, _vp]),
     "wan_kv_masked_attention_workspace": (_i64, [_vp, _vp, _i32]),
     "wan_kv_fork": (_i32, [_vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp]),
+    "wan_kv_check_compact": (_i32, [_vp, _vp, _vp, _i32, _i64]),
     "wan_kv_compact": (_i32, [_vp, _vp, _vp, _vp, _vp]),
     "wan_selftest_kv_attention_timeout": (_i32, [_i32, ctypes.POINTER(_i32), _vp]),
 }

@@ -2,6 +2,7 @@
 // launches.
 #include <algorithm>
 #include <cmath>
+#include <map>
 #include <set>
 #include <utility>
 #include <vector>
@@ -315,6 +316,61 @@ wan_status wan_kv_check(const wan_kv_batch* batch, int32_t page_size, int64_t pa
       for (int k = len - n; k < len; ++k)
         if (!rows.insert({row[k / page_size], k % page_size}).second)
           return fail(WAN_ERR_INVALID_ARG, "sequence %d: key %d shares its row with another new token", i, k);
+    }
+    return WAN_OK;
+  })
+}
+
+wan_status wan_kv_check_compact(const wan_kv_batch* batch, const int32_t* held, const int32_t* keep, int32_t page_size,
+                                int64_t pages) {
+  API_GUARD({
+    if (page_size < 1 || pages < 1) return fail(WAN_ERR_INVALID_ARG, "%lld pages of %d rows", (long long)pages, page_size);
+    KvBatch b;
+    WAN_TRY(check_batch(batch, page_size, &b));
+    if (!b.cu || !held || (!keep && b.T > 0)) return fail(WAN_ERR_INVALID_ARG, "null ranges, lengths or keys");
+    struct Place {
+      int sequence, key;
+    };
+    std::map<std::pair<int, int>, Place> written;  // by page and row
+    std::set<int> pages_written;
+    for (int i = 0; i < b.B; ++i) {
+      int r0, n, first, len;
+      if (!kv_rows(b.cu, b.T, i, &r0, &n)) return fail(WAN_ERR_INVALID_ARG, "sequence %d: its range is none of the %d keys", i, b.T);
+      if (!kv_length(held[i], b.max_pages, page_size, &len))
+        return fail(WAN_ERR_INVALID_ARG, "sequence %d: length %d in a table of %d pages of %d keys", i, held[i], b.max_pages, page_size);
+      if (!kv_length(b.lengths[i], b.max_pages, page_size, &first) || first > len)
+        return fail(WAN_ERR_INVALID_ARG, "sequence %d: %d first keys of %d", i, b.lengths[i], len);
+      const int* row = b.pages + i * b.page_stride;
+      for (int j = 0; j < n; ++j) {
+        const int from = keep[r0 + j], to = first + j;
+        if (from < to || from >= len || (j > 0 && from <= keep[r0 + j - 1]))
+          return fail(WAN_ERR_INVALID_ARG, "sequence %d: key %d of %d cannot move to place %d behind key %d", i, from, len, to,
+                      j > 0 ? keep[r0 + j - 1] : -1);
+        if (from == to) continue;
+        for (const int k : {from, to})
+          if (kv_page(row, k, page_size, pages) < 0)
+            return fail(WAN_ERR_INVALID_ARG, "sequence %d: page %d is number %d of a cache of %lld", i, k / page_size,
+                        row[k / page_size], (long long)pages);
+        const auto put = written.insert({{row[to / page_size], to % page_size}, Place{i, to}});
+        if (!put.second)
+          return fail(WAN_ERR_INVALID_ARG, "sequence %d: place %d shares its row with place %d of sequence %d", i, to,
+                      put.first->second.key, put.first->second.sequence);
+        pages_written.insert(row[to / page_size]);
+      }
+    }
+    // nothing that moves may land in a row that stands for another key
+    for (int i = 0; i < b.B; ++i) {
+      const int* row = b.pages + i * b.page_stride;
+      for (int64_t k0 = 0; k0 < held[i]; k0 += page_size) {
+        const int page = row[k0 / page_size];
+        if (!pages_written.count(page)) continue;
+        for (int r = 0; r < page_size && k0 + r < held[i]; ++r) {
+          const auto w = written.find({page, r});
+          if (w != written.end() && (w->second.sequence != i || w->second.key != k0 + r))
+            return fail(WAN_ERR_INVALID_ARG, "sequence %d: key %d has its row in page %d, which place %d of sequence %d would be written to",
+                        i, (int)(k0 + r), page, w->second.key, w->second.sequence);
+        }
+      }
     }
     return WAN_OK;
   })

@@ -581,8 +581,9 @@ def kv_fork(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor, l
     lengths, the rows of pages, and what has to be copied of the caches.
 
     share: whole pages become common to both, and only the keys of a last, partly
-    filled page are copied, to page fresh[i, 0].  Otherwise all keys are copied,
-    to pages fresh[i, 0], fresh[i, 1], ...  sources, targets [forks] and fresh
+    filled page are copied, to page fresh[i, 0].  No kv_compact may move keys
+    inside common pages.  Otherwise all keys are copied, to pages fresh[i, 0],
+    fresh[i, 1], ...  sources, targets [forks] and fresh
     [forks, n]: int32; fresh pages are the caller's to hand out.  A target must be
     neither a source of the call nor the target of two forks: such forks, and
     those whose numbers are none of the tables', are left out and leave a code in
@@ -625,7 +626,13 @@ def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor
     int32.  A sequence's numbers ascend, from first[b] or later on.  Where they do
     not, or a page is none, some of its keys are left out and a code is left in
     `status`, as for sequences whose ranges are none.  Pages behind the new lengths
-    are the caller's again.  The caches may be one tensor (its rows move once);
+    are the caller's again.
+
+    Keys must move to rows that are the sequence's alone.  Pages that it shares with
+    other sequences after kv_fork (share=True) have to stand ahead of the first
+    place that a key moves to: else the others' keys are overwritten, whether they
+    are in the call or not, and nothing tells of it (kv_check does, of host tables).
+    Fork a sequence that is to roll on inside them with share=False.  The caches may be one tensor (its rows move once);
     otherwise no row of one has memory in common with the other."""
     short = _short or _short_way()
     if stream is None:
@@ -657,12 +664,29 @@ def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor
 
 
 def kv_check(pages: torch.Tensor, lengths: torch.Tensor, page_size: int, n_pages: int, cu_tokens: torch.Tensor = None,
-             tokens: int = None, append: bool = False):
+             tokens: int = None, append: bool = False, first: torch.Tensor = None, keep: torch.Tensor = None):
     """Checks host (CPU int32) tables as kv_append (append=True) and kv_attention
     would read them; raises WanError naming the sequence at fault.
+    first, keep: as kv_compact would, with cu_tokens the ranges of keep and lengths
+    the sequences' before the call.  So a key that would land in another's row is
+    found; sequences whose keys only have to stay as they are have empty ranges.
     kv_window_attention and kv_tree_attention ask for no more new tokens than keys,
     as kv_append does, and look only at pages that some token sees."""
     cpu = torch.device("cpu")
+    if (first is None) != (keep is None):
+        raise ValueError("first and keep go together")
+    if keep is not None:
+        _on(keep, cpu, "keep", _INT32, 1)
+        _on(lengths, cpu, "lengths", _INT32, 1)
+        if not keep.is_contiguous() or not lengths.is_contiguous():
+            raise ValueError("keep and lengths must be contiguous")
+        if cu_tokens is None:
+            raise ValueError("cu_tokens must hold the ranges of keep")
+        _int32(page_size, "keys as page size")
+        b, B = _batch(cpu, pages, first, cu_tokens, keep.shape[0], None)
+        if lengths.shape[0] != B:
+            raise ValueError(f"lengths has {lengths.shape[0]} values for {B} sequences")
+        return check(load().wan_kv_check_compact(b, lengths.data_ptr(), keep.data_ptr() or None, page_size, n_pages))
     if tokens is None:
         tokens = int(cu_tokens[-1]) if cu_tokens is not None else lengths.shape[0]
     _int32(page_size, "keys as page size")
