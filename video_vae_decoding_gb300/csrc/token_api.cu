@@ -128,6 +128,8 @@ bool rows_meet(const KvCache& c) {
     least[i] = least[i + 1] + steps[i].lo * steps[i].stride;
     most[i] = most[i + 1] + steps[i].hi * steps[i].stride;
   }
+  const wide apart = ((wide)(intptr_t)c.k - (wide)(intptr_t)c.v) / 2;
+  if (apart + most[0] <= -c.D || apart + least[0] >= c.D) return false;  // (two allocations: no division)
   const auto floor_div = [](wide x, wide y) { return x / y - (x % y < 0); };  // y > 0
   int budget = 4096;
   const auto found = [&](const auto& self, int i, wide at) -> bool {
@@ -139,7 +141,7 @@ bool rows_meet(const KvCache& c) {
       if (--budget < 0 || self(self, i + 1, at + t * s.stride)) return true;
     return false;
   };
-  return found(found, 0, ((wide)(intptr_t)c.k - (wide)(intptr_t)c.v) / 2);
+  return found(found, 0, apart);
 }
 
 // Whether two arrays of numbers have memory in common.
