@@ -190,7 +190,7 @@ __device__ __forceinline__ bool cut_tiles(const AttnArgs& a, int me, int G, Piec
   const int lane = threadIdx.x & 31;
   const long long most = (kSmall + 1) * G;  // (a sequence's numbers are cut to it: sums of 32 then fit 32 bits)
   Tiles t{0, 0, 0};
-  if (lane < a.b.B) t = tiles_of<true>(a, sequence(a, lane, false));
+  if (lane < a.b.B) t = tiles_of<true>(a, sequence<true>(a, lane, false));
   const int total = (int)__reduce_add_sync(0xffffffffu, (uint32_t)min(t.all, most));
   if (total > kSmall * G) return false;
   const int runs = t.key_tiles > 0 ? (int)t.runs : 0;
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
   int parts = 0;
   Piece pc;
   if (!X || !cut_tiles(a, me, gridDim.x * kWarps, &pc, &parts))
-    pc = cut_line<kWarps, kWarps>(a.b.B, kLeast, s_line, [&](int b) { return tiles_of<X>(a, sequence(a, b, false)).all; });
+    pc = cut_line<kWarps, kWarps>(a.b.B, kLeast, s_line, [&](int b) { return tiles_of<X>(a, sequence<X>(a, b, false)).all; });
   if (lane == 0) ws.open[me].parts = 0;
   int b = pc.b;
   long long at = pc.at;
@@ -276,11 +276,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<DP>::kCtas)
   const T* vbase = (const T*)a.c.v;
 
   for (long long line = pc.beg; line < pc.end;) {
-    Seq s = sequence(a, b, false);
+    Seq s = sequence<X>(a, b, false);
     Tiles tl = tiles_of<X>(a, s);
     while (at >= tl.all) {  // the next sequence with a tile
       at -= tl.all;
-      s = sequence(a, ++b, false);
+      s = sequence<X>(a, ++b, false);
       tl = tiles_of<X>(a, s);
     }
     // the run: key tiles [kt0, kt1) of one row tile and head

@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
     Seq s{0, 0, 0};
     long long rt = 0;
     if (b0 + lane < a.b.B) {
-      s = sequence(a, b0 + lane, false);
+      s = sequence<X>(a, b0 + lane, false);
       rt = place - ((long long)s.r0 * a.group / tile + b0 + lane);
     }
     const uint32_t mine = __ballot_sync(0xffffffffu, s.len > 0 && rt >= 0 && rt * tile < (long long)s.n * a.group);
@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto units = [&](const RowTile& t, int w) { return (long long)(kRunUnits + w * (t.k1 - t.k0)); };
   const Piece cut = cut_line<kThreads / 32, 1>((int)row_tiles(a), kLeast, reinterpret_cast<long long*>(half_ml), [&](int i) {
     const Tile<X> t = ws.tiles[i];
-    return t.b < 0 ? 0 : a.c.heads * units(t, tile_weight<X>(a, sequence(a, t.b, false), t.rt));
+    return t.b < 0 ? 0 : a.c.heads * units(t, tile_weight<X>(a, sequence<X>(a, t.b, false), t.rt));
   });
   tc_fence_before();
   __syncthreads();
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int w = 0;
       for (;;) {
         if (t.b >= 0) {
-          s = sequence(a, t.b, false);
+          s = sequence<X>(a, t.b, false);
           w = tile_weight<X>(a, s, t.rt);
           n = units(t, w);
           if (at < a.c.heads * n) break;

@@ -47,13 +47,15 @@ struct Seq {
   int r0, n, len;  // first token row, tokens, keys
 };
 // Sequence b; one that its batch does not describe has no tokens (or no keys),
-// and is told to the status word if `tell`.
+// and is told to the status word if `tell`.  X: rows may see by their place (calls
+// with ranges take up to 1% longer if that is asked each time).
+template <bool X = true>
 __device__ __forceinline__ Seq sequence(const AttnArgs& a, int b, bool tell) {
   Seq s;
   const bool ok = kv_rows(a.b.cu, a.b.T, b, &s.r0, &s.n);
   bool okl = kv_length(a.b.lengths[b], a.b.max_pages, a.c.page_size, &s.len);
   // its tokens have no places, or are more than a tree's may be
-  if (a.mask != kMaskRanges && (s.n > s.len || (a.mask == kMaskTree && s.n > kMaxDrafts))) {
+  if (X && a.mask != kMaskRanges && (s.n > s.len || (a.mask == kMaskTree && s.n > kMaxDrafts))) {
     okl = false;
     s.len = 0;
   }
