@@ -141,3 +141,25 @@ def test_rows_behind_the_last_sequence_stay(wv):
     wv.kv_window_attention(wide, kc, vc, pages, lengths, 70, 9, cu_tokens=cu, out=out)
     assert bool((out[150:] == 5.0).all())
     ref.check_attention(out[:150], None, place.attention(q, kc, vc, pages, lengths, cu, [place.window_sees(500, 150, 70, 9, 1)]))
+
+
+@pytest.mark.parametrize("new", [1, 64], ids=["few", "many"])
+def test_windows_of_more_than_2_31_keys(wv, new):
+    """Two frames of 1.5e9 keys hold a sequence of 1.6e9 (two pages, which the table repeats: the first half of the places
+    has ones as values, the second zeros); frames that end past 2^31 leave the narrow windows as they are."""
+    size, ones, n = 1 << 20, 762, 1_600_000_000
+    kc = torch.zeros(2, 1, size, 8, dtype=torch.bfloat16, device="cuda")
+    vc = kc.clone()
+    vc[0] = 1.0
+    pages = torch.ones(1, -(-n // size), dtype=torch.int32, device="cuda")
+    pages[0, :ones] = 0
+    q, lengths, cu = _randn(new, 1, 8, dtype=torch.bfloat16), _i32([n]), _i32([0, new])
+    for window, frame, sinks, lo in ((2, 1_500_000_000, 0, 0), (3, 1_000_000_000, 5, 0), (2 ** 31 - 1, 2 ** 31 - 1, 0, 0),
+                                     (1, 1_500_000_000, 0, 1_500_000_000), (1, 1_500_000_000, 1000, 1_500_000_000)):
+        out, lse = wv.kv_window_attention(q, kc, vc, pages, lengths, window, sinks, frame, cu, return_lse=True)
+        seen = n - lo + (min(sinks, lo) if lo else 0)
+        want = torch.full((new, 1, 8), (ones * size if lo == 0 else sinks) / seen, dtype=torch.float64, device="cuda")
+        # counts of up to 1.6e9 ones, summed in 32 bits: 2^-23 for each chained sum of a part's blocks and of the parts (a part
+        # of 1 / 152 or less has under 2^24 keys, whose count is exact)
+        ref.assert_rounded(out, want, want * 152 * 2.0 ** -23)
+        assert bool(((lse.double() - math.log(seen)).abs() < 1e-4).all())

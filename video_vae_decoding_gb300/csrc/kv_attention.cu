@@ -159,7 +159,7 @@ __device__ __forceinline__ Tiles tiles_of(const AttnArgs& a, const Seq& s) {
     // the tokens of 16 rows reach over 15 / group + 1 steps at most, each of which can begin a frame
     const uint32_t steps = s.n > 1 ? min((uint32_t)(s.n - 1), (uint32_t)((kRows - 1) / a.group + 1)) : 0;
     const uint32_t reach = steps == 0 ? 0 : a.frame >= steps ? a.frame : ((steps - 1) / a.frame + 1) * a.frame;
-    const uint32_t most = (a.span + reach) / kKeys + 2 + ((uint32_t)a.sinks + kKeys - 1) / kKeys;
+    const uint32_t most = (min(a.span, (uint32_t)s.len) + reach) / kKeys + 2 + ((uint32_t)a.sinks + kKeys - 1) / kKeys;
     t.key_tiles = (int)min((uint32_t)t.key_tiles, most);
   }
   t.runs = ((long long)s.n * a.group + kRows - 1) / kRows * a.c.heads;

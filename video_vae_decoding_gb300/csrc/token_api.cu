@@ -520,7 +520,8 @@ wan_status wan_kv_window_attention(const wan_kv_cache* cache, const wan_kv_batch
       return fail(WAN_ERR_INVALID_ARG, "a window of %d frames of %d keys, and %d first keys", window, frame, sinks);
     a.mask = kMaskWindow;
     a.frame = (uint32_t)frame;
-    a.span = (uint32_t)std::min<int64_t>((int64_t)window * frame, 0x7fffffff);  // (more than any sequence holds)
+    // (a frame's end is below 2^32, and 2^31 - 1 keys behind it may be short of the window)
+    a.span = (uint32_t)std::min<int64_t>((int64_t)window * frame, 0xffffffffLL);
     a.sinks = sinks;
     return attend(a, q, q_token, q_head, scale, out, out_token, out_head, lse, workspace, workspace_bytes, stream);
   })
