@@ -534,15 +534,16 @@ int64_t wan_kv_attention_workspace(const wan_kv_cache* cache, const wan_kv_batch
  * it, or -1 for none.  One that does not come before its child counts as none
  * and leaves a code in the batch's status word.  A row's mask is found by a walk
  * up the tree, so a call takes time by its depth; what is a chain throughout is
- * better a range.  At most 1024 new tokens a sequence.
+ * better a range.  At most 1024 new tokens a sequence.  There is no window: a
+ * stream that attends by windows compacts its cache to the window first.
  *
  * A sequence with more new tokens than keys (or than a tree may have) gets zeros
  * and leaves a code in the status word.  Pages that hold no key that any token sees (between the first
  * keys and the windows) are not read, and their numbers in the table may be
  * anything.  Precision, kernels, errors and the other arguments are those of
- * wan_kv_attention (the kernel for many rows is taken from 20 rows a sequence on
- * average, in calls of 1.3e6 products or more, counted by the keys that a window
- * leaves); workspace: wan_kv_masked_attention_workspace bytes. */
+ * wan_kv_attention (the kernel for many rows, whose weights are rounded to 16 bits,
+ * is taken from 20 rows a sequence on average, where ranges take it from 64, in calls
+ * of 1.3e6 products or more, counted by the keys that a window leaves); workspace: wan_kv_masked_attention_workspace bytes. */
 wan_status wan_kv_window_attention(const wan_kv_cache* cache, const wan_kv_batch* batch, const void* q, int32_t q_heads,
                                    int64_t q_token, int64_t q_head, int32_t window, int32_t sinks, int32_t frame,
                                    float scale, void* out, int64_t out_token, int64_t out_head, float* lse,

@@ -29,9 +29,9 @@
 //
 // Bound: the tensor cores, 4 D operations per row and key; K and V come through
 // a ring each and serve both halves, so a block of 128 keys asks 64 KB (D = 128) for
-// 33.6 MFLOP.  880 tokens of 16 heads of 128 against 27,280 keys take 171 us, 1.15
-// PFLOP/s (60% of a large library product's); with heads of 64 135 us, where the
-// softmax bounds, and with 8 heads of 256 248 us: 128 KB a block for 16.8 MFLOP is 8
+// 33.6 MFLOP.  880 tokens of 16 heads of 128 against 27,280 keys take 174 us, 1.13
+// PFLOP/s (59% of a large library product's); with heads of 64 135 us, where the
+// softmax bounds, and with 8 heads of 256 246 us: 128 KB a block for 16.8 MFLOP is 8
 // TB/s from the L2.
 // V is taken as it lies in the cache, [key][channel]: the MMA's second operand
 // with its N dimension contiguous, so nothing is transposed on the way.
@@ -48,9 +48,9 @@
 // The second form (X) is for rows that see by their place (a window with first keys,
 // a tree of drafts): blocks are made of the pages that some row of the tile sees.
 // A window of 9 latent frames and the first one, 880 tokens of 16 heads of 128, takes
-// 87 us (0.73 PFLOP/s: runs of 30 blocks, of which start and end are a quarter), 64
-// drafts of 24 sequences of up to 9000 keys, 32 heads on 8, 134 us, ragged windows of
-// 1000 keys at heads of 64 85 us.
+// 86 us (0.73 PFLOP/s: runs of 30 blocks, of which start and end are a quarter), 64
+// drafts of 24 sequences of up to 9000 keys, 32 heads on 8, 133 us, ragged windows of
+// 1000 keys at heads of 64 84 us.
 #include <type_traits>
 
 #include "kv_common.cuh"
@@ -269,7 +269,7 @@ struct RowTile {
 // With X (rows see by their place) its rows see the first keys and a window.  What holds them is taken together: units (pages,
 // or the blocks of a longer page) 0 .. firsts - 1, and `skip` units further on the rest of `units`; a block takes as many
 // units as it has pages.  (With blocks of the window alone and of the first keys alone, ragged prompts with windows of 1000 keys
-// and pages of 32 took 103 us instead of 92.)
+// and pages of 32 took 11 us more, of 103.)
 struct SightTile : RowTile {
   int firsts, skip, units, pad;
 };
@@ -282,8 +282,9 @@ __host__ __device__ inline long long row_tiles(const AttnArgs& a) {
 }
 
 // What a row tile with a head takes of the line: kRunUnits (start, end and the blocks at a mask's edge), and for each
-// block kPairUnits, or kSingleUnits in a tile of at most 128 rows.  They stand for what these cost: two chunks of 1300
-// causal tokens of 48 heads take 184 us with 30 for a run, 173 with 45, 162 with 60, 164 with 80.  (A smaller tile does
+// block kPairUnits, or kSingleUnits in a tile of at most 128 rows.  They stand for what these cost.  us with 30, 45, 60, 80 for
+// a run: two chunks of 1300 causal tokens of 48 heads 123, 120, 127, 124; 64 drafts of 24 sequences 146, 140, 133, 136; ragged
+// causal chunks at heads of 64 93, 92, 91, 94; 880 tokens against 27,280 keys 173, 170, 175, 182.  (A smaller tile does
 // half the arithmetic, but asks for K and V as fast as a larger one would at twice the speed.)
 constexpr int kPairUnits = 5, kSingleUnits = 4, kRunUnits = 60;
 constexpr int kSightSingleUnits = 3;  // with X (trees of up to 47 drafts 40 us with 4, 38 with 3)
@@ -425,7 +426,7 @@ __device__ __forceinline__ Columns columns_of(const ChunkGeo& geo, int page_size
 // slot, half 0 does this for both, ahead of its arrival and so of either product: no
 // product reads a value while it changes.  Not inline but for windows and trees at
 // heads of 64: the softmax's loop needs the registers (two chunks of 1300 causal
-// tokens of 48 heads 159 us, 162 inline; ragged windows at heads of 64 90 and 85).
+// tokens of 48 heads 127 us, 134 inline; ragged windows at heads of 64 89 and 85).
 template <int DP, bool X>
 constexpr bool kCleanInline = X && DP == 64;
 template <typename T>
@@ -491,7 +492,7 @@ __device__ __noinline__ bool clean_values_apart(uint8_t* ring, uint64_t* full, i
 // thread has written as output, or as a part in `o`.  Called where the run is over: the softmax's loop needs the registers.
 // What a row sees of 64 columns is found once for all channels, and a lane looks whether one of 32 keys has such a value (a
 // chain of 1024 drafts with an infinity in the first and in the last takes 218 us, as without; with a walk up the tree for each
-// key and 16 channels it took 5800.  24 trees of 64 drafts with NaN behind the sequences' ends 137, where those were walked for
+// key and 16 channels it took 5800.  24 trees of 64 drafts with NaN behind the sequences' ends 136, where those were walked for
 // too 3100).  With ranges the softmax's threads do it, key by key, as they put out 16 channels: a range is soon looked up,
 // and that loop loses 10 to 27% by how it is then compiled if they do not.
 template <typename T, int DP>
@@ -735,8 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
 
   // The first V of the next run, and q, come while this one ends: q in its room from the last Q K on (by warp 1), where the
-  // halves do not need that for their sums and its rows can be copied as they are.  880 tokens against 27,280 keys take 176 us
-  // with q ahead, 190 without; with X a window of 9 latent frames 102 and 89; at heads of 64 ragged causal chunks 104 and 91
+  // halves do not need that for their sums and its rows can be copied as they are.  880 tokens against 27,280 keys take 175 us
+  // with q ahead, 202 without; with X a window of 9 latent frames 92 and 87; at heads of 64 ragged causal chunks 107 and 92
   // (too little time to fill).
   constexpr bool kValuesAhead = DP > 64, kAheadOfRun = DP > 64 && !X;
   const bool q_plain = a.scale_log2 > 0.f && ((uintptr_t)a.q & 15) == 0 && (a.q_t & 7) == 0 && (a.q_h & 7) == 0;
@@ -1087,7 +1088,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (tails) behind = geo.parts - 1 - at % geo.parts;
       // A block's values are cleaned behind its weights, when S has left the registers, and ahead of the barrier that the products
-      // wait for; with ranges and heads of 64 ahead of the weights (880 tokens against 27,280 keys 136 us, 140 behind them).
+      // wait for; with ranges and heads of 64 ahead of the weights (880 tokens against 27,280 keys 135 us, 139 behind them).
       constexpr bool kCleanFirst = !X && DP == 64;
       uint32_t s_there = 0;  // S of block i is known to be there
       for (int i = 0; i < mine; ++i) {

@@ -543,7 +543,12 @@ def kv_window_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     `window` keys up to its own; larger frames: its own frame's later keys too).
 
     Pages that hold no key that any token sees are not read: their numbers in
-    `pages` may be anything, so the cache need not grow with the stream."""
+    `pages` may be anything, so the cache need not grow with the stream.
+
+    Precision and page sizes as kv_attention's, but the tensor-core kernel, whose
+    weights are rounded to 16 bits, takes calls from 20 rows a sequence on (64
+    there): between the two a window's result is off by 1.2 to 1.4 times its own
+    rounding where the same ranges in kv_attention give that alone."""
     short = _short or _short_way()
     if stream is None:
         got = short.window(q, k_cache, v_cache, pages, lengths, cu_tokens, window, sinks, frame, scale, out, return_lse, status)
@@ -564,7 +569,9 @@ def kv_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     drafts (0: the first), which comes before it, or -1.  Others count as -1 and
     leave a code in `status`.  Time goes with the tree's depth; a chain is better
     a range of kv_attention.  At most 1024 drafts a sequence (others get zeros and
-    leave a code)."""
+    leave a code).  There is no window: drafts see every key ahead of them, so a
+    stream that attends by windows compacts its cache to the window first.
+    Precision as kv_window_attention's."""
     short = _short or _short_way()
     if stream is None:
         got = short.tree(q, k_cache, v_cache, pages, lengths, cu_tokens, parents, scale, out, return_lse, status)
