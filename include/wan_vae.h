@@ -592,11 +592,11 @@ wan_status wan_kv_fork(const wan_kv_cache* cache, int32_t* pages, int64_t page_s
  * they had) and a code is left in the batch's status word; so is a sequence whose
  * f, range or result the table cannot hold (none of its keys move, and its result
  * is f, or 0 where f is none).
- * The rows that keys move to must be the sequence's alone: whole pages that it
- * shares with others after wan_kv_fork (share 1) stand ahead of f + the first key
- * that moves, or the others' keys are overwritten, whether they are in the call
- * or not, and nothing tells of it (wan_kv_check_compact does, of host tables).
- * A sequence that is to roll on inside them is forked with share 0.  lengths: device int32, not in
+ * The rows that keys move to must be the sequence's alone: pages that it shares
+ * with others after wan_kv_fork (share 1) have to end ahead of the first place that
+ * a key moves to, or the others' keys are overwritten, whether they are in the call
+ * or not, and nothing tells of it (wan_kv_check_compact does, of host tables).  A
+ * sequence that is to roll on inside them is forked with share 0.  lengths: device int32, not in
  * the memory that the call reads.  k and v may be one tensor, whose rows then move
  * once; otherwise they have no memory in common (rows may interleave).  heads: up
  * to 1000.  Errors: as above. */

@@ -80,7 +80,8 @@ def test_check_of_compactions_that_cannot_be(lib):  # noqa: F811
         with pytest.raises(wv.WanError, match=names):
             _check(pages, lengths, first, keeps)
     table, one = _i([[0, 1]]), _i([1])
-    for kw in (dict(first=one), dict(keep=one), dict(first=one, keep=one), dict(cu_tokens=_i([0, 1]), first=_i([1, 2]), keep=one),
+    for kw in (dict(first=one), dict(keep=one), dict(first=one, keep=one), dict(cu_tokens=_i([0, 1]), first=one, keep=one, append=True),
+               dict(cu_tokens=_i([0, 1]), first=one, keep=one, tokens=1), dict(cu_tokens=_i([0, 1]), first=_i([1, 2]), keep=one),
                dict(cu_tokens=_i([0, 1]), first=one, keep=one.long()), dict(cu_tokens=_i([0, 1, 1]), first=one, keep=one),
                dict(cu_tokens=_i([0, 1]), first=one, keep=_i([1, 2, 3])[::2])):
         with pytest.raises(ValueError):

@@ -636,11 +636,13 @@ def kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor
     are the caller's again.
 
     Keys must move to rows that are the sequence's alone.  Pages that it shares with
-    other sequences after kv_fork (share=True) have to stand ahead of the first
-    place that a key moves to: else the others' keys are overwritten, whether they
+    other sequences after kv_fork (share=True) have to end ahead of the first place
+    that a key moves to: else the others' keys are overwritten, whether they
     are in the call or not, and nothing tells of it (kv_check does, of host tables).
-    Fork a sequence that is to roll on inside them with share=False.  The caches may be one tensor (its rows move once);
-    otherwise no row of one has memory in common with the other."""
+    Fork a sequence that is to roll on inside them with share=False.
+
+    The caches may be one tensor (its rows move once); otherwise no row of one has
+    memory in common with the other."""
     short = _short or _short_way()
     if stream is None:
         got = short.compact(k_cache, v_cache, pages, first, keep, cu_keep, lengths, status)
@@ -682,6 +684,8 @@ def kv_check(pages: torch.Tensor, lengths: torch.Tensor, page_size: int, n_pages
     cpu = torch.device("cpu")
     if (first is None) != (keep is None):
         raise ValueError("first and keep go together")
+    if keep is not None and (append or tokens is not None):
+        raise ValueError("keep's tables are not those of an append: neither append nor tokens goes with it")
     if keep is not None:
         _on(keep, cpu, "keep", _INT32, 1)
         _on(lengths, cpu, "lengths", _INT32, 1)
